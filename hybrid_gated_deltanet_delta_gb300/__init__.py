@@ -12,9 +12,12 @@ Entry points (same names as the C ABI):
   gdn_commit_accepted_f16, gdn_commit_index, gdn_conv_commit,
   gdn_replay_accepted,
   gdn_prefill_chunked, gdn_prefill_workspace_bytes, gdn_prefill_chunked_noalloc
+  the 4-bit key/value cache of the full-attention layers: gdn_kv4_append,
+  gdn_kv4_read, gdn_kv4_attention, gdn_kv4_commit, and its page pool:
+  gdn_kv4_release, gdn_kv4_fork, gdn_kv4_reserve
 and, for serving loops that issue the same call every step, bound calls
 (bind_verify_chain, bind_verify_tree, bind_commit_accepted,
-bind_replay_accepted, bind_prefill_chunked): the arguments are marshalled once
+bind_replay_accepted, bind_prefill_chunked, bind_kv4_*): the arguments are marshalled once
 and each call is one ctypes call.
 """
 from __future__ import annotations
@@ -36,10 +39,15 @@ GDN_ERR_SLOT_RANGE = -7
 GDN_ERR_WORKSPACE = -8
 GDN_ERR_SCRATCH_LIMIT = -9
 GDN_ERR_TIMEOUT = -10
+GDN_ERR_PAGE_RANGE = -11
+GDN_ERR_POOL_EMPTY = -12
+GDN_ERR_ROW_RANGE = -13
+GDN_ERR_NONFINITE = -14
 PREFILL_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 GDN_F32 = 0
 GDN_BF16 = 1
+GDN_F16 = 2
 
 _lib = None
 
@@ -62,6 +70,28 @@ class VerifyArgs(ctypes.Structure):
         ("Hv", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
         ("in_dtype", ctypes.c_int32), ("tile_cols", ctypes.c_int32),
         ("row_warps", ctypes.c_int32), ("max_depth", ctypes.c_int32),
+    ]
+
+
+class Kv4Cache(ctypes.Structure):
+    """Mirror of gdn_kv4_cache."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+    ]
+
+
+class Kv4Pool(ctypes.Structure):
+    """Mirror of gdn_kv4_pool."""
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+        ("status", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
     ]
 
 
@@ -110,6 +140,26 @@ def load(path: str | None = None):
     lib.gdn_prefill_chunked_noalloc.argtypes = [P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32,
                                                 P, P, P, P]
     lib.gdn_prefill_chunked_noalloc.restype = ctypes.c_int
+    C, L = ctypes.POINTER(Kv4Cache), ctypes.POINTER(Kv4Pool)
+    lib.gdn_kv4_append.argtypes = [C, P, P, i32, i64, i64, i64, i64, i32, P]
+    lib.gdn_kv4_append.restype = ctypes.c_int
+    lib.gdn_kv4_read.argtypes = [C, P, P, i32, i32, P]
+    lib.gdn_kv4_read.restype = ctypes.c_int
+    lib.gdn_kv4_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.gdn_kv4_attention_workspace_bytes.restype = sz
+    lib.gdn_kv4_attention.argtypes = [C, P, i32, i64, i64, i32, i32, ctypes.c_float, P, P, P, P,
+                                      sz, P]
+    lib.gdn_kv4_attention.restype = ctypes.c_int
+    lib.gdn_kv4_commit.argtypes = [C, i64, i32, i32, P, P, P, P]
+    lib.gdn_kv4_commit.restype = ctypes.c_int
+    lib.gdn_kv4_release.argtypes = [L, P, P, i32, P]
+    lib.gdn_kv4_release.restype = ctypes.c_int
+    lib.gdn_kv4_fork.argtypes = [L, P, P, i32, P]
+    lib.gdn_kv4_fork.restype = ctypes.c_int
+    lib.gdn_kv4_reserve_workspace_bytes.argtypes = [i32]
+    lib.gdn_kv4_reserve_workspace_bytes.restype = sz
+    lib.gdn_kv4_reserve.argtypes = [L, P, i64, i64, i32, i32, i32, P, P, i32, P, sz, P]
+    lib.gdn_kv4_reserve.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []
@@ -458,3 +508,249 @@ def bind_prefill_chunked(q, k, v, alpha, beta, state, o, workspace=None, *, chun
             _stream(stream))
     return BoundCall(load().gdn_prefill_chunked, "gdn_prefill_chunked", args,
                      (q, k, v, alpha, beta, state, o, workspace, status))
+
+
+# ------------------------------------------- the 4-bit key/value cache
+# Every function builds one BoundCall (checks and marshalling) and calls it; the
+# bind_kv4_* functions return it.
+def _dtype16(t):
+    import torch
+
+    if t.dtype == torch.float16:
+        return GDN_F16
+    return _dtype_code(t)
+
+
+def _i32(t, shape, what):
+    import torch
+
+    _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and
+                        tuple(t.shape) == tuple(shape)),
+          f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _kv4_pages(pages):
+    """(n_layers, n_pages, Hkv, page_tokens, D, page_stride, layer_stride) of a
+    pages tensor [n_pages,Hkv,page_tokens/32,36*D] (or with a layer dimension in
+    front), uint8; the last three dimensions contiguous."""
+    import torch
+
+    _need(pages.dtype == torch.uint8 and pages.dim() in (4, 5),
+          "pages must be uint8 [n_pages,Hkv,page_tokens/32,36*D], or [n_layers,...]")
+    n_pages, Hkv, recs, rec = pages.shape[-4:]
+    _need(rec % 36 == 0 and pages.stride()[-3:] == (recs * rec, rec, 1),
+          "a page must be contiguous records of 36*D bytes")
+    layers = pages.shape[0] if pages.dim() == 5 else 1
+    return (layers, n_pages, Hkv, recs * 32, rec // 36, pages.stride(-4),
+            pages.stride(0) if pages.dim() == 5 else 0)
+
+
+def _kv4_table(table):
+    import torch
+
+    _need(table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1,
+          "table must be int32 [rows,max_pages] with contiguous rows")
+
+
+def _kv4_cache(pages, table, kv_len, k_scale, v_scale, status):
+    import torch
+
+    _, n_pages, Hkv, page_tokens, D, page_stride, _ = _kv4_pages(pages)
+    B = kv_len.numel()
+    _kv4_table(table)
+    _need(table.shape[0] == B, "table and kv_len must have one row per sequence")
+    _i32(kv_len, (B,), "kv_len")
+    for t in (k_scale, v_scale):
+        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() == Hkv),
+              "k_scale and v_scale must be contiguous float32 [Hkv]")
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    return Kv4Cache(pages=ptr(pages), table=ptr(table), kv_len=ptr(kv_len), k_scale=ptr(k_scale),
+                    v_scale=ptr(v_scale), status=ptr(status), page_stride=page_stride,
+                    table_stride=table.stride(0), n_pages=n_pages, page_tokens=page_tokens,
+                    max_pages=table.shape[1], B=B, Hkv=Hkv, D=D)
+
+
+def _rows(t, c, what):
+    """Batch and node strides of [B,N,H,D] with contiguous heads and channels."""
+    _need(t.dim() == 4 and t.shape[0] == c.B and t.shape[3] == c.D, f"{what} must be [B,N,H,D]")
+    _need(t.stride(3) == 1 and (t.shape[2] == 1 or t.stride(2) == c.D),
+          f"{what}'s heads and channels must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def bind_kv4_append(k, v, pages, table, kv_len, *, k_scale=None, v_scale=None, status=None,
+                    stream=None):
+    """gdn_kv4_append bound to these buffers."""
+    _need(pages.dim() == 4, "append takes one layer's pages")
+    c = _kv4_cache(pages, table, kv_len, k_scale, v_scale, status)
+    ks, vs = _rows(k, c, "k"), _rows(v, c, "v")
+    _need(k.shape == v.shape and k.shape[2] == c.Hkv and k.dtype == v.dtype,
+          "k and v must share a shape [B,N,Hkv,D] and a dtype")
+    return BoundCall(load().gdn_kv4_append, "gdn_kv4_append",
+                     (ctypes.byref(c), _ptr(k), _ptr(v), _dtype16(k), *ks, *vs, k.shape[1],
+                      _stream(stream)),
+                     (c, k, v, pages, table, kv_len, k_scale, v_scale, status))
+
+
+def gdn_kv4_append(k, v, pages, table, kv_len, **kw):
+    """Quantise k, v [B,N,Hkv,D] (float32, bfloat16 or float16; any batch and
+    node strides) into positions kv_len[b]-N .. kv_len[b]-1 of the 4-bit cache.
+
+    pages uint8 [n_pages,Hkv,page_tokens/32,36*D]; table int32 [B,max_pages];
+    kv_len int32 [B]; k_scale, v_scale optional float32 [Hkv]; status an optional
+    int32 device word (see include/gdn.h)."""
+    bind_kv4_append(k, v, pages, table, kv_len, **kw)()
+
+
+def bind_kv4_read(pages, table, kv_len, k_out, v_out, *, k_scale=None, v_scale=None, status=None,
+                  stream=None):
+    """gdn_kv4_read bound to these buffers."""
+    _need(pages.dim() == 4, "read takes one layer's pages")
+    c = _kv4_cache(pages, table, kv_len, k_scale, v_scale, status)
+    _rows(k_out, c, "k_out")
+    _need(k_out.shape == v_out.shape and k_out.dtype == v_out.dtype and
+          k_out.shape[2] == c.Hkv and k_out.is_contiguous() and v_out.is_contiguous(),
+          "k_out and v_out must be contiguous [B,N,Hkv,D] of one dtype")
+    return BoundCall(load().gdn_kv4_read, "gdn_kv4_read",
+                     (ctypes.byref(c), _ptr(k_out), _ptr(v_out), _dtype16(k_out), k_out.shape[1],
+                      _stream(stream)),
+                     (c, pages, table, kv_len, k_out, v_out, k_scale, v_scale, status))
+
+
+def gdn_kv4_read(pages, table, kv_len, k_out, v_out, **kw):
+    """The stored values of positions kv_len[b]-N .. kv_len[b]-1 into k_out and
+    v_out [B,N,Hkv,D]; keyword arguments as for gdn_kv4_append."""
+    bind_kv4_read(pages, table, kv_len, k_out, v_out, **kw)()
+
+
+def gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D) -> int:
+    return int(load().gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D))
+
+
+def bind_kv4_attention(q, pages, table, kv_len, o, workspace, *, scale, parent=None, lse=None,
+                       k_scale=None, v_scale=None, status=None, stream=None):
+    """gdn_kv4_attention bound to these buffers."""
+    import torch
+
+    _need(pages.dim() == 4, "attention takes one layer's pages")
+    c = _kv4_cache(pages, table, kv_len, k_scale, v_scale, status)
+    qs = _rows(q, c, "q")
+    B, N, Hq, _ = q.shape
+    _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(),
+          "o must be a contiguous tensor of q's shape and dtype")
+    _i32(parent, (B, N), "parent")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and
+                          tuple(lse.shape) == (B, N, Hq)), "lse must be float32 [B,N,Hq]")
+    return BoundCall(load().gdn_kv4_attention, "gdn_kv4_attention",
+                     (ctypes.byref(c), _ptr(q), _dtype16(q), *qs, N, Hq, scale, _ptr(parent),
+                      _ptr(o), _ptr(lse), _ptr(workspace),
+                      workspace.numel() * workspace.element_size(), _stream(stream)),
+                     (c, q, pages, table, kv_len, o, workspace, parent, lse, k_scale, v_scale,
+                      status))
+
+
+def gdn_kv4_attention(q, pages, table, kv_len, o, workspace, **kw):
+    """o[b,n,h] = softmax(scale * q[b,n,h] . k) v over the cached positions that
+    node n sees: all before the block, and within it the nodes up to n, or n's
+    ancestors and itself where parent [B,N] is given (N <= 64).
+
+    q, o [B,N,Hq,D] bfloat16 or float16 (q with any batch and node strides);
+    workspace a uint8 tensor of gdn_kv4_attention_workspace_bytes(...) bytes;
+    scale a float; lse an optional float32 [B,N,Hq]; the others as for
+    gdn_kv4_append."""
+    bind_kv4_attention(q, pages, table, kv_len, o, workspace, **kw)()
+
+
+def bind_kv4_commit(pages, table, kv_len, accept_idx, len_out, *, N, parent=None, status=None,
+                    stream=None):
+    """gdn_kv4_commit bound to these buffers."""
+    c = _kv4_cache(pages, table, kv_len, None, None, status)
+    _i32(accept_idx, (c.B,), "accept_idx")
+    _i32(len_out, (c.B,), "len_out")
+    _i32(parent, (c.B, N), "parent")
+    layers, layer_stride = (pages.shape[0], pages.stride(0)) if pages.dim() == 5 else (1, 0)
+    return BoundCall(load().gdn_kv4_commit, "gdn_kv4_commit",
+                     (ctypes.byref(c), layer_stride, layers, N, _ptr(parent), _ptr(accept_idx),
+                      _ptr(len_out), _stream(stream)),
+                     (c, pages, table, kv_len, accept_idx, len_out, parent, status))
+
+
+def gdn_kv4_commit(pages, table, kv_len, accept_idx, len_out, **kw):
+    """Move the accepted path of every block of N nodes to the block's start, in
+    every layer of pages [n_layers,n_pages,Hkv,page_tokens/32,36*D], and write
+    the committed lengths to len_out [B] (not kv_len itself).  accept_idx [B];
+    parent [B,N] for trees, None for chains (whose path is in place already)."""
+    bind_kv4_commit(pages, table, kv_len, accept_idx, len_out, **kw)()
+
+
+def _kv4_pool(table, kv_len, ref, page_tokens, status):
+    _kv4_table(table)
+    n_rows = table.shape[0]
+    _i32(kv_len, (n_rows,), "kv_len")
+    _i32(ref, (ref.numel(),), "ref")
+    return Kv4Pool(table=table.data_ptr(), kv_len=kv_len.data_ptr(), ref=ref.data_ptr(),
+                   status=None if status is None else status.data_ptr(),
+                   table_stride=table.stride(0), n_rows=n_rows, max_pages=table.shape[1],
+                   n_pages=ref.numel(), page_tokens=page_tokens)
+
+
+def bind_kv4_release(table, kv_len, ref, rows, keep_len, *, page_tokens, status=None,
+                     stream=None):
+    """gdn_kv4_release bound to these buffers."""
+    p = _kv4_pool(table, kv_len, ref, page_tokens, status)
+    _i32(rows, (rows.numel(),), "rows")
+    _i32(keep_len, (rows.numel(),), "keep_len")
+    return BoundCall(load().gdn_kv4_release, "gdn_kv4_release",
+                     (ctypes.byref(p), _ptr(rows), _ptr(keep_len), rows.numel(),
+                      _stream(stream)), (p, table, kv_len, ref, rows, keep_len, status))
+
+
+def gdn_kv4_release(table, kv_len, ref, rows, keep_len, **kw):
+    """Truncate rows[i] of the page table to keep_len[i] tokens (0 frees the
+    row).  table int32 [n_rows,max_pages], kv_len int32 [n_rows], ref int32
+    [n_pages] (holders of each page; 0 = free); page_tokens a keyword."""
+    bind_kv4_release(table, kv_len, ref, rows, keep_len, **kw)()
+
+
+def bind_kv4_fork(table, kv_len, ref, src, dst, *, page_tokens, status=None, stream=None):
+    """gdn_kv4_fork bound to these buffers."""
+    p = _kv4_pool(table, kv_len, ref, page_tokens, status)
+    _i32(src, (src.numel(),), "src")
+    _i32(dst, (src.numel(),), "dst")
+    return BoundCall(load().gdn_kv4_fork, "gdn_kv4_fork",
+                     (ctypes.byref(p), _ptr(src), _ptr(dst), src.numel(), _stream(stream)),
+                     (p, table, kv_len, ref, src, dst, status))
+
+
+def gdn_kv4_fork(table, kv_len, ref, src, dst, **kw):
+    """Branch row src[i] onto the empty row dst[i]: both hold the same pages."""
+    bind_kv4_fork(table, kv_len, ref, src, dst, **kw)()
+
+
+def gdn_kv4_reserve_workspace_bytes(F) -> int:
+    return int(load().gdn_kv4_reserve_workspace_bytes(F))
+
+
+def bind_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, *, status=None,
+                     stream=None):
+    """gdn_kv4_reserve bound to these buffers."""
+    layers, n_pages, Hkv, page_tokens, D, page_stride, layer_stride = _kv4_pages(pages)
+    p = _kv4_pool(table, kv_len, ref, page_tokens, status)
+    _need(p.n_pages == n_pages, "ref must have one entry per page")
+    _i32(rows, (rows.numel(),), "rows")
+    _i32(new_len, (rows.numel(),), "new_len")
+    return BoundCall(load().gdn_kv4_reserve, "gdn_kv4_reserve",
+                     (ctypes.byref(p), _ptr(pages), page_stride, layer_stride, layers, Hkv, D,
+                      _ptr(rows), _ptr(new_len), rows.numel(), _ptr(workspace),
+                      workspace.numel() * workspace.element_size(), _stream(stream)),
+                     (p, pages, table, kv_len, ref, rows, new_len, workspace, status))
+
+
+def gdn_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, **kw):
+    """Grow rows[i] to new_len[i] tokens with the lowest-numbered free pages; a
+    partly filled last page that has other holders is copied first, in every
+    layer of pages.  workspace: gdn_kv4_reserve_workspace_bytes(len(rows))."""
+    bind_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, **kw)()

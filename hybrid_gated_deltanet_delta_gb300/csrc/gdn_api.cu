@@ -168,6 +168,48 @@ int prefill_checks(const void* q, const void* k, const void* v, int32_t in_dtype
   return GDN_OK;
 }
 
+bool kv4_head_size(int32_t D) { return D == 64 || D == 128 || D == 256; }
+
+int kv4_checks(const gdn_kv4_cache* c, int32_t N) {
+  if (c == nullptr) return GDN_ERR_INVALID_ARG;
+  if (c->B < 0 || N < 1 || c->Hkv < 1 || c->max_pages < 1 || c->n_pages < 1 || c->page_tokens < 1)
+    return GDN_ERR_INVALID_ARG;
+  if (!kv4_head_size(c->D) || c->page_tokens % 32 != 0) return GDN_ERR_UNSUPPORTED;
+  if (c->B > 65535 || c->Hkv > 65535 || N > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * c->page_tokens > 0x7fffffffLL - (1 << 24))
+    return GDN_ERR_UNSUPPORTED;
+  if (c->table_stride < c->max_pages) return GDN_ERR_INVALID_ARG;
+  if (c->page_stride < (int64_t)c->Hkv * (c->page_tokens / 32) * 36 * c->D)
+    return GDN_ERR_INVALID_ARG;
+  if (c->page_stride % 16 != 0) return GDN_ERR_MISALIGNED;
+  if (c->B == 0) return GDN_OK;
+  if (c->pages == nullptr || c->table == nullptr || c->kv_len == nullptr)
+    return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(c->pages)) return GDN_ERR_MISALIGNED;
+  if (!ok_ptr4(c->table) || !ok_ptr4(c->kv_len) || !ok_ptr4(c->k_scale) ||
+      !ok_ptr4(c->v_scale) || !ok_ptr4(c->status))
+    return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
+int kv4_pool_checks(const gdn_kv4_pool* p, const int32_t* a, const int32_t* b, int32_t F) {
+  if (p == nullptr || F < 0) return GDN_ERR_INVALID_ARG;
+  if (p->n_rows < 1 || p->max_pages < 1 || p->n_pages < 1 || p->page_tokens < 1)
+    return GDN_ERR_INVALID_ARG;
+  if (p->page_tokens % 32 != 0 || F > 65535) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages * p->page_tokens > 0x7fffffffLL - (1 << 24))
+    return GDN_ERR_UNSUPPORTED;
+  if (p->table_stride < p->max_pages) return GDN_ERR_INVALID_ARG;
+  if (F == 0) return GDN_OK;
+  if (a == nullptr || b == nullptr || p->table == nullptr || p->kv_len == nullptr ||
+      p->ref == nullptr)
+    return GDN_ERR_INVALID_ARG;
+  if (!ok_ptr4(a) || !ok_ptr4(b) || !ok_ptr4(p->table) || !ok_ptr4(p->kv_len) ||
+      !ok_ptr4(p->ref) || !ok_ptr4(p->status))
+    return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -308,6 +350,130 @@ int gdn_prefill_chunked_noalloc(const void* q, const void* k, const void* v, int
                                      o, status, static_cast<cudaStream_t>(stream));
 }
 
+int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t dtype,
+                   int64_t k_stride_b, int64_t k_stride_n, int64_t v_stride_b,
+                   int64_t v_stride_n, int32_t N, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (dtype != GDN_F32 && dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
+  if (c->B == 0) return GDN_OK;
+  if (k == nullptr || v == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(k) || !gdn::aligned16(v)) return GDN_ERR_MISALIGNED;
+  const int64_t unit = dtype == GDN_F32 ? 4 : 8;
+  if (k_stride_b % unit != 0 || k_stride_n % unit != 0 || v_stride_b % unit != 0 ||
+      v_stride_n % unit != 0)
+    return GDN_ERR_MISALIGNED;
+  return gdn::launch_kv4_append(*c, k, v, dtype, k_stride_b, k_stride_n, v_stride_b, v_stride_n,
+                                N, static_cast<cudaStream_t>(stream));
+}
+
+int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype, int32_t N,
+                 void* stream) {
+  GDN_RANGE();
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (dtype != GDN_F32 && dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
+  if (c->B == 0) return GDN_OK;
+  if (k_out == nullptr || v_out == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(k_out) || !gdn::aligned16(v_out)) return GDN_ERR_MISALIGNED;
+  return gdn::launch_kv4_read(*c, k_out, v_out, dtype, N, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_kv4_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                                         int32_t D) {
+  if (B < 1 || N < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || !kv4_head_size(D)) return 0;
+  return gdn::kv4_attention_workspace_bytes(B, N, Hq, Hkv, D);
+}
+
+int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int64_t q_stride_b,
+                      int64_t q_stride_n, int32_t N, int32_t Hq, float scale,
+                      const int32_t* parent, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (Hq < 1 || Hq % c->Hkv != 0) return GDN_ERR_INVALID_ARG;
+  if (dtype == GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
+  if (parent != nullptr && N > 64) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)N * Hq > (1 << 30)) return GDN_ERR_UNSUPPORTED;
+  if (c->B == 0) return GDN_OK;
+  if (q == nullptr || o == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(q) || !gdn::aligned16(o) || !gdn::aligned16(workspace))
+    return GDN_ERR_MISALIGNED;
+  if (q_stride_b % 8 != 0 || q_stride_n % 8 != 0) return GDN_ERR_MISALIGNED;
+  if (!ok_ptr4(parent) || !ok_ptr4(lse)) return GDN_ERR_MISALIGNED;
+  if (workspace == nullptr ||
+      workspace_bytes < gdn_kv4_attention_workspace_bytes(c->B, N, Hq, c->Hkv, c->D))
+    return GDN_ERR_WORKSPACE;
+  return gdn::launch_kv4_attention(*c, q, dtype, q_stride_b, q_stride_n, N, Hq, scale, parent, o,
+                                   lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int gdn_kv4_commit(const gdn_kv4_cache* c, int64_t layer_stride, int32_t n_layers, int32_t N,
+                   const int32_t* parent, const int32_t* accept_idx, int32_t* len_out,
+                   void* stream) {
+  GDN_RANGE();
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (n_layers < 1) return GDN_ERR_INVALID_ARG;
+  if (n_layers > 65535 || (parent != nullptr && N > 64)) return GDN_ERR_UNSUPPORTED;
+  if (layer_stride % 16 != 0) return GDN_ERR_MISALIGNED;
+  if (n_layers > 1 && layer_stride < (int64_t)c->n_pages * c->page_stride)
+    return GDN_ERR_INVALID_ARG;
+  if (c->B == 0) return GDN_OK;
+  if (accept_idx == nullptr || len_out == nullptr || len_out == c->kv_len)
+    return GDN_ERR_INVALID_ARG;
+  if (!ok_ptr4(parent) || !ok_ptr4(accept_idx) || !ok_ptr4(len_out)) return GDN_ERR_MISALIGNED;
+  return gdn::launch_kv4_commit(*c, layer_stride, n_layers, N, parent, accept_idx, len_out,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int gdn_kv4_release(const gdn_kv4_pool* p, const int32_t* rows, const int32_t* keep_len,
+                    int32_t F, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_pool_checks(p, rows, keep_len, F);
+  if (st != GDN_OK || F == 0) return st;
+  return gdn::launch_kv4_release(*p, rows, keep_len, F, static_cast<cudaStream_t>(stream));
+}
+
+int gdn_kv4_fork(const gdn_kv4_pool* p, const int32_t* src, const int32_t* dst, int32_t F,
+                 void* stream) {
+  GDN_RANGE();
+  const int st = kv4_pool_checks(p, src, dst, F);
+  if (st != GDN_OK || F == 0) return st;
+  return gdn::launch_kv4_fork(*p, src, dst, F, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_kv4_reserve_workspace_bytes(int32_t F) {
+  return F < 1 ? 0 : gdn::kv4_reserve_workspace_bytes(F);
+}
+
+int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
+                    int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
+                    const int32_t* rows, const int32_t* new_len, int32_t F, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_pool_checks(p, rows, new_len, F);
+  if (st != GDN_OK) return st;
+  if (Hkv < 1 || n_layers < 1) return GDN_ERR_INVALID_ARG;
+  if (!kv4_head_size(D) || n_layers > 65535 || Hkv > 65535) return GDN_ERR_UNSUPPORTED;
+  const int64_t head = (int64_t)(p->page_tokens / 32) * 36 * D;
+  if (page_stride < head * Hkv) return GDN_ERR_INVALID_ARG;
+  if (n_layers > 1 && layer_stride < (int64_t)p->n_pages * page_stride)
+    return GDN_ERR_INVALID_ARG;
+  if (head * Hkv / 16 > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+  if (page_stride % 16 != 0 || layer_stride % 16 != 0) return GDN_ERR_MISALIGNED;
+  if (F == 0) return GDN_OK;
+  if (pages == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(pages) || !gdn::aligned16(workspace)) return GDN_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < gdn::kv4_reserve_workspace_bytes(F))
+    return GDN_ERR_WORKSPACE;
+  return gdn::launch_kv4_reserve(*p, pages, page_stride, layer_stride, n_layers, Hkv, D, rows,
+                                 new_len, F, workspace, static_cast<cudaStream_t>(stream));
+}
+
 const char* gdn_status_string(int status) {
   switch (status) {
     case GDN_OK: return "GDN_OK";
@@ -321,6 +487,10 @@ const char* gdn_status_string(int status) {
     case GDN_ERR_WORKSPACE: return "GDN_ERR_WORKSPACE";
     case GDN_ERR_SCRATCH_LIMIT: return "GDN_ERR_SCRATCH_LIMIT";
     case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT";
+    case GDN_ERR_PAGE_RANGE: return "GDN_ERR_PAGE_RANGE";
+    case GDN_ERR_POOL_EMPTY: return "GDN_ERR_POOL_EMPTY";
+    case GDN_ERR_ROW_RANGE: return "GDN_ERR_ROW_RANGE";
+    case GDN_ERR_NONFINITE: return "GDN_ERR_NONFINITE";
     default: return "GDN_ERR_UNKNOWN";
   }
 }

@@ -53,4 +53,25 @@ int launch_prefill_noalloc(const void* q, const void* k, const void* v, bool bf1
                            int dv, int chunk, float* state, float* o, int32_t* status,
                            cudaStream_t stream);
 
+// The 4-bit key/value cache (gdn_kv4_cache.cu), its attention (gdn_kv4_attn.cu)
+// and its page pool (gdn_kv4_pool.cu).
+int launch_kv4_append(const gdn_kv4_cache& c, const void* k, const void* v, int dtype,
+                      int64_t ksb, int64_t ksn, int64_t vsb, int64_t vsn, int N, cudaStream_t s);
+int launch_kv4_read(const gdn_kv4_cache& c, void* k, void* v, int dtype, int N, cudaStream_t s);
+size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
+                         int64_t qsn, int N, int Hq, float scale, const int32_t* parent, void* o,
+                         float* lse, void* workspace, cudaStream_t s);
+int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers, int N,
+                      const int32_t* parent, const int32_t* accept, int32_t* len_out,
+                      cudaStream_t s);
+int launch_kv4_release(const gdn_kv4_pool& p, const int32_t* rows, const int32_t* keep, int F,
+                       cudaStream_t s);
+int launch_kv4_fork(const gdn_kv4_pool& p, const int32_t* src, const int32_t* dst, int F,
+                    cudaStream_t s);
+size_t kv4_reserve_workspace_bytes(int F);
+int launch_kv4_reserve(const gdn_kv4_pool& p, void* pages, int64_t page_stride,
+                       int64_t layer_stride, int n_layers, int Hkv, int D, const int32_t* rows,
+                       const int32_t* new_len, int F, void* workspace, cudaStream_t s);
+
 }  // namespace gdn

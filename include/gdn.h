@@ -76,13 +76,20 @@ typedef enum gdn_status {
   GDN_ERR_SLOT_RANGE = -7,    /* device: slot outside [0, n_slots) */
   GDN_ERR_WORKSPACE = -8,     /* workspace missing or smaller than required */
   GDN_ERR_SCRATCH_LIMIT = -9, /* problem too large for the built-in scratch of the _noalloc call */
-  GDN_ERR_TIMEOUT = -10       /* device: a bounded wait on an asynchronous copy or tensor-core
+  GDN_ERR_TIMEOUT = -10,      /* device: a bounded wait on an asynchronous copy or tensor-core
                                  operation expired; that call's outputs are not valid */
+  GDN_ERR_PAGE_RANGE = -11,   /* device: a page-table entry outside [0, n_pages) */
+  GDN_ERR_POOL_EMPTY = -12,   /* device: fewer free pages than a row needs */
+  GDN_ERR_ROW_RANGE = -13,    /* device: a row outside the table, a length below 0 or beyond the
+                                 table's width, or a branch onto a row that is not empty */
+  GDN_ERR_NONFINITE = -14     /* device: a NaN or infinity was given to the 4-bit cache */
 } gdn_status;
 
+/* GDN_F16 (IEEE binary16) is taken by the gdn_kv4_* calls only. */
 typedef enum gdn_dtype {
   GDN_F32 = 0,
-  GDN_BF16 = 1
+  GDN_BF16 = 1,
+  GDN_F16 = 2
 } gdn_dtype;
 
 /*
@@ -377,6 +384,178 @@ int gdn_prefill_chunked_noalloc(const void* q, const void* k, const void* v, int
                                 const float* alpha, const float* beta, int32_t T, int32_t Hk,
                                 int32_t Hv, int32_t dk, int32_t dv, int32_t chunk, float* state,
                                 float* o, int32_t* status, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 4-bit key/value cache of the full-attention layers
+ * ---------------------------------------------------------------------------
+ * A hybrid model keeps one full-attention layer for every three recurrent
+ * ones.  The calls below give those layers the same speculative step as the
+ * recurrent ones have: the block's keys and values are appended to a paged
+ * cache held in 4 bits ("We got 207 tok/s with Qwen3.5-27B on an RTX 3090":
+ * a KV cache quantised on write, 128K context), the block's queries attend
+ * over it under the causal or the ancestor mask, the accepted path is
+ * committed, and sequences share and free pages.
+ *
+ * Values.  A stored value is  code * scale * head_scale:  a 4-bit e2m1 code
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit 3 is the sign), an e4m3
+ * scale shared by 16 consecutive channels of one token, and an fp32 scale per
+ * kv head (k_scale, v_scale; 1 where the pointer is NULL).  code * scale is
+ * exact in binary16.
+ *
+ * Pages.  `pages` holds n_pages pages, page_stride bytes apart; a page holds
+ * page_tokens tokens (a multiple of 32) of Hkv heads as
+ * [Hkv][page_tokens/32] records of 36*D bytes.  A record is 32 tokens of one
+ * head:
+ *     K codes   [D/32][32 tokens][16 bytes]  byte i: channels 2i (low half), 2i+1
+ *     V codes   [D][16 bytes]                byte i: tokens 2i (low half), 2i+1
+ *     K scales  [32 tokens][D/16]            e4m3
+ *     V scales  [D/16][32 tokens]            e4m3
+ * Position p of sequence b is token p % page_tokens of page
+ * table[b][p / page_tokens].
+ *
+ * Blocks.  kv_len[b] counts the block: node n of a block of N nodes is at
+ * position kv_len[b] - N + n.  Nodes at negative positions do not exist (so
+ * shorter blocks, and sequences of length 0, are given right-aligned in one
+ * call): they are not written, read back as 0, and attend over nothing.
+ *
+ * Supported sizes: D in {64, 128, 256}; page_tokens a multiple of 32; any
+ * Hkv >= 1, B >= 0, N >= 1.  Page starts are 16-byte aligned (page_stride a
+ * multiple of 16).  A sequence with a length below 0 or above
+ * max_pages*page_tokens is taken to have length 0, and GDN_ERR_ROW_RANGE is
+ * reported; positions on a page number outside [0, n_pages) are left out (not
+ * written, read as 0, not attended over), and GDN_ERR_PAGE_RANGE is reported.
+ */
+typedef struct gdn_kv4_cache {
+  void* pages;
+  const int32_t* table;  /* [B] rows of max_pages entries, table_stride entries apart */
+  const int32_t* kv_len; /* [B] */
+  const float* k_scale;  /* [Hkv] or NULL */
+  const float* v_scale;  /* [Hkv] or NULL */
+  int32_t* status;       /* optional device error word */
+  int64_t page_stride;   /* bytes */
+  int64_t table_stride;  /* entries */
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t max_pages;
+  int32_t B;
+  int32_t Hkv;
+  int32_t D;
+} gdn_kv4_cache;
+
+/*
+ * Append: quantise k and v [B][N][Hkv][D] (dtype GDN_F32, GDN_BF16 or GDN_F16;
+ * the two strides of each in elements, multiples of 16 bytes; heads and
+ * channels contiguous) into positions kv_len[b] - N .. kv_len[b] - 1.  With
+ * y = x * (1 / head_scale), saturated at +-2688, and a = max |y| over the 16
+ * channels, the scale is a * (1/6) rounded to e4m3 and the code y * (1 / scale)
+ * rounded to e2m1, both to nearest even and saturating (every operation in
+ * fp32; a scale that rounds to 0 gives codes of 0).  A NaN is stored as 0, an
+ * infinity at +-2688, and GDN_ERR_NONFINITE is reported: what the cache holds
+ * is always finite.  Pages written to must not be shared by two sequences of
+ * the call (see gdn_kv4_reserve).
+ */
+int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t dtype,
+                   int64_t k_stride_b, int64_t k_stride_n, int64_t v_stride_b,
+                   int64_t v_stride_n, int32_t N, void* stream);
+
+/*
+ * Read back: the stored values of positions kv_len[b] - N .. kv_len[b] - 1 into
+ * k_out and v_out [B][N][Hkv][D] (contiguous; rounded once to dtype).
+ */
+int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype, int32_t N,
+                 void* stream);
+
+/*
+ * Attention of the block's N query nodes over the cache (the block's own keys
+ * and values having been appended):
+ *     o[b][n][h] = sum_j p_j v_j,   p = softmax_j(scale * q[b][n][h] . k_j)
+ * over the positions j that node n sees: all before the block, and in the
+ * block the nodes up to n (parent == NULL, any N: a decoded token, a draft
+ * chain, a piece of a prompt) or n's ancestors and n itself (parent [B][N] as in
+ * gdn_verify_tree, N <= 64).  Query head h reads kv head h / (Hq / Hkv).
+ *   q    [B][N][Hq][D] GDN_BF16 or GDN_F16, strides in elements (multiples of
+ *        8), heads and channels contiguous
+ *   o    [B][N][Hq][D] contiguous, q's dtype
+ *   lse  optional [B][N][Hq] fp32: log sum_j exp(scale * q . k_j)
+ * A node that sees nothing gives o = 0 and lse = -infinity.  A sequence whose
+ * parent array is malformed is taken to have length 0 and GDN_ERR_BAD_TREE is
+ * reported.  The workspace (gdn_kv4_attention_workspace_bytes, on the current
+ * device) need not be initialised and may be reused once the call's work has
+ * finished on the stream; the size depends on the sizes given here only, not on
+ * the lengths.  The probabilities are rounded to binary16 for the product with
+ * v; sums and the running maximum are fp32.
+ */
+size_t gdn_kv4_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                                         int32_t D);
+
+int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int64_t q_stride_b,
+                      int64_t q_stride_n, int32_t N, int32_t Hq, float scale,
+                      const int32_t* parent, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Commit the accepted path of a block, for n_layers layers at once (layer l's
+ * pages at pages + l*layer_stride bytes, one table and length for all).  The
+ * path is nodes 0 .. accept_idx[b] (parent == NULL) or the ancestors of
+ * accept_idx[b] from the root (parent [B][N], N <= 64); its i-th node's keys
+ * and values are moved to position kv_len[b] - N + i, codes and scales
+ * unchanged, and len_out[b] = kv_len[b] - N + (nodes on the path).  Positions
+ * from len_out[b] on keep unspecified contents.  len_out must not be kv_len.
+ * A block with kv_len[b] < N, a bad accept index or a malformed parent array
+ * leaves the sequence as it is (len_out[b] = kv_len[b]) and is reported
+ * (GDN_ERR_ROW_RANGE, GDN_ERR_ACCEPT_RANGE, GDN_ERR_BAD_TREE).
+ */
+int gdn_kv4_commit(const gdn_kv4_cache* c, int64_t layer_stride, int32_t n_layers, int32_t N,
+                   const int32_t* parent, const int32_t* accept_idx, int32_t* len_out,
+                   void* stream);
+
+/*
+ * The page pool: a table of n_rows sequences, their lengths, and for every page
+ * the number of table entries that hold it (ref[p]; 0 = free).  A row of length
+ * n holds its first ceil(n / page_tokens) entries; the others are -1.  All of it
+ * is device memory that the three calls below read and update on the stream, so
+ * a captured step can branch and free sequences without the host.  The rows
+ * named by one call must be distinct (fork: the dst rows; a dst row is not a
+ * src row).  A row that cannot be served is left as it is and reported.
+ */
+typedef struct gdn_kv4_pool {
+  int32_t* table;  /* [n_rows] rows of max_pages entries, table_stride entries apart */
+  int32_t* kv_len; /* [n_rows] */
+  int32_t* ref;    /* [n_pages] */
+  int32_t* status;
+  int64_t table_stride;
+  int32_t n_rows;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_tokens;
+} gdn_kv4_pool;
+
+/* Truncate rows[i] to keep_len[i] tokens (0 frees it; a keep_len of the row's length or more
+ * changes nothing): the pages past it lose a holder and their entries become -1. */
+int gdn_kv4_release(const gdn_kv4_pool* p, const int32_t* rows, const int32_t* keep_len,
+                    int32_t F, void* stream);
+
+/* Branch row src[i] onto the empty row dst[i]: the same pages, one more holder each. */
+int gdn_kv4_fork(const gdn_kv4_pool* p, const int32_t* src, const int32_t* dst, int32_t F,
+                 void* stream);
+
+/*
+ * Grow rows[i] to new_len[i] tokens (no less than its length), taking the
+ * lowest-numbered free pages in the order of the rows.  Where the row's last
+ * page is partly filled and had other holders when the call began, the row gets
+ * a page of its own first: the records that hold tokens are copied, in all
+ * n_layers layers (copy-on-write), and the old page loses a holder.  A row that
+ * does not fit, and every row after it that needs pages, is left as it is:
+ * GDN_ERR_POOL_EMPTY.  Afterwards positions below new_len[i] from the old
+ * length on may be appended to.
+ */
+size_t gdn_kv4_reserve_workspace_bytes(int32_t F);
+
+int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
+                    int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
+                    const int32_t* rows, const int32_t* new_len, int32_t F, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a gdn_status value (static string, never NULL). */
 const char* gdn_status_string(int status);
