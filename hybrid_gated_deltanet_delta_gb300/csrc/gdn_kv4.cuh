@@ -139,6 +139,7 @@ __device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
 // Checks parent[0..N) (N <= 64) of one sequence; every thread may call it.
 __device__ __forceinline__ bool tree_ok(const int32_t* parent, int N) {
   bool ok = parent[0] == -1;
+#pragma unroll 4
   for (int n = 1; n < N; ++n) ok = ok && parent[n] >= 0 && parent[n] < n;
   return ok;
 }

@@ -21,7 +21,7 @@ int blocks() {
     (void)cudaGetLastError();
     return 0;
   }
-  return sms;
+  return sms < 1024 ? sms : 1024;
 }
 
 void row_tiles(int rows, int* tiles, int* per_tile) {
@@ -36,7 +36,8 @@ size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   row_tiles(N * (Hq / Hkv), &tiles, &per_tile);
   // without a device (a size asked for on the host alone) as for 256 SMs
   const int sms = blocks();
-  return (size_t)2 * (sms > 0 ? sms : 256) * round_rows(per_tile) * (D * 4 + 8);
+  return (size_t)(sms > 0 ? sms : 256) *
+         (2 * round_rows(per_tile) * (D * 4 + 8) + sizeof(kv4::AttnJoin));
 }
 
 int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb, int64_t qsn,
@@ -62,6 +63,7 @@ int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64
   const int NT = round_rows(a.rows_per_tile);
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * parts * NT * c.D);
+  a.join = reinterpret_cast<kv4::AttnJoin*>(a.part_ml + (size_t)2 * parts * NT);
   switch (c.D) {
     case 64: return kv4::attn_launch_64(a, NT, parts, s);
     case 128: return kv4::attn_launch_128(a, NT, parts, s);

@@ -85,9 +85,18 @@ struct AttnCfg {
 
 struct Row {       // of a query row, beside its operand
   float c;         // logit of S: c * S (log2 units)
-  float pad;
-  unsigned lo, hi; // chain: node in lo; tree: the positions of the block it sees
+  int at;          // row of the output, from the item's first node and head on
+  unsigned lo, hi; // trees: the positions of the block that the row sees
 };
+
+// The part of one item that a block works on: tiles [t0, t1) of `tiles` (t1 = 0: the end).
+struct Seg {
+  int b, h, t0, t1, tiles, len, row0, rows;
+  int last;  // block that holds the item's last tile
+};
+
+constexpr int kSegs = 16;    // ring of segments; a block's warps are fewer apart
+constexpr int kLens = 1024;  // lengths kept in shared memory
 
 template <typename C>
 struct AttnShared {
@@ -95,18 +104,20 @@ struct AttnShared {
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
   uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], vs_full[2], vs_empty[2];
   uint64_t q_full[C::NQ], q_empty[C::NQ], row_full[2], row_empty[2], o_full, o_empty, drain;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int dead;
-  AttnSpan span;
   int tile_ok[8];  // records of a tile that could be read, by tile number
   alignas(16) float2 cm[C::NT];  // (c, m) of the rows in work; read two rows a load
+  alignas(16) Seg seg[kSegs];
+  alignas(16) Row row[2][C::NT];
   float alpha[C::NT], inv[C::NT];
   float wmax[4][C::NT];
-  Row row[2][C::NT];
+  int len[kLens];
 };
 
 // A wait that ends: false once any wait of the block has run out.
-__device__ __forceinline__ bool attn_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
+static __device__ __noinline__ bool attn_wait_on(uint64_t* bar, unsigned parity, volatile int* dead) {
   for (int i = 0; i < kWaitPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 63 && *dead) return false;
@@ -115,8 +126,32 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, unsigned parity, volati
   return false;
 }
 
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return attn_wait_on(bar, parity, dead);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(e));
+  return e != 0;
+}
+
+// Named barrier over `threads` threads; true for all when `x` holds for any.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.u32 p, %1, 0;"
+      " barrier.cta.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q;}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
 }
 
 // tcgen05.mma kind::f16 with A in TMEM.
@@ -196,21 +231,11 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(i);
 }
 
-// ---------------------------------------------------------------- segments
-// The part of one item that a block works on: tiles [t0, t1) of `tiles`.
-struct Seg {
-  int b, h, rt, t0, t1, tiles;
-  int len, rows, n_lo, n_hi;
-};
-
-__device__ __forceinline__ bool attn_tree_bad(const AttnArgs& a, int b) {
-  return a.parent != nullptr && !tree_ok(a.parent + (int64_t)b * a.N, a.N);
-}
-
+// ---------------------------------------------------------------- work
 // Length of sequence b as attention counts it (0: skipped).
-__device__ __forceinline__ int attn_len(const AttnArgs& a, int b, bool report_it) {
+static __device__ __noinline__ int attn_len(const AttnArgs& a, int b, bool report_it) {
   const int n = seq_len(a.c, b, report_it);
-  if (n > 0 && attn_tree_bad(a, b)) {
+  if (n > 0 && a.parent != nullptr && !tree_ok(a.parent + (int64_t)b * a.N, a.N)) {
     if (report_it) report(a.c.status, GDN_ERR_BAD_TREE);
     return 0;
   }
@@ -221,109 +246,206 @@ __device__ __forceinline__ int attn_len(const AttnArgs& a, int b, bool report_it
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int len, int rt) {
   int see = len;
   if (a.parent == nullptr) {
-    int last = (rt + 1) * a.rows_per_tile - 1;
-    if (last >= a.rows_total) last = a.rows_total - 1;
+    const int last = min((rt + 1) * a.rows_per_tile, a.rows_total) - 1;
     see = len - a.N + last / a.G + 1;
   }
   return see <= 0 ? 0 : (see + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ int64_t attn_cost(const AttnArgs& a, int len) {
-  int64_t t = 0;
-  for (int rt = 0; rt < a.row_tiles; ++rt) t += attn_tiles(a, len, rt);
-  return t * a.c.Hkv;
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-__device__ __forceinline__ void seg_rows(const AttnArgs& a, Seg& s) {
-  const int first = s.rt * a.rows_per_tile;
-  s.rows = a.rows_total - first < a.rows_per_tile ? a.rows_total - first : a.rows_per_tile;
-  s.n_lo = first / a.G;
-  s.n_hi = (first + s.rows - 1) / a.G;
-}
+// The lengths the block works with: the first kLens are kept in shared memory.
+struct Lens {
+  const AttnArgs& a;
+  const int* kept;
+  __device__ __forceinline__ int operator()(int b) const {
+    return b < kLens ? kept[b] : attn_len(a, b, false);
+  }
+};
 
-// First segment of the block's run; false when the run is empty.
-__device__ __forceinline__ bool seg_first(const AttnArgs& a, const AttnSpan& sp, Seg& s,
-                                          int64_t& left) {
-  left = sp.count;
-  if (left <= 0) return false;
-  s.b = sp.b, s.h = sp.h, s.rt = sp.rt, s.t0 = sp.t0;
-  s.len = attn_len(a, s.b, false);
-  s.tiles = attn_tiles(a, s.len, s.rt);
-  s.t1 = s.t0 + left < s.tiles ? s.t0 + (int)left : s.tiles;
-  left -= s.t1 - s.t0;
-  seg_rows(a, s);
-  return true;
-}
-
-__device__ __forceinline__ bool seg_next(const AttnArgs& a, Seg& s, int64_t& left) {
-  if (left <= 0) return false;
-  do {
-    if (++s.rt == a.row_tiles) {
-      s.rt = 0;
-      if (++s.h == a.c.Hkv) {
-        s.h = 0;
-        if (++s.b >= a.c.B) return false;
-        s.len = attn_len(a, s.b, false);
-      }
-    }
-    s.tiles = attn_tiles(a, s.len, s.rt);
-  } while (s.tiles == 0);
-  s.t0 = 0;
-  s.t1 = left < s.tiles ? (int)left : s.tiles;
-  left -= s.t1;
-  seg_rows(a, s);
-  return true;
-}
-
-// The run of block `part` of `parts`, found by one warp: every sequence's tiles
-// are summed, then the one that holds the run's first tile is taken apart.
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int part, int parts,
-                                              bool report_it) {
+// Lengths into shared memory, by all threads: a thread a sequence, or for
+// trees a warp a sequence (its lanes check the nodes).
+__device__ __forceinline__ void attn_lens(const AttnArgs& a, int* kept, bool report_it) {
+  if (a.parent == nullptr) {
+#pragma unroll 1
+    for (int b = threadIdx.x; b < min(a.c.B, kLens); b += blockDim.x)
+      kept[b] = seq_len(a.c, b, report_it);
+    return;
+  }
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b = threadIdx.x >> 5; b < min(a.c.B, kLens); b += blockDim.x >> 5) {
+    const int32_t* p = a.parent + (int64_t)b * a.N;
+    bool ok = true;
+    for (int n = lane; n < a.N; n += 32) ok = ok && (n == 0 ? p[n] == -1 : p[n] >= 0 && p[n] < n);
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      const int len = seq_len(a.c, b, report_it);
+      if (report_it && len > 0 && !ok) report(a.c.status, GDN_ERR_BAD_TREE);
+      kept[b] = ok ? len : 0;
+    }
+  }
+  if (report_it)  // the others' reports (their lengths are looked up when needed)
+#pragma unroll 1
+    for (int b = kLens + threadIdx.x; b < a.c.B; b += blockDim.x) (void)attn_len(a, b, true);
+}
+
+// Tiles of sequence b over all heads, by a whole warp.
+__device__ __forceinline__ int64_t warp_cost(const AttnArgs& a, int len) {
+  int64_t t = 0;
+#pragma unroll 1
+  for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_tiles(a, len, rt);
+  return warp_sum(t) * a.c.Hkv;
+}
+
+// Equal runs of `total` tiles for at most `parts` blocks: the first `extra` runs
+// have one tile more.
+struct Runs {
+  int64_t each, extra;
+  int parts;
+  __device__ __forceinline__ Runs(int64_t total, int n) {
+    parts = total < n ? (int)total : n;  // no empty runs in between
+    each = parts > 0 ? total / parts : 0;
+    extra = total - each * parts;
+  }
+  __device__ __forceinline__ int64_t start(int part) const {
+    return each * part + (part < extra ? part : extra);
+  }
+  // the run that holds tile x
+  __device__ __forceinline__ int of(int64_t x) const {
+    const int64_t head = extra * (each + 1);
+    return (int)(x < head ? x / (each + 1) : extra + (x - head) / each);
+  }
+};
+
+// Walks the tiles of a block's run, item by item (one warp).
+struct Run {
+  int b, h, rt, t0;
+  int64_t at, left;
+  Runs runs;
+};
+
+// The run of block `part` of `parts`: the tiles of all sequences are counted,
+// then the sequence that holds the run's first tile is taken apart.
+static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens, int part, int parts) {
+  const int lane = threadIdx.x & 31;
+  const bool by_lane = a.row_tiles <= 4;  // a lane a sequence, or the warp a sequence
   int64_t total = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t x = b < a.c.B ? attn_cost(a, attn_len(a, b, report_it)) : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    total += x;
-  }
-  AttnSpan sp = {};
-  if (parts > total) parts = (int)total;  // no empty runs in between
-  if (part >= parts) return sp;
-  const int64_t start = total * part / parts, end = total * (part + 1) / parts;
-  sp.count = end - start;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int64_t mine = b < a.c.B ? attn_cost(a, attn_len(a, b, false)) : 0;
-    int64_t x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + x > start);
-    if (hit != 0) {
-      const int l = __ffs(hit) - 1;
-      const int64_t upto = __shfl_sync(0xffffffffu, x, l), its = __shfl_sync(0xffffffffu, mine, l);
-      int64_t in = start - before - (upto - its);
-      sp.b = b0 + l;
-      const int64_t per_head = its / a.c.Hkv;
-      sp.h = (int)(in / per_head);
-      in -= sp.h * per_head;
-      const int len = attn_len(a, sp.b, false);
-      for (sp.rt = 0;; ++sp.rt) {
-        const int t = attn_tiles(a, len, sp.rt);
-        if (in < t) break;
-        in -= t;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.c.B; b0 += by_lane ? 32 : 1) {
+    if (by_lane) {
+      if (b0 + lane < a.c.B) {
+        const int len = lens(b0 + lane);
+#pragma unroll 1
+        for (int rt = 0; rt < a.row_tiles; ++rt) total += attn_tiles(a, len, rt);
       }
-      sp.t0 = (int)in;
-      return sp;
+    } else {
+      total += warp_cost(a, lens(b0));
     }
-    before += __shfl_sync(0xffffffffu, x, 31);
   }
-  return sp;
+  if (by_lane) total = warp_sum(total) * a.c.Hkv;
+  const Runs runs(total, parts);
+  Run r = {0, 0, 0, 0, 0, 0, runs};
+  if (part >= runs.parts) return r;
+  const int64_t start = runs.start(part);
+  r.at = start;
+  r.left = runs.start(part + 1) - start;
+  int64_t before = 0, its = 0;
+#pragma unroll 1
+  for (int b0 = 0;; b0 += by_lane ? 32 : 1) {
+    if (by_lane) {
+      int64_t mine = 0;
+      if (b0 + lane < a.c.B) {
+        const int len = lens(b0 + lane);
+#pragma unroll 1
+        for (int rt = 0; rt < a.row_tiles; ++rt) mine += attn_tiles(a, len, rt);
+        mine *= a.c.Hkv;
+      }
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + x > start);
+      if (hit == 0) {
+        before += __shfl_sync(0xffffffffu, x, 31);
+        continue;
+      }
+      const int l = __ffs(hit) - 1;
+      its = __shfl_sync(0xffffffffu, mine, l);
+      before += __shfl_sync(0xffffffffu, x, l) - its;
+      r.b = b0 + l;
+    } else {
+      its = warp_cost(a, lens(b0));
+      if (before + its <= start) {
+        before += its;
+        continue;
+      }
+      r.b = b0;
+    }
+    break;
+  }
+  int in = (int)(start - before);  // of the sequence's its tiles
+  const int per_head = (int)(its / a.c.Hkv), len = lens(r.b);
+  r.h = in / per_head;
+  in -= r.h * per_head;
+#pragma unroll 1
+  for (;; ++r.rt) {
+    const int t = attn_tiles(a, len, r.rt);
+    if (in < t) break;
+    in -= t;
+  }
+  r.t0 = in;
+  return r;
+}
+
+// The run's next segment (t1 = 0 when it is at its end).
+static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens& lens, Run& r) {
+  Seg s = {};
+#pragma unroll 1
+  while (r.left > 0 && r.b < a.c.B) {
+    const int len = lens(r.b);
+    const int tiles = attn_tiles(a, len, r.rt);
+    const int t0 = r.t0, rt = r.rt, h = r.h, b = r.b;
+    r.t0 = 0;
+    if (++r.rt == a.row_tiles) {
+      r.rt = 0;
+      if (++r.h == a.c.Hkv) r.h = 0, ++r.b;
+    }
+    if (tiles <= t0) continue;
+    s.b = b, s.h = h, s.t0 = t0, s.tiles = tiles, s.len = len;
+    s.t1 = r.left < tiles - t0 ? t0 + (int)r.left : tiles;
+    r.left -= s.t1 - t0;
+    r.at += s.t1 - t0;
+    s.last = s.t1 < tiles ? r.runs.of(r.at + tiles - s.t1 - 1) : 0;
+    s.row0 = rt * a.rows_per_tile;
+    s.rows = min(a.rows_total - s.row0, a.rows_per_tile);
+    return s;
+  }
+  return s;
+}
+
+// Rows that see no tile at all: 0 (and -infinity), spread over the blocks; 128 threads.
+static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& lens, int D, int tid) {
+  const int64_t pairs = (int64_t)a.c.B * a.row_tiles;
+#pragma unroll 1
+  for (int64_t i = blockIdx.x; i < pairs; i += gridDim.x) {
+    const int b = (int)(i / a.row_tiles), rt = (int)(i % a.row_tiles);
+    if (attn_tiles(a, lens(b), rt) > 0) continue;
+    const int row0 = rt * a.rows_per_tile, rows = min(a.rows_total - row0, a.rows_per_tile);
+#pragma unroll 1
+    for (int k = 0; k < rows * a.c.Hkv; ++k) {
+      const int h = k / rows, r = row0 + k % rows;
+      const int64_t at = ((int64_t)b * a.N + r / a.G) * a.Hq + h * a.G + r % a.G;
+      if (tid < D / 2) static_cast<uint32_t*>(a.o)[at * (D / 2) + tid] = 0;
+      if (a.lse != nullptr && tid == 0) a.lse[at] = -INFINITY;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -347,6 +469,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       mbar_init(&sh.row_full[i], 2), mbar_init(&sh.row_empty[i], 8);
     }
     for (int i = 0; i < C::NQ; ++i) mbar_init(&sh.q_full[i], 2), mbar_init(&sh.q_empty[i], 1);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 19);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.o_empty, 8);
     mbar_init(&sh.drain, 1);
@@ -355,39 +478,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   }
   if (warp == 16) tc::tmem_alloc(&sh.tmem, 512);
   pdl_enter();
-  if (warp == 17) {
-    const AttnSpan sp = attn_span(a, blockIdx.x, gridDim.x, blockIdx.x == 0);
-    if (lane == 0) sh.span = sp;
-  }
+  attn_lens(a, sh.len, blockIdx.x == 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
-  const AttnSpan span = sh.span;
+
+  // every warp but 17 takes the run's segments from the ring
+  int seg_no = 0;
   Seg s;
-  int64_t left;
-  bool on = seg_first(a, span, s, left);
+  auto next_seg = [&]() {
+    const int i = seg_no & (kSegs - 1);
+    attn_wait(&sh.seg_full[i], (seg_no / kSegs) & 1, dead);
+    s = sh.seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.seg_empty[i]);
+    return s.t1 > 0 && !__any_sync(0xffffffffu, *dead);
+  };
 
   if (warp < 4) {
     // ------------------------------------------------ K -> TMEM
     const uint32_t dst = tmem + ((uint32_t)(warp * 32) << 16);
     int stage = 0, unit = 0;
     unsigned raw_ph = 0, unit_ph = 1;  // an empty ring's first pass does not wait
-    for (; on; on = seg_next(a, s, left)) {
+    for (; next_seg(); ++seg_no) {
+#pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t) {
         attn_wait(&sh.raw_full[stage], raw_ph, dead);
         const uint8_t* rec = smem + C::oRaw + stage * C::RAW + warp * rec_bytes(D);
-        uint32_t s8[D / 64];
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          s8[i] = reinterpret_cast<const uint32_t*>(rec + off_ks(D) + lane * (D / 16))[i];
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < C::UNITS; ++u) {
+          const uint32_t s8 =
+              *reinterpret_cast<const uint32_t*>(rec + off_ks(D) + lane * (D / 16) + u * 4);
           uint32_t w[32];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const uint4 q4 = *reinterpret_cast<const uint4*>(rec + (2 * u + half) * 512 + lane * 16);
-            const uint32_t sc = e4m3x2(s8[u] >> (16 * half));
+            const uint32_t sc = e4m3x2(s8 >> (16 * half));
             const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
             dequant8(q4.x, s0, w + 16 * half);
             dequant8(q4.y, s0, w + 16 * half + 4);
@@ -404,7 +531,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           if (lane == 0) mbar_arrive(&sh.k_full[unit]);
           if (++unit == C::KU) unit = 0, unit_ph ^= 1;
         }
-        __syncwarp();
         if (lane == 0) mbar_arrive(&sh.raw_empty[stage]);
         if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
       }
@@ -413,14 +539,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     // ------------------------------------------------ V^T -> TMEM
     const int quarter = warp - 4;
     const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + C::cV;
+    attn_zero(a, Lens{a, sh.len}, D, threadIdx.x - 128);
     int stage = 0, unit = 0, vb = 0;
     unsigned vs_ph = 0, unit_ph = 1;
-    for (; on; on = seg_next(a, s, left)) {
+    for (; next_seg(); ++seg_no) {
+#pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t) {
         attn_wait(&sh.vs_full[vb], vs_ph, dead);  // the records have landed before
         const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
         const uint8_t* vs = smem + C::oVS + vb * C::VSB;
-#pragma unroll
+#pragma unroll 1
         for (int r = 0; r < 4; ++r) {
           uint32_t w[C::MB][16];
 #pragma unroll
@@ -455,7 +583,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           if (lane == 0) mbar_arrive(&sh.v_full[unit]);
           if (++unit == C::VU) unit = 0, unit_ph ^= 1;
         }
-        __syncwarp();
         if (lane == 0) mbar_arrive(&sh.raw_empty[stage]), mbar_arrive(&sh.vs_empty[vb]);
         if (++stage == C::NRAW) stage = 0;
         if (++vb == 2) vb = 0, vs_ph ^= 1;
@@ -468,107 +595,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     const int gt = (threadIdx.x - 256) & 127;      // thread of the group
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     constexpr int CH = C::NH < 16 ? C::NH : 16;    // columns of one load
-    int tile = 0, seg_no = 0;
-    for (; on; on = seg_next(a, s, left), ++seg_no) {
+    int tile = 0;
+    AttnJoin join = {};
+    for (;; ++seg_no) {
+      // all eight warps go on, or none: they meet at barriers below
+      if (barrier_any(3, 256, !next_seg())) break;
       const int base = s.len - a.N;
+      const int n_lo = s.row0 / a.G;
       const Row* rows = sh.row[seg_no & 1];
       attn_wait(&sh.row_full[seg_no & 1], (seg_no >> 1) & 1, dead);
+      if (gt < C::NH) sh.cm[c0 + gt] = make_float2(rows[c0 + gt].c, kNone);
+      tc::named_barrier(1 + group, 128);
       float l[C::NH];
 #pragma unroll
       for (int i = 0; i < C::NH; ++i) l[i] = 0.f;
+#pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int buf = tile & 1;
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
         tc::fence_after_sync();
-        if (t == s.t0) {  // the rows' scales came with the queries
-          if (gt < C::NH) sh.cm[c0 + gt] = make_float2(rows[c0 + gt].c, kNone);
-          tc::named_barrier(1 + group, 128);
-        }
-        attn_wait(&sh.p_empty[buf], ph ^ 1, dead);
         const int ok = sh.tile_ok[tile & 7];
-        const int pos = t * kTile + quarter * 32 + lane, u = pos - base;
-        // every row sees the whole tile?
-        const bool masked = ok != 15 || (a.parent != nullptr ? t * kTile + kTile > base
-                                                             : t * kTile + kTile - 1 > base + s.n_lo);
-        const bool gone = !((ok >> quarter) & 1);
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
-        uint8_t* prow = smem + C::oP + buf * C::PB + (quarter * 32 + lane) * 128;
-        auto hidden = [&](int r) {
-          if (gone) return true;
-          const Row& w = rows[c0 + r];
-          if (a.parent == nullptr) return u > (int)w.lo;
-          if (u < 0) return false;
-          return u >= 64 || !(((u < 32 ? w.lo : w.hi) >> (u & 31)) & 1);
-        };
-        // p of all rows with the present references, sums updated; returns the
-        // largest exponent seen
-        auto pass = [&](bool mask) {
+        // rows that see this position, where not all rows see all of the tile
+        const bool masked = ok != 15 || (a.parent != nullptr ? (t + 1) * kTile > base
+                                                             : (t + 1) * kTile - 1 > base + n_lo);
+        unsigned long long vis = ~0ull;
+        if (masked) {
+          const int u = t * kTile + quarter * 32 + lane - base;
+          if (!((ok >> quarter) & 1)) {
+            vis = 0;
+          } else if (a.parent == nullptr) {
+            // nodes rise with the rows: the first row of node u
+            const int64_t from = (int64_t)u * a.G - s.row0 - c0;
+            vis = from <= 0 ? ~0ull : from >= 64 ? 0ull : ~0ull << from;
+          } else if (u >= 0) {
+            vis = 0;
+            if (u < 64)
+#pragma unroll 1
+              for (int r = 0; r < C::NH; ++r) {
+                const Row& w = rows[c0 + r];
+                vis |= (unsigned long long)(((u < 32 ? w.lo : w.hi) >> (u & 31)) & 1) << r;
+              }
+          }
+        }
+        // ---- would any p pass 2^kSlack?  (first tile: yes)
+        bool raise = t == s.t0;
+        if (!raise) {
           float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < C::NH; k += CH) {
             uint32_t x[CH];
             tmem_load(sa + k, x);
             tc::tmem_wait_ld(x);
-            uint32_t p[CH / 2];
+            const unsigned v = (unsigned)(vis >> k);
 #pragma unroll
             for (int i = 0; i < CH; i += 2) {
               const float4 cm = *reinterpret_cast<const float4*>(&sh.cm[c0 + k + i]);
               float y0 = fmaf(__uint_as_float(x[i]), cm.x, -cm.y);
               float y1 = fmaf(__uint_as_float(x[i + 1]), cm.z, -cm.w);
-              if (mask) {
-                if (hidden(k + i)) y0 = -INFINITY;
-                if (hidden(k + i + 1)) y1 = -INFINITY;
+              if (masked) {
+                y0 = (v >> i) & 1 ? y0 : -INFINITY;
+                y1 = (v >> (i + 1)) & 1 ? y1 : -INFINITY;
               }
               top = fmaxf(top, fmaxf(y0, y1));
-              y0 = exp2_fast(y0);
-              y1 = exp2_fast(y1);
-              l[k + i] += y0;
-              l[k + i + 1] += y1;
-              p[i / 2] = pack_f16x2(y0, y1);
-            }
-#pragma unroll
-            for (int i = 0; i < CH / 8; ++i) {
-              const int col = c0 + k + 8 * i;  // 16-byte chunk of 8 rows, swizzled by position
-              uint8_t* at = prow + (col >> 6) * (kTile * 128) +
-                            ((((col & 63) >> 3) ^ (lane & 7)) << 4);
-              *reinterpret_cast<uint4*>(at) =
-                  make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
             }
           }
-          return top;
-        };
-        // takes back what pass() added (a row whose p overflowed held less than
-        // 2^-24 of what is to come)
-        auto undo = [&](bool mask) {
-#pragma unroll
+          raise = barrier_any(1 + group, 128, top > kSlack);  // NaN rows stay NaN without it
+        }
+        if (raise) {
+          // ---- new references: the largest logits so far
+#pragma unroll 1
           for (int k = 0; k < C::NH; k += CH) {
             uint32_t x[CH];
             tmem_load(sa + k, x);
             tc::tmem_wait_ld(x);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const float2 cm = sh.cm[c0 + k + i];
-              float y = fmaf(__uint_as_float(x[i]), cm.x, -cm.y);
-              if (mask && hidden(k + i)) y = -INFINITY;
-              l[k + i] = y > 100.f ? 0.f : l[k + i] - exp2_fast(y);
-            }
-          }
-        };
-        // new references: the largest logit so far
-        auto raise = [&](bool mask, bool first) {
-#pragma unroll
-          for (int k = 0; k < C::NH; k += CH) {
-            uint32_t x[CH];
-            tmem_load(sa + k, x);
-            tc::tmem_wait_ld(x);
+            const unsigned v = (unsigned)(vis >> k);
+            float mine = 0.f;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
               float y = __uint_as_float(x[i]) * sh.cm[c0 + k + i].x;
-              if (mask && hidden(k + i)) y = -INFINITY;
-              y = warp_max(y);
-              if (lane == 0) sh.wmax[quarter][c0 + k + i] = y;
+              y = warp_max((v >> i) & 1 ? y : -INFINITY);
+              if (lane == i) mine = y;
             }
+            if (lane < CH) sh.wmax[quarter][c0 + k + lane] = mine;
           }
           tc::named_barrier(1 + group, 128);
           if (gt < C::NH) {
@@ -584,44 +694,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             sh.alpha[r] = exp2_fast(old - m);
           }
           tc::named_barrier(1 + group, 128);
-          if (!first) {
+          if (t != s.t0) {
             // every product into O^T so far is done: the last one freed its P
             attn_wait(&sh.p_empty[buf ^ 1], ((tile - 1) >> 1) & 1, dead);
             tc::fence_after_sync();
 #pragma unroll
             for (int k = 0; k < C::NH; ++k) l[k] *= sh.alpha[c0 + k];
-            for (int mb = 0; mb < C::MB; ++mb) {
+#pragma unroll 1
+            for (int k = 0; k < C::MB * C::NH; k += 8) {
+              const int col = c0 + k % C::NH;
+              const uint32_t oa = lane_base + C::cO + k / C::NH * C::NT + col;
+              uint32_t x[8];
+              tc::tmem_ld8(oa, x);
+              tc::tmem_wait_ld(x);
 #pragma unroll
-              for (int k = 0; k < C::NH; k += 8) {
-                const uint32_t oa = lane_base + C::cO + mb * C::NT + c0 + k;
-                uint32_t x[8];
-                tc::tmem_ld8(oa, x);
-                tc::tmem_wait_ld(x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  x[i] = __float_as_uint(__uint_as_float(x[i]) * sh.alpha[c0 + k + i]);
-                tmem_st8(oa, x);
-              }
+              for (int i = 0; i < 8; ++i)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) * sh.alpha[col + i]);
+              tmem_st8(oa, x);
             }
             tmem_wait_st();
           }
-        };
-        const bool first = t == s.t0;
-        if (first) raise(masked, true);
-        float top = masked ? pass(true) : pass(false);
-        if (!first) {
-          // NaN logits keep their row NaN and do not count here
-          unsigned over = top > kSlack, any;
-          asm volatile(
-              "{.reg .pred p, q; setp.ne.u32 p, %1, 0;"
-              " barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q;}"
-              : "=r"(any)
-              : "r"(over), "r"(1 + group)
-              : "memory");
-          if (any) {
-            undo(masked);
-            raise(masked, false);
-            pass(masked);
+        }
+        // ---- p, its sums, and P as the B operand
+        attn_wait(&sh.p_empty[buf], ph ^ 1, dead);
+        uint8_t* prow = smem + C::oP + buf * C::PB + (quarter * 32 + lane) * 128;
+#pragma unroll
+        for (int k = 0; k < C::NH; k += CH) {
+          uint32_t x[CH];
+          tmem_load(sa + k, x);
+          tc::tmem_wait_ld(x);
+          uint32_t p[CH / 2];
+          const unsigned v = (unsigned)(vis >> k);
+#pragma unroll
+          for (int i = 0; i < CH; i += 2) {
+            const float4 cm = *reinterpret_cast<const float4*>(&sh.cm[c0 + k + i]);
+            float y0 = exp2_fast(fmaf(__uint_as_float(x[i]), cm.x, -cm.y));
+            float y1 = exp2_fast(fmaf(__uint_as_float(x[i + 1]), cm.z, -cm.w));
+            if (masked) {
+              y0 = (v >> i) & 1 ? y0 : 0.f;
+              y1 = (v >> (i + 1)) & 1 ? y1 : 0.f;
+            }
+            l[k + i] += y0;
+            l[k + i + 1] += y1;
+            p[i / 2] = pack_f16x2(y0, y1);
+          }
+#pragma unroll
+          for (int i = 0; i < CH / 8; ++i) {
+            const int col = c0 + k + 8 * i;  // 16-byte chunk of 8 rows, swizzled by position
+            uint8_t* at = prow + (col >> 6) * (kTile * 128) +
+                          ((((col & 63) >> 3) ^ (lane & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) =
+                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
           }
         }
         fence_proxy_async_smem();
@@ -629,9 +752,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.s_empty[buf]), mbar_arrive(&sh.p_full[buf]);
       }
-      if (lane == 0) mbar_arrive(&sh.row_empty[seg_no & 1]);
       // ---- epilogue
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      const int64_t item = (int64_t)s.b * a.N * a.Hq + s.h * a.G;  // output row of node 0
       attn_wait(&sh.o_full, seg_no & 1, dead);
       tc::fence_after_sync();
       float* sums = reinterpret_cast<float*>(smem + C::oP) + c0 * 129;  // P is free now
@@ -639,7 +762,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       for (int k = 0; k < C::NH; ++k) sums[k * 129 + gt] = l[k];
       tc::named_barrier(1 + group, 128);
       const int64_t slot = 2 * (int64_t)blockIdx.x + (seg_no > 0);
-      const int row0 = s.rt * a.rows_per_tile;
+      if (s.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
+        join = {item, s.h, s.row0, s.rows, (int)slot, s.last};
       if (gt < C::NH) {
         const int r = c0 + gt;
         float total = 0.f;
@@ -649,191 +773,206 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         if (whole) {
           const float vsc = a.c.v_scale != nullptr ? a.c.v_scale[s.h] : 1.f;
           sh.inv[r] = total != 0.f ? vsc / total : 0.f;
-          if (a.lse != nullptr && r < s.rows) {
-            const int n = (row0 + r) / a.G, g = (row0 + r) % a.G;
-            a.lse[((int64_t)s.b * a.N + n) * a.Hq + s.h * a.G + g] =
+          if (a.lse != nullptr && r < s.rows)
+            a.lse[item + rows[r].at] =
                 total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
-          }
         } else {
           a.part_ml[slot * NT + r] = make_float2(m, total);
           sh.inv[r] = 1.f;
         }
       }
       tc::named_barrier(3, 256);  // both groups' sums are read: P may be written again
+#pragma unroll 1
       for (int mb = 0; mb < C::MB; ++mb) {
         const int ch = mb * 128 + quarter * 32 + lane;
-#pragma unroll
-        for (int k = 0; k < C::NH; k += 8) {
-          if (c0 + k >= s.rows) break;
+#pragma unroll 1
+        for (int r0 = c0; r0 < c0 + C::NH && r0 < s.rows; r0 += 8) {
           uint32_t x[8];
-          tc::tmem_ld8(lane_base + C::cO + mb * C::NT + c0 + k, x);
+          tc::tmem_ld8(lane_base + C::cO + mb * C::NT + r0, x);
           tc::tmem_wait_ld(x);
-          if (ch >= D) continue;
+          if (D < 128 && ch >= D) continue;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = c0 + k + i;
+            const int r = r0 + i;
             if (r >= s.rows) break;
             const float o = __uint_as_float(x[i]) * sh.inv[r];
-            if (whole) {
-              const int n = (row0 + r) / a.G, g = (row0 + r) % a.G;
-              const int64_t at = (((int64_t)s.b * a.N + n) * a.Hq + s.h * a.G + g) * D + ch;
-              static_cast<uint16_t*>(a.o)[at] =
+            if (whole)
+              static_cast<uint16_t*>(a.o)[(item + rows[r].at) * D + ch] =
                   a.bf16 ? Elem<GDN_BF16>::from(o) : Elem<GDN_F16>::from(o);
-            } else {
+            else
               a.part_o[(slot * NT + r) * D + ch] = o;
-            }
           }
         }
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_empty);
+      if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.row_empty[seg_no & 1]);
     }
+    if (threadIdx.x == 256) a.join[blockIdx.x] = join;
   } else if (warp == 16) {
-    // ------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f16(NT, false), id_o = idesc_f16(NT, true);
-      const uint32_t q0 = smem_addr(smem + C::oQ), p0 = smem_addr(smem + C::oP);
-      int ku = 0, vu = 0, s_tile = 0, o_tile = 0, qs = 0, seg_no = 0;
-      unsigned ku_ph = 0, vu_ph = 0, q_ph = 0;
-      // S^T of the next tile; `fresh`: the first of a segment, `last`: its queries are done with
-      auto issue_s = [&](bool fresh, bool last) {
-        const int buf = s_tile & 1;
-        if (fresh) attn_wait(&sh.q_full[qs], q_ph, dead);
-        attn_wait(&sh.s_empty[buf], ((s_tile >> 1) & 1) ^ 1, dead);
-        const uint32_t q = q0 + qs * C::QB;
+    // ------------------------------------------------ MMA issue (one elected lane)
+    constexpr uint32_t id_s = idesc_f16(NT, false), id_o = idesc_f16(NT, true);
+    // descriptors advance by 16-byte units in their low word
+    const uint64_t q_desc = tc::sdesc_sw128(smem_addr(smem + C::oQ), 16, 1024);
+    const uint64_t p_desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
+    int ku = 0, vu = 0, s_tile = 0, o_tile = 0, qs = 0;
+    unsigned ku_ph = 0, vu_ph = 0, q_ph = 0;
+    for (; next_seg(); ++seg_no) {
 #pragma unroll 1
-        for (int u = 0; u < C::UNITS; ++u) {
-          const bool live = attn_wait(&sh.k_full[ku], ku_ph, dead);
-          tc::fence_after_sync();
-          if (live) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + C::cS + buf * NT, tmem + ku * 32 + k * 8,
-                     tc::sdesc_sw128(q + u * NT * 128 + k * 32, 16, 1024), id_s, u > 0 || k > 0);
-          }
-          tc::mma_commit(&sh.k_empty[ku]);
-          if (++ku == C::KU) ku = 0, ku_ph ^= 1;
-        }
-        tc::mma_commit(&sh.s_full[buf]);
-        if (last) {
-          tc::mma_commit(&sh.q_empty[qs]);
-          if (++qs == C::NQ) qs = 0, q_ph ^= 1;
-        }
-        ++s_tile;
-      };
-      auto issue_o = [&](bool fresh, bool last) {
-        const int buf = o_tile & 1;
-        if (fresh) attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
-        attn_wait(&sh.p_full[buf], (o_tile >> 1) & 1, dead);
-        const uint32_t p = p0 + buf * C::PB;
+      for (int t = s.t0; t <= s.t1; ++t) {
+        if (t < s.t1) {
+          // S^T of tile t
+          const int buf = s_tile & 1;
+          if (t == s.t0) attn_wait(&sh.q_full[qs], q_ph, dead);
+          attn_wait(&sh.s_empty[buf], ((s_tile >> 1) & 1) ^ 1, dead);
+          const uint32_t d = tmem + C::cS + buf * NT;
 #pragma unroll 1
-        for (int r = 0; r < 4; ++r) {
-          const bool live = attn_wait(&sh.v_full[vu], vu_ph, dead);
-          tc::fence_after_sync();
-          if (live) {
+          for (int u = 0; u < C::UNITS; ++u) {
+            const bool live = attn_wait(&sh.k_full[ku], ku_ph, dead);
+            tc::fence_after_sync();
+            const uint64_t b = q_desc + ((qs * C::QB + u * NT * 128) >> 4);
+            const uint32_t ka = tmem + ku * 32;
+            if (elect_one()) {
+              if (live) {
+                mma_ts(d, ka, b, id_s, u > 0);
 #pragma unroll
-            for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_ts(tmem + C::cO + mb * NT, tmem + C::cV + (vu * C::MB + mb) * 16 + k * 8,
-                       tc::sdesc_sw128(p + (r * 2 + k) * 2048, kTile * 128, 1024), id_o,
-                       !(fresh && r == 0 && k == 0));
+                for (int k = 1; k < 4; ++k) mma_ts(d, ka + k * 8, b + k * 2, id_s, 1);
+              }
+              tc::mma_commit(&sh.k_empty[ku]);
+              if (u + 1 == C::UNITS) {
+                tc::mma_commit(&sh.s_full[buf]);
+                if (t + 1 == s.t1) tc::mma_commit(&sh.q_empty[qs]);
+              }
+            }
+            if (++ku == C::KU) ku = 0, ku_ph ^= 1;
           }
-          tc::mma_commit(&sh.v_empty[vu]);
-          if (++vu == C::VU) vu = 0, vu_ph ^= 1;
+          if (t + 1 == s.t1 && ++qs == C::NQ) qs = 0, q_ph ^= 1;
+          ++s_tile;
         }
-        tc::mma_commit(&sh.p_empty[buf]);
-        if (last) tc::mma_commit(&sh.o_full);
-        ++o_tile;
-      };
-      for (; on; on = seg_next(a, s, left), ++seg_no) {
-        issue_s(true, s.t0 + 1 == s.t1);
-        for (int t = s.t0; t < s.t1; ++t) {
-          if (t + 1 < s.t1) issue_s(false, t + 2 == s.t1);
-          issue_o(t == s.t0, t + 1 == s.t1);
+        if (t > s.t0) {
+          // O^T of the tile before
+          const int buf = o_tile & 1;
+          const bool fresh = t - 1 == s.t0;
+          if (fresh) attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
+          attn_wait(&sh.p_full[buf], (o_tile >> 1) & 1, dead);
+          const uint32_t d = tmem + C::cO;
+#pragma unroll 1
+          for (int r = 0; r < 4; ++r) {
+            const bool live = attn_wait(&sh.v_full[vu], vu_ph, dead);
+            tc::fence_after_sync();
+            const uint64_t b = p_desc + ((buf * C::PB + r * 4096) >> 4);
+            const uint32_t va = tmem + C::cV + vu * C::MB * 16;
+            if (elect_one()) {
+              if (live) {
+#pragma unroll
+                for (int mb = 0; mb < C::MB; ++mb) {
+                  mma_ts(d + mb * NT, va + mb * 16, b, id_o, !(fresh && r == 0));
+                  mma_ts(d + mb * NT, va + mb * 16 + 8, b + (2048 >> 4), id_o, 1);
+                }
+              }
+              tc::mma_commit(&sh.v_empty[vu]);
+              if (r == 3) {
+                tc::mma_commit(&sh.p_empty[buf]);
+                if (t == s.t1) tc::mma_commit(&sh.o_full);
+              }
+            }
+            if (++vu == C::VU) vu = 0, vu_ph ^= 1;
+          }
+          ++o_tile;
         }
-      }
-      if (*dead) {  // products in flight end before TMEM is given back
-        tc::mma_commit(&sh.drain);
-        (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
       }
     }
-    __syncwarp();
+    if (*dead) {  // products in flight end before TMEM is given back
+      if (elect_one()) tc::mma_commit(&sh.drain);
+      (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
+    }
   } else if (warp == 17) {
-    // ------------------------------------------------ records in, V scales to binary16
-    Seg f = s;  // the copies run ahead of the conversion
-    int64_t f_left = left;
-    bool f_on = on;
-    int f_t = on ? s.t0 : 0, f_tile = 0, stage_f = 0;
+    // ------------------------------------------------ segments and records in, V scales to binary16
+    const Lens lens = {a, sh.len};
+    Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    Seg f = {};  // the copies run ahead of the conversion
+    int f_t = 0, f_seg = 0, f_tile = 0, f_stage = 0;
+    bool f_on = true;
     unsigned empty_ph = 1;
     auto fetch = [&]() {
-      if (!f_on) return;
-      attn_wait(&sh.raw_empty[stage_f], empty_ph, dead);
-      int ok = 0;
-      const uint8_t* src = nullptr;
-      if (lane < 4) {
-        const int pos = f_t * kTile + lane * kRec;
-        if (pos < f.len) {
-          src = record(a.c, f.b, f.h, pos);
-          if (src == nullptr) report(a.c.status, GDN_ERR_PAGE_RANGE);
-        } else {
-          ok = 1;  // nothing to read: hidden by position
+      if (f_t == f.t1 && f_on) {  // publish the next segment
+        f = attn_seg(a, lens, run);
+        f_t = f.t0;
+        f_on = f.t1 > 0;
+        const int i = f_seg & (kSegs - 1);
+        attn_wait(&sh.seg_empty[i], ((f_seg / kSegs) & 1) ^ 1, dead);
+        if (lane == 0) {
+          sh.seg[i] = f;
+          mbar_arrive(&sh.seg_full[i]);
         }
-        if (src != nullptr) ok = 1;
+        ++f_seg;
       }
-      const unsigned good = __ballot_sync(0xffffffffu, ok != 0) & 15u;
+      if (!f_on) return;
+      attn_wait(&sh.raw_empty[f_stage], empty_ph, dead);
+      const uint8_t* src = nullptr;
+      bool ok = true;  // past the end: nothing to read, hidden by position
+      const int pos = f_t * kTile + lane * kRec;
+      if (lane < 4 && pos < f.len) {
+        src = record(a.c, f.b, f.h, pos);
+        ok = src != nullptr;
+        if (!ok) report(a.c.status, GDN_ERR_PAGE_RANGE);
+      }
+      const unsigned good = __ballot_sync(0xffffffffu, ok) & 15u;
       const unsigned copies = __ballot_sync(0xffffffffu, src != nullptr);
       if (lane == 0) {
         sh.tile_ok[f_tile & 7] = (int)good;
-        mbar_arrive_expect_tx(&sh.raw_full[stage_f], __popc(copies) * rec_bytes(D));
+        mbar_arrive_expect_tx(&sh.raw_full[f_stage], __popc(copies) * rec_bytes(D));
       }
       __syncwarp();
       if (src != nullptr)
-        bulk_g2s(smem + C::oRaw + stage_f * C::RAW + lane * rec_bytes(D), src, rec_bytes(D),
-                 &sh.raw_full[stage_f]);
-      if (++stage_f == C::NRAW) stage_f = 0, empty_ph ^= 1;
+        bulk_g2s(smem + C::oRaw + f_stage * C::RAW + lane * rec_bytes(D), src, rec_bytes(D),
+                 &sh.raw_full[f_stage]);
+      if (++f_stage == C::NRAW) f_stage = 0, empty_ph ^= 1;
       ++f_tile;
-      if (++f_t == f.t1) {
-        f_on = seg_next(a, f, f_left);
-        f_t = f.t0;
-      }
+      ++f_t;
     };
-    for (int i = 0; i < C::NRAW; ++i) fetch();
-    // a stage is filled again one tile later, so that the conversion of the next
-    // tile does not wait for the readers of this one
-    int stage = 0, vb = 0, tile = 0;
+    // the conversion follows the copies NRAW - 2 tiles behind, so that it does not
+    // wait for the readers of the tile before it
+    int stage = 0, vb = 0, tile = 0, t = 0;
     unsigned raw_ph = 0, vs_ph = 1;
-    for (; on; on = seg_next(a, s, left)) {
-      for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        attn_wait(&sh.raw_full[stage], raw_ph, dead);
-        attn_wait(&sh.vs_empty[vb], vs_ph, dead);
-        const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
-        uint8_t* vs = smem + C::oVS + vb * C::VSB;
-        const int ok = sh.tile_ok[tile & 7];
-        // 8 scales of a group a step; positions past the end count as 0
-#pragma unroll 4
-        for (int i = lane; i < 4 * (D / 16) * 4; i += 32) {
-          const int r = i / (D / 4), g = (i / 4) % (D / 16), o = i & 3;
-          const uint2 s8 = *reinterpret_cast<const uint2*>(raw + r * rec_bytes(D) + off_vs(D) +
-                                                           g * kRec + o * 8);
-          uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
-          int n = s.len - (t * kTile + r * kRec + o * 8);  // positions that exist
-          if (!((ok >> r) & 1)) n = 0;
-          if (n < 8) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = n >= 2 * j + 2 ? w[j] : n == 2 * j + 1 ? (w[j] & 0xffffu) : 0u;
-          }
-          *reinterpret_cast<uint4*>(vs + g * C::VSG + r * 64 + o * 16) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.vs_full[vb]), mbar_arrive(&sh.raw_empty[stage]);
-        if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
-        if (++vb == 2) vb = 0, vs_ph ^= 1;
-        if (tile > 0) fetch();
+    const Seg* c = nullptr;
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      fetch();
+      if (k < C::NRAW - 2) continue;
+      if (tile == f_tile) break;
+      if (c == nullptr || t == c->t1) {  // the segment of this tile
+        c = &sh.seg[seg_no++ & (kSegs - 1)];
+        t = c->t0;
       }
+      attn_wait(&sh.raw_full[stage], raw_ph, dead);
+      attn_wait(&sh.vs_empty[vb], vs_ph, dead);
+      const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
+      uint8_t* vs = smem + C::oVS + vb * C::VSB;
+      const int ok = sh.tile_ok[tile & 7];
+      const int end = c->len - t * kTile;
+      // 8 scales of a group a step; positions past the end count as 0
+#pragma unroll 2
+      for (int i = lane; i < 4 * (D / 16) * 4; i += 32) {
+        const int r = i / (D / 4), g = (i / 4) % (D / 16), o = i & 3;
+        const uint2 s8 = *reinterpret_cast<const uint2*>(raw + r * rec_bytes(D) + off_vs(D) +
+                                                         g * kRec + o * 8);
+        uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
+        const int n = (ok >> r) & 1 ? end - (r * kRec + o * 8) : 0;  // positions that exist
+        if (n < 8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = n >= 2 * j + 2 ? w[j] : n == 2 * j + 1 ? (w[j] & 0xffffu) : 0u;
+        }
+        *reinterpret_cast<uint4*>(vs + g * C::VSG + r * 64 + o * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.vs_full[vb]), mbar_arrive(&sh.raw_empty[stage]);
+      if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
+      if (++vb == 2) vb = 0, vs_ph ^= 1;
+      ++t;
+      ++tile;
     }
     if (*dead) {  // copies in flight land before the block's memory is given back
       for (int i = 0; i < C::NRAW && i < f_tile; ++i)
@@ -841,86 +980,79 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     }
   } else {
     // ------------------------------------------------ queries
+    // Copied as they are to where the operand goes, then each lane turns its own
+    // channels into binary16 in place.
     constexpr int E = D / 32;   // channels of a lane
     const int half = warp - 18;
-    int qb = 0, seg_no = 0;
+    int qb = 0;
     unsigned ph = 1;
-    for (; on; on = seg_next(a, s, left), ++seg_no) {
+    for (; next_seg(); ++seg_no) {
       attn_wait(&sh.q_empty[qb], ph, dead);
       attn_wait(&sh.row_empty[seg_no & 1], ((seg_no >> 1) & 1) ^ 1, dead);
       const float ks = a.c.k_scale != nullptr ? a.c.k_scale[s.h] : 1.f;
-      uint8_t* q = smem + C::oQ + qb * C::QB;
-      const int row0 = s.rt * a.rows_per_tile;
-      constexpr int BATCH = 8;
-      for (int r0 = half; r0 < NT; r0 += 2 * BATCH) {
-        uint32_t x[BATCH][E / 2];
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          const int r = r0 + 2 * j;
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) x[j][i] = 0;
-          if (r < s.rows) {
-            const int n = (row0 + r) / a.G, g = (row0 + r) % a.G;
-            const uint16_t* src = static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b +
-                                  n * a.q_stride_n + (int64_t)(s.h * a.G + g) * D + lane * E;
-            if constexpr (E == 8) {
-              const uint4 v = ld_nc_u4(src);
-              x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
-            } else if constexpr (E == 4) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-              x[j][0] = v.x, x[j][1] = v.y;
-            } else {
-              x[j][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-          }
+      const int ch = lane * E;
+      uint8_t* q = smem + C::oQ + qb * C::QB + (ch >> 6) * (NT * 128) + (ch & 7) * 2;
+      const uint16_t* src0 =
+          static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
+      int n = (s.row0 + half) / a.G, g = (s.row0 + half) % a.G;
+      const int n0 = n, g0 = g;
+#pragma unroll 1
+      for (int r = half; r < NT; r += 2) {
+        uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
+        if (r < s.rows) {
+          const uint16_t* src = src0 + n * a.q_stride_n + (int64_t)g * D;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)), "l"(src),
+                       "n"(E * 2)
+                       : "memory");
+        } else if constexpr (E == 8) {
+          *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+        } else if constexpr (E == 4) {
+          *reinterpret_cast<uint2*>(at) = make_uint2(0, 0);
+        } else {
+          *reinterpret_cast<uint32_t*>(at) = 0;
         }
+        for (g += 2; g >= a.G; g -= a.G) ++n;
+      }
+      cp_async_wait_all();
+      n = n0, g = g0;
+#pragma unroll 1
+      for (int r = half; r < NT; r += 2) {
+        uint32_t* at =
+            reinterpret_cast<uint32_t*>(q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4));
+        float f[E];
+        unsigned big = 0;
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          const int r = r0 + 2 * j;
-          if (r >= NT) break;
-          float f[E];
-          unsigned big = 0;
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            if (a.bf16) {
-              f[2 * i] = __uint_as_float(x[j][i] << 16);
-              f[2 * i + 1] = __uint_as_float(x[j][i] & 0xffff0000u);
-            } else {
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[j][i]));
-              f[2 * i] = v.x;
-              f[2 * i + 1] = v.y;
-            }
-            big = max(big, max(__float_as_uint(f[2 * i]) & 0x7fffffffu,
-                               __float_as_uint(f[2 * i + 1]) & 0x7fffffffu));
+        for (int i = 0; i < E / 2; ++i) {
+          const uint32_t x = at[i];
+          if (a.bf16) {
+            f[2 * i] = __uint_as_float(x << 16);
+            f[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
+          } else {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
           }
-          big = __reduce_max_sync(0xffffffffu, big) >> 23;
-          // the row's largest magnitude to [2^8, 2^9); not for zeros, infinities and NaN
-          const unsigned up = big == 0 || big == 255 ? 127u : min(262u - big, 252u);
-          const float mul = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
-          uint32_t w[E / 2];
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) w[i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
-          const int ch = lane * E;
-          uint8_t* at = q + (ch >> 6) * (NT * 128) + r * 128 +
-                        ((((ch & 63) >> 3) ^ (r & 7)) << 4) + (ch & 7) * 2;
-          if constexpr (E == 8) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-          else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-          else *reinterpret_cast<uint32_t*>(at) = w[0];
-          if (lane == 0) {
-            Row info = {a.scale * back * (ks * kLog2e), 0.f, 0, 0};
-            const int n = r < s.rows ? (row0 + r) / a.G : 0;
-            if (a.parent == nullptr) {
-              info.lo = n;
-            } else {
-              unsigned long long seen = 0;
-              const int32_t* p = a.parent + (int64_t)s.b * a.N;
-              for (int m = n; m >= 0; m = p[m]) seen |= 1ull << m;
-              info.lo = (unsigned)seen;
-              info.hi = (unsigned)(seen >> 32);
-            }
-            sh.row[seg_no & 1][r] = info;
-          }
+          big = max(big, max(__float_as_uint(f[2 * i]) & 0x7fffffffu,
+                             __float_as_uint(f[2 * i + 1]) & 0x7fffffffu));
         }
+        big = __reduce_max_sync(0xffffffffu, big) >> 23;
+        // the row's largest magnitude to [2^8, 2^9); not for zeros, infinities and NaN
+        const unsigned up = big == 0 || big == 255 ? 127u : min(262u - big, 252u);
+        const float mul = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) at[i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
+        if (lane == 0) {
+          Row info = {a.scale * back * (ks * kLog2e), n * a.Hq + g, 0, 0};
+          if (a.parent != nullptr && r < s.rows) {
+            const int32_t* p = a.parent + (int64_t)s.b * a.N;
+            unsigned long long seen = 0;
+            for (int m = n; m >= 0; m = p[m]) seen |= 1ull << m;
+            info.lo = (unsigned)seen;
+            info.hi = (unsigned)(seen >> 32);
+          }
+          sh.row[seg_no & 1][r] = info;
+        }
+        for (g += 2; g >= a.G; g -= a.G) ++n;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -940,87 +1072,76 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- join
-// One block per item: nothing for an item that one block wrote whole, zeros for
-// one that sees nothing, else the parts' sum in block order.
-constexpr int kJoinWarps = 8;
+// Grid (blocks of the main kernel, rows): the item that block x left unfinished,
+// if any, row by row: the parts of blocks x .. last, in that order.  A thread
+// has four channels of every NP-th part.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 16;      // grid rows; more rows are taken in turn
+constexpr int kJoinParts = 1024;   // parts kept in shared memory: as many blocks at most
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-join_kernel(const __grid_constant__ AttnArgs a, int NT, int parts) {
-  __shared__ int64_t red[kJoinWarps][2];
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(const __grid_constant__ AttnArgs a, int NT) {
+  constexpr int Q = D / 4, NP = kJoinThreads / Q;
+  __shared__ float weight[kJoinParts];
+  __shared__ float red[kJoinThreads / 32][2];
+  __shared__ __align__(16) float acc[NP][D];
   pdl_enter();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int item = blockIdx.x;
-  const int rt = item % a.row_tiles;
-  item /= a.row_tiles;
-  const int h = item % a.c.Hkv, b = item / a.c.Hkv;
-  int64_t total = 0, before = 0;
-  for (int i = threadIdx.x; i < a.c.B; i += kJoinWarps * 32) {
-    const int64_t x = attn_cost(a, attn_len(a, i, false));
-    total += x;
-    if (i < b) before += x;
-  }
+  const AttnJoin j = a.join[blockIdx.x];
+  const int parts = j.rows > 0 ? j.last - (int)blockIdx.x + 1 : 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quad = threadIdx.x % Q, group = threadIdx.x / Q;
+  auto slot = [&](int i) { return i == 0 ? (int64_t)j.slot : 2 * ((int64_t)blockIdx.x + i); };
+  const float vsc = a.c.v_scale != nullptr ? a.c.v_scale[j.h] : 1.f;
+#pragma unroll 1
+  for (int r = blockIdx.y; r < j.rows; r += kJoinRows) {
+    float top = kNone;
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+      const float m = a.part_ml[slot(i) * NT + r].x;
+      top = m > top || m != m ? m : top;
+    }
+    top = warp_max(top);
+    if (lane == 0) red[warp][0] = top;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      const float m = red[w][0];
+      top = m > top || m != m ? m : top;
+    }
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+      const float2 ml = a.part_ml[slot(i) * NT + r];
+      const float w = exp2_fast(ml.x - top);
+      weight[i] = w;
+      sum += w * ml.y;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) red[warp][0] = total, red[warp][1] = before;
-  __syncthreads();
-  total = before = 0;
-  for (int w = 0; w < kJoinWarps; ++w) total += red[w][0], before += red[w][1];
-  if (parts > total) parts = (int)total;
-  const int len = attn_len(a, b, false);
-  int64_t per_head = 0;
-  for (int i = 0; i < a.row_tiles; ++i) {
-    const int t = attn_tiles(a, len, i);
-    if (i < rt) before += t;
-    per_head += t;
-  }
-  before += h * per_head;
-  Seg s = {};
-  s.rt = rt;
-  seg_rows(a, s);
-  const int tiles = attn_tiles(a, len, rt), row0 = rt * a.rows_per_tile;
-  int first = 0, last = 0;
-  if (tiles > 0) {
-    // the blocks that hold the item's first and last tile
-    first = (int)(((before + 1) * parts + total - 1) / total) - 1;
-    last = (int)(((before + tiles) * parts + total - 1) / total) - 1;
-    if (first == last) return;
-  }
-  const float vsc = a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.f;
-  for (int r = warp; r < s.rows; r += kJoinWarps) {
-    float acc[D / 32] = {}, sum = 0.f, top = kNone;
-    if (tiles > 0) {
-      for (int c = first + lane; c <= last; c += 32) {
-        const int64_t slot = 2 * (int64_t)c + (total * c / parts < before);
-        const float m = a.part_ml[slot * NT + r].x;
-        top = m > top || m != m ? m : top;
-      }
-      top = warp_max(top);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[warp][1] = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) sum += red[w][1];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int c = first; c <= last; ++c) {
-        const int64_t slot = 2 * (int64_t)c + (total * c / parts < before);
-        const float2 ml = a.part_ml[slot * NT + r];
-        const float w = exp2_fast(ml.x - top);
-        sum += w * ml.y;
-        const float* p = a.part_o + (slot * NT + r) * D + lane;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] += w * p[i * 32];
-      }
+    for (int i = group; i < parts; i += NP) {
+      const float4 p =
+          __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * NT + r) * D) + quad);
+      const float w = weight[i];
+      o.x += w * p.x, o.y += w * p.y, o.z += w * p.z, o.w += w * p.w;
     }
-    const int n = (row0 + r) / a.G, g = (row0 + r) % a.G;
-    const int64_t at = ((int64_t)b * a.N + n) * a.Hq + h * a.G + g;
-    const float inv = sum != 0.f ? vsc / sum : 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float o = acc[i] * inv;
-      static_cast<uint16_t*>(a.o)[at * D + i * 32 + lane] =
-          a.bf16 ? Elem<GDN_BF16>::from(o) : Elem<GDN_F16>::from(o);
+    *reinterpret_cast<float4*>(&acc[group][quad * 4]) = o;
+    __syncthreads();
+    const int row = j.row0 + r;
+    const int64_t at = j.item + (int64_t)(row / a.G) * a.Hq + row % a.G;
+    if (threadIdx.x < D) {
+      float x = 0.f;
+      for (int g = 0; g < NP; ++g) x += acc[g][threadIdx.x];
+      x *= sum != 0.f ? vsc / sum : 0.f;
+      static_cast<uint16_t*>(a.o)[at * D + threadIdx.x] =
+          a.bf16 ? Elem<GDN_BF16>::from(x) : Elem<GDN_F16>::from(x);
+      if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
-    if (a.lse != nullptr && lane == 0)
-      a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    __syncthreads();
   }
 }
 
@@ -1034,8 +1155,8 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
   }
   const int rc = launch_pdl(attn_kernel<D, NT>, dim3(parts), dim3(kAttnThreads), C::SMEM, s, a);
   if (rc != GDN_OK) return rc;
-  return launch_pdl(join_kernel<D>, dim3(a.c.B * a.c.Hkv * a.row_tiles), dim3(kJoinWarps * 32), 0,
-                    s, a, NT, parts);
+  return launch_pdl(join_kernel<D>, dim3(parts, min(NT, kJoinRows)), dim3(kJoinThreads), 0, s, a,
+                    NT);
 }
 
 template <int D>

@@ -9,6 +9,13 @@
 namespace gdn {
 namespace kv4 {
 
+// An item whose tiles end in a later block: what its first block leaves to the join.
+struct AttnJoin {
+  int64_t item;          // output row of its first node and head
+  int h, row0, rows;     // rows = 0: nothing to join
+  int slot, last;        // of its own part; block with the last part
+};
+
 struct AttnArgs {
   gdn_kv4_cache c;
   const void* q;
@@ -18,16 +25,11 @@ struct AttnArgs {
   float* lse;
   float* part_o;    // [2 per block][rows][D]
   float2* part_ml;  // [2 per block][rows]: reference and sum
+  AttnJoin* join;   // [blocks]
   float scale;
   int N, Hq, G;     // G: query heads of a kv head
   int rows_total, rows_per_tile, row_tiles;
   int bf16;
-};
-
-// A block's run of tiles.
-struct AttnSpan {
-  int64_t count;
-  int b, h, rt, t0;  // the item and tile that it begins with
 };
 
 int attn_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
