@@ -24,8 +24,9 @@
 //   4-7    V: channel = TMEM lane; the same for V^T (32 positions a unit)
 //   8-15   softmax, two groups of four, each half of the rows: S^T from TMEM, p to
 //          shared memory (B operand), sums in registers, and the item's epilogue
-//   16     issues the MMAs        17   bulk copies of records, V scales to binary16
-//   18-19  query rows: to binary16, scaled by a power of two per row so that
+//   16     issues S^T's MMAs      19   issues O^T's
+//   17     the run's segments, bulk copies of records, V scales to binary16
+//   18     query rows: to binary16, scaled by a power of two per row so that
 //          any bf16 magnitude fits, into the B operand's swizzled layout
 //
 // The reference m is moved only when some p would pass 2^8 (p is at most 65504
@@ -466,13 +467,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_empty[i], 8);
       mbar_init(&sh.p_full[i], 8), mbar_init(&sh.p_empty[i], 1);
       mbar_init(&sh.vs_full[i], 1), mbar_init(&sh.vs_empty[i], 4);
-      mbar_init(&sh.row_full[i], 2), mbar_init(&sh.row_empty[i], 8);
+      mbar_init(&sh.row_full[i], 1), mbar_init(&sh.row_empty[i], 8);
     }
-    for (int i = 0; i < C::NQ; ++i) mbar_init(&sh.q_full[i], 2), mbar_init(&sh.q_empty[i], 1);
+    for (int i = 0; i < C::NQ; ++i) mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 19);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.o_empty, 8);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.dead = 0;
     mbar_init_fence();
   }
@@ -482,7 +483,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem;
+  // all 512 columns are this block's, so its tensor memory begins at address 0
+  if (sh.tmem != 0) *dead = 1;
+  constexpr uint32_t tmem = 0;
 
   // every warp but 17 takes the run's segments from the ring
   int seg_no = 0;
@@ -810,81 +813,80 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     }
     if (threadIdx.x == 256) a.join[blockIdx.x] = join;
   } else if (warp == 16) {
-    // ------------------------------------------------ MMA issue (one elected lane)
-    constexpr uint32_t id_s = idesc_f16(NT, false), id_o = idesc_f16(NT, true);
+    // ------------------------------------------------ S^T products (one elected lane)
+    constexpr uint32_t id = idesc_f16(NT, false);
     // descriptors advance by 16-byte units in their low word
-    const uint64_t q_desc = tc::sdesc_sw128(smem_addr(smem + C::oQ), 16, 1024);
-    const uint64_t p_desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
-    int ku = 0, vu = 0, s_tile = 0, o_tile = 0, qs = 0;
-    unsigned ku_ph = 0, vu_ph = 0, q_ph = 0;
+    const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oQ), 16, 1024);
+    int tile = 0, qs = 0, ku = 0;
+    unsigned ku_ph = 0, q_ph = 0;
     for (; next_seg(); ++seg_no) {
+      attn_wait(&sh.q_full[qs], q_ph, dead);
+      const uint64_t q = desc + (uint32_t)(qs * (C::QB >> 4));
 #pragma unroll 1
-      for (int t = s.t0; t <= s.t1; ++t) {
-        if (t < s.t1) {
-          // S^T of tile t
-          const int buf = s_tile & 1;
-          if (t == s.t0) attn_wait(&sh.q_full[qs], q_ph, dead);
-          attn_wait(&sh.s_empty[buf], ((s_tile >> 1) & 1) ^ 1, dead);
-          const uint32_t d = tmem + C::cS + buf * NT;
-#pragma unroll 1
-          for (int u = 0; u < C::UNITS; ++u) {
-            const bool live = attn_wait(&sh.k_full[ku], ku_ph, dead);
-            tc::fence_after_sync();
-            const uint64_t b = q_desc + ((qs * C::QB + u * NT * 128) >> 4);
-            const uint32_t ka = tmem + ku * 32;
-            if (elect_one()) {
-              if (live) {
-                mma_ts(d, ka, b, id_s, u > 0);
+      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+        const int buf = tile & 1;
+        attn_wait(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1, dead);
+        const uint32_t d = C::cS + buf * NT;
 #pragma unroll
-                for (int k = 1; k < 4; ++k) mma_ts(d, ka + k * 8, b + k * 2, id_s, 1);
-              }
-              tc::mma_commit(&sh.k_empty[ku]);
-              if (u + 1 == C::UNITS) {
-                tc::mma_commit(&sh.s_full[buf]);
-                if (t + 1 == s.t1) tc::mma_commit(&sh.q_empty[qs]);
-              }
+        for (int u = 0; u < C::UNITS; ++u) {
+          const int k0 = C::UNITS >= C::KU ? u % C::KU : ku + u;
+          const bool live = attn_wait(&sh.k_full[k0], ku_ph ^ (C::UNITS > C::KU && u >= C::KU), dead);
+          tc::fence_after_sync();
+          if (elect_one() && live) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(d, k0 * 32 + k * 8, q + (u * NT * 128 + k * 32) / 16, id, u > 0 || k > 0);
+            tc::mma_commit(&sh.k_empty[k0]);
+            if (u + 1 == C::UNITS) {
+              tc::mma_commit(&sh.s_full[buf]);
+              if (t + 1 == s.t1) tc::mma_commit(&sh.q_empty[qs]);
             }
-            if (++ku == C::KU) ku = 0, ku_ph ^= 1;
           }
-          if (t + 1 == s.t1 && ++qs == C::NQ) qs = 0, q_ph ^= 1;
-          ++s_tile;
         }
-        if (t > s.t0) {
-          // O^T of the tile before
-          const int buf = o_tile & 1;
-          const bool fresh = t - 1 == s.t0;
-          if (fresh) attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
-          attn_wait(&sh.p_full[buf], (o_tile >> 1) & 1, dead);
-          const uint32_t d = tmem + C::cO;
-#pragma unroll 1
-          for (int r = 0; r < 4; ++r) {
-            const bool live = attn_wait(&sh.v_full[vu], vu_ph, dead);
-            tc::fence_after_sync();
-            const uint64_t b = p_desc + ((buf * C::PB + r * 4096) >> 4);
-            const uint32_t va = tmem + C::cV + vu * C::MB * 16;
-            if (elect_one()) {
-              if (live) {
-#pragma unroll
-                for (int mb = 0; mb < C::MB; ++mb) {
-                  mma_ts(d + mb * NT, va + mb * 16, b, id_o, !(fresh && r == 0));
-                  mma_ts(d + mb * NT, va + mb * 16 + 8, b + (2048 >> 4), id_o, 1);
-                }
-              }
-              tc::mma_commit(&sh.v_empty[vu]);
-              if (r == 3) {
-                tc::mma_commit(&sh.p_empty[buf]);
-                if (t == s.t1) tc::mma_commit(&sh.o_full);
-              }
-            }
-            if (++vu == C::VU) vu = 0, vu_ph ^= 1;
-          }
-          ++o_tile;
+        if (C::UNITS < C::KU) {
+          ku += C::UNITS;
+          if (ku == C::KU) ku = 0, ku_ph ^= 1;
+        } else if ((C::UNITS / C::KU) & 1) {
+          ku_ph ^= 1;
         }
       }
+      if (++qs == C::NQ) qs = 0, q_ph ^= 1;
     }
-    if (*dead) {  // products in flight end before TMEM is given back
-      if (elect_one()) tc::mma_commit(&sh.drain);
-      (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
+  } else if (warp == 19) {
+    // ------------------------------------------------ O^T products (one elected lane)
+    constexpr uint32_t id = idesc_f16(NT, true);
+    const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
+    int tile = 0;
+    unsigned vu_ph = 0;
+    for (; next_seg(); ++seg_no) {
+      attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
+#pragma unroll 1
+      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+        const int buf = tile & 1;
+        attn_wait(&sh.p_full[buf], (tile >> 1) & 1, dead);
+        const uint64_t p = desc + (uint32_t)(buf * (C::PB >> 4));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          constexpr int VU = C::VU;
+          const int vu = r % VU;
+          const bool live = attn_wait(&sh.v_full[vu], vu_ph ^ (r >= VU), dead);
+          tc::fence_after_sync();
+          if (elect_one() && live) {
+#pragma unroll
+            for (int mb = 0; mb < C::MB; ++mb) {
+              const uint32_t d = C::cO + mb * NT, va = C::cV + (vu * C::MB + mb) * 16;
+              mma_ts(d, va, p + r * 256, id, t > s.t0 || r > 0);
+              mma_ts(d, va + 8, p + r * 256 + 128, id, 1);
+            }
+            tc::mma_commit(&sh.v_empty[vu]);
+            if (r == 3) {
+              tc::mma_commit(&sh.p_empty[buf]);
+              if (t + 1 == s.t1) tc::mma_commit(&sh.o_full);
+            }
+          }
+        }
+        if ((4 / C::VU) & 1) vu_ph ^= 1;
+      }
     }
   } else if (warp == 17) {
     // ------------------------------------------------ segments and records in, V scales to binary16
@@ -983,7 +985,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     // Copied as they are to where the operand goes, then each lane turns its own
     // channels into binary16 in place.
     constexpr int E = D / 32;   // channels of a lane
-    const int half = warp - 18;
     int qb = 0;
     unsigned ph = 1;
     for (; next_seg(); ++seg_no) {
@@ -994,10 +995,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       uint8_t* q = smem + C::oQ + qb * C::QB + (ch >> 6) * (NT * 128) + (ch & 7) * 2;
       const uint16_t* src0 =
           static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
-      int n = (s.row0 + half) / a.G, g = (s.row0 + half) % a.G;
+      int n = s.row0 / a.G, g = s.row0 % a.G;
       const int n0 = n, g0 = g;
 #pragma unroll 1
-      for (int r = half; r < NT; r += 2) {
+      for (int r = 0; r < NT; ++r) {
         uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
         if (r < s.rows) {
           const uint16_t* src = src0 + n * a.q_stride_n + (int64_t)g * D;
@@ -1011,12 +1012,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         } else {
           *reinterpret_cast<uint32_t*>(at) = 0;
         }
-        for (g += 2; g >= a.G; g -= a.G) ++n;
+        if (++g == a.G) g = 0, ++n;
       }
       cp_async_wait_all();
       n = n0, g = g0;
 #pragma unroll 1
-      for (int r = half; r < NT; r += 2) {
+      for (int r = 0; r < NT; ++r) {
         uint32_t* at =
             reinterpret_cast<uint32_t*>(q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4));
         float f[E];
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           }
           sh.row[seg_no & 1][r] = info;
         }
-        for (g += 2; g >= a.G; g -= a.G) ++n;
+        if (++g == a.G) g = 0, ++n;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1060,14 +1061,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       if (++qb == C::NQ) qb = 0, ph ^= 1;
     }
   }
-  // every role is done with its loops, hence (bounded) with its copies and products
+  // every role is done with its loops, hence with its copies and products; after a
+  // wait that ran out, products in flight end (bounded) before TMEM is given back
+  if ((warp == 16 || warp == 19) && __any_sync(0xffffffffu, *dead)) {
+    if (elect_one()) tc::mma_commit(&sh.drain);
+    (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *dead) report(a.c.status, GDN_ERR_TIMEOUT);
   if (warp == 16) {
     tc::fence_after_sync();
     tc::tmem_relinquish();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(sh.tmem, 512);
   }
 }
 
