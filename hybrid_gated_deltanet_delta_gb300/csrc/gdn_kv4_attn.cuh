@@ -19,15 +19,16 @@
 // starts or ends inside an item writes that part's O, m and l to the workspace,
 // and join_kernel adds the parts in block order; whole items are written at once.
 //
-// Warps of a block (20), connected by mbarriers only:
-//   0-3    K: position = TMEM lane; codes * scale -> binary16 -> TMEM (64 channels a unit)
-//   4-7    V: channel = TMEM lane; the same for V^T (32 positions a unit)
-//   8-15   softmax, two groups of four, each half of the rows: S^T from TMEM, p to
-//          shared memory (B operand), sums in registers, and the item's epilogue
-//   16     issues S^T's MMAs      19   issues O^T's
-//   17     the run's segments, bulk copies of records, V scales to binary16
-//   18     query rows: to binary16, scaled by a power of two per row so that
-//          any bf16 magnitude fits, into the B operand's swizzled layout
+// Warps of a block (24, in groups of four), connected by mbarriers only:
+//   K groups   position = TMEM lane; codes * scale -> binary16 -> TMEM (64 channels a unit)
+//   V groups   channel = TMEM lane; the same for V^T (32 positions a unit)
+//   softmax groups, 32 rows each: S^T from TMEM, p to shared memory (B operand),
+//              sums in registers, and the item's epilogue
+//   and a warp each that issues S^T's products, issues O^T's, turns queries into
+//   the B operand (binary16, scaled by a power of two per row so that any bf16
+//   magnitude fits), and walks the run: segments, bulk copies of the records.
+// Few rows leave the time to the 4-bit operand, many to the softmax, so up to 32
+// rows two groups each dequantise K and V, and 96 rows take three softmax groups.
 //
 // The reference m is moved only when some p would pass 2^8 (p is at most 65504
 // in binary16): the sums and O^T are then multiplied by 2^(old - new), which
@@ -49,9 +50,9 @@ namespace gdn {
 namespace kv4 {
 
 constexpr int kTile = 128;  // positions of a tile: four records
-constexpr int kAttnThreads = 640;
+constexpr int kAttnThreads = 768;
 constexpr float kNone = -1e30f;      // reference of a row that has seen nothing
-constexpr float kSlack = 8.f;        // log2 of the largest p before m moves
+constexpr unsigned kMostP = 0x5c00;  // 2^8 in binary16: the largest p before m moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaitPolls = 1 << 20;  // bound of every wait
 
@@ -59,7 +60,12 @@ template <int D_, int NT_>
 struct AttnCfg {
   static constexpr int D = D_, NT = NT_;
   static constexpr int MB = D == 256 ? 2 : 1;  // 128-channel blocks of O^T
-  static constexpr int NH = NT / 2;            // rows of a softmax group
+  static constexpr int NS = NT < 64 ? 1 : NT / 32;  // softmax groups
+  static constexpr int NH = NT / NS;                // rows of one
+  static constexpr int NK = NT < 96 ? 2 : 1;        // groups that dequantise K, and V
+  static constexpr int NV = 5 - NS - NK;
+  static constexpr int wV = 4 * NK, wS = wV + 4 * NV;  // first warps of the roles
+  static_assert(NV >= 1 && wS + 4 * NS == 20, "warps");
   static constexpr int UNITS = D / 64;         // K units of a tile
   // TMEM columns: K ring, two S^T, O^T, V ring.  The widest case keeps two
   // stages per ring so that S^T can be double buffered.
@@ -73,8 +79,7 @@ struct AttnCfg {
   static constexpr int PB = (NT > 64 ? 2 : 1) * kTile * 128;
   static constexpr int VSG = 272;  // bytes between the scale rows of two groups (bank offset)
   static constexpr int VSB = D / 16 * VSG;
-  static constexpr int LS = NT * 129 * 4;  // row sums of every lane, over the P buffers
-  static constexpr int P2 = 2 * PB > LS ? 2 * PB : (LS + 1023) / 1024 * 1024;
+  static constexpr int P2 = 2 * PB;
   static constexpr int ROOM = 224 * 1024 - P2 - 2 * VSB - 4096;
   static constexpr int NQ = ROOM - 2 * QB >= 2 * RAW ? 2 : 1;
   static constexpr int NRAW = (ROOM - NQ * QB) / RAW > 4 ? 4 : (ROOM - NQ * QB) / RAW;
@@ -82,12 +87,6 @@ struct AttnCfg {
   static constexpr int oQ = 0, oP = oQ + NQ * QB, oRaw = oP + P2, oVS = oRaw + NRAW * RAW;
   static constexpr int oEnd = oVS + 2 * VSB;
   static constexpr int SMEM = oEnd + 1024;  // + alignment of the swizzled operands
-};
-
-struct Row {       // of a query row, beside its operand
-  float c;         // logit of S: c * S (log2 units)
-  int at;          // row of the output, from the item's first node and head on
-  unsigned lo, hi; // trees: the positions of the block that the row sees
 };
 
 // The part of one item that a block works on: tiles [t0, t1) of `tiles` (t1 = 0: the end).
@@ -103,17 +102,23 @@ template <typename C>
 struct AttnShared {
   uint64_t raw_full[C::NRAW], raw_empty[C::NRAW];
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
-  uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], vs_full[2], vs_empty[2];
+  uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
   uint64_t q_full[C::NQ], q_empty[C::NQ], row_full[2], row_empty[2], o_full, o_empty, drain;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int dead;
   int tile_ok[8];  // records of a tile that could be read, by tile number
-  alignas(16) float2 cm[C::NT];  // (c, m) of the rows in work; read two rows a load
-  alignas(16) Seg seg[kSegs];
-  alignas(16) Row row[2][C::NT];
-  float alpha[C::NT], inv[C::NT];
-  float wmax[4][C::NT];
+  Seg seg[kSegs];
+  // of the query rows, by segment: c (logit of S: c * S, log2 units), the row of
+  // the output from the item's first node and head on, and for trees the
+  // positions of the block that the row sees
+  alignas(16) float row_c[2][C::NT];
+  alignas(16) int row_at[2][C::NT];
+  uint2 row_path[2][C::NT];
+  uint2 path[64];                   // of each node
+  alignas(16) float4 cm[C::NT / 2]; // rows in work, by pairs: c, c, -m, -m
+  alignas(16) float alpha[C::NT], inv[C::NT];
+  float part[4][C::NT];             // of a softmax group's four warps
   int len[kLens];
 };
 
@@ -170,13 +175,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16, "columns");
-  if constexpr (N == 8) tc::tmem_ld8(addr, r);
-  else tc::tmem_ld16(addr, r);
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -213,6 +211,47 @@ __device__ __forceinline__ uint32_t pack_f16x2(float first, float second) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(second), "f"(first));
   return d;
+}
+
+// Pairs of fp32 values in one instruction.
+union Pair {
+  unsigned long long u;
+  float2 f;
+};
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  Pair x, y, z;
+  x.f = a, y.f = b, z.f = c;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return z.f;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  Pair x, y;
+  x.f = a, y.f = b;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x.u) : "l"(x.u), "l"(y.u));
+  return x.f;
+}
+
+// Reduces N values (16 or 32) over the warp's lanes: lane i ends with value
+// i % N's result.  Each step halves the values that a lane still carries.
+template <int N, typename Op>
+__device__ __forceinline__ float warp_transpose_reduce(float (&v)[N], Op op) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (N == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
+  }
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = upper ? v[i + o] : v[i], give = upper ? v[i] : v[i + o];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  return v[0];
 }
 
 // 8 codes (one word) times the scale pair(s): four f16x2 words.
@@ -449,6 +488,121 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& len
   }
 }
 
+// ---------------------------------------------------------------- queries
+// Query rows of segment s into the B operand at q, and what goes with them into
+// buffer `rb`: four rows at a time, quads `first`, first + step, ... of a warp.
+// The rows are copied as they are to where the operand goes, then each lane
+// turns its own channels into binary16 in place.
+template <int D, int NT>
+static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
+                                              const Seg& s, uint8_t* q, int rb, int first,
+                                              int step) {
+  constexpr int E = D / 32;  // channels of a lane
+  const int lane = threadIdx.x & 31, ch = lane * E;
+  q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
+  auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
+  const uint16_t* src0 =
+      static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
+#pragma unroll 1
+  for (int r0 = first * 4; r0 < NT; r0 += step * 4) {
+    int n = (s.row0 + r0) / a.G, g = (s.row0 + r0) % a.G;
+#pragma unroll 1
+    for (int r = r0; r < r0 + 4; ++r) {
+      uint8_t* at = place(r);
+      if (r < s.rows) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)),
+                     "l"(src0 + n * a.q_stride_n + (int64_t)g * D), "n"(E * 2)
+                     : "memory");
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) reinterpret_cast<uint32_t*>(at)[i] = 0;
+      }
+      if (++g == a.G) g = 0, ++n;
+    }
+  }
+  if (a.parent != nullptr) {
+    // path of every node: pointers double their reach in each step
+    const int32_t* p = a.parent + (int64_t)s.b * a.N;
+    int to[2];
+    unsigned long long path[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int m = lane + 32 * i;
+      to[i] = m < a.N ? __ldg(p + m) : -1;
+      path[i] = 1ull << m;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 6; ++k) {
+      int next[2];
+      unsigned long long more[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int from = to[i] & 31;
+        const unsigned long long m0 = __shfl_sync(0xffffffffu, path[0], from);
+        const unsigned long long m1 = __shfl_sync(0xffffffffu, path[1], from);
+        const int t0 = __shfl_sync(0xffffffffu, to[0], from);
+        const int t1 = __shfl_sync(0xffffffffu, to[1], from);
+        more[i] = to[i] < 0 ? 0 : to[i] < 32 ? m0 : m1;
+        next[i] = to[i] < 0 ? -1 : to[i] < 32 ? t0 : t1;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) path[i] |= more[i], to[i] = next[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)  // several warps may write the same values
+      sh.path[lane + 32 * i] = make_uint2((unsigned)path[i], (unsigned)(path[i] >> 32));
+    __syncwarp();
+  }
+  const float to_log2 = a.scale * ((a.c.k_scale != nullptr ? a.c.k_scale[s.h] : 1.f) * kLog2e);
+  cp_async_wait_all();
+#pragma unroll 1
+  for (int r0 = first * 4; r0 < NT; r0 += step * 4) {
+    // four rows at a time, for their latencies to overlap
+    uint32_t x[4][E / 2];
+    unsigned big[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) x[j][i] = reinterpret_cast<uint32_t*>(place(r0 + j))[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i)  // magnitudes order as integers in either type
+        big[j] = max(big[j], max(x[j][i] & 0x7fffu, (x[j][i] >> 16) & 0x7fffu));
+      big[j] = __reduce_max_sync(0xffffffffu, big[j]);
+    }
+    float back = 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float top = a.bf16 ? __uint_as_float(big[j] << 16)
+                               : __half2float(__ushort_as_half((unsigned short)big[j]));
+      const unsigned e = __float_as_uint(top) >> 23;
+      // the row's largest magnitude to [2^8, 2^9); not for zeros, infinities and NaN
+      const unsigned up = e == 0 || e == 255 ? 127u : min(262u - e, 252u);
+      const float mul = __uint_as_float(up << 23);
+      if (lane == j) back = __uint_as_float((254u - up) << 23);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        float2 f;
+        if (a.bf16) {
+          f = make_float2(__uint_as_float(x[j][i] << 16), __uint_as_float(x[j][i] & 0xffff0000u));
+        } else {
+          f = __half22float2(*reinterpret_cast<const __half2*>(&x[j][i]));
+        }
+        reinterpret_cast<uint32_t*>(place(r0 + j))[i] = pack_f16x2(f.x * mul, f.y * mul);
+      }
+    }
+    if (lane < 4) {  // a lane a row
+      const int r = r0 + lane, row = s.row0 + min(r, s.rows - 1), n = row / a.G;
+      sh.row_c[rb][r] = to_log2 * back;
+      sh.row_at[rb][r] = n * a.Hq + row % a.G;
+      if (a.parent != nullptr) sh.row_path[rb][r] = sh.path[n];
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
@@ -460,34 +614,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   volatile int* dead = &sh.dead;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NRAW; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 9);
+    for (int i = 0; i < C::NRAW; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4 * (C::NK + C::NV));
     for (int i = 0; i < C::KU; ++i) mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < C::VU; ++i) mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_empty[i], 8);
-      mbar_init(&sh.p_full[i], 8), mbar_init(&sh.p_empty[i], 1);
-      mbar_init(&sh.vs_full[i], 1), mbar_init(&sh.vs_empty[i], 4);
-      mbar_init(&sh.row_full[i], 1), mbar_init(&sh.row_empty[i], 8);
+      mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_empty[i], 4 * C::NS);
+      mbar_init(&sh.p_full[i], 4 * C::NS), mbar_init(&sh.p_empty[i], 1);
+      mbar_init(&sh.row_full[i], 1), mbar_init(&sh.row_empty[i], 4 * C::NS);
     }
     for (int i = 0; i < C::NQ; ++i) mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 1);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 19);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 23);
     mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.o_empty, 8);
+    mbar_init(&sh.o_empty, 4 * C::NS);
     mbar_init(&sh.drain, 2);
     sh.dead = 0;
     mbar_init_fence();
   }
-  if (warp == 16) tc::tmem_alloc(&sh.tmem, 512);
+  if (warp == 20) tc::tmem_alloc(&sh.tmem, 512);
   pdl_enter();
   attn_lens(a, sh.len, blockIdx.x == 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  // all 512 columns are this block's, so its tensor memory begins at address 0
+  // all 512 columns are this block's, so its tensor memory begins at address 0, and
+  // the addresses below are column numbers known at compile time
   if (sh.tmem != 0) *dead = 1;
-  constexpr uint32_t tmem = 0;
 
-  // every warp but 17 takes the run's segments from the ring
+  // every warp but 23 takes the run's segments from the ring
   int seg_no = 0;
   Seg s;
   auto next_seg = [&]() {
@@ -499,60 +652,105 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     return s.t1 > 0 && !__any_sync(0xffffffffu, *dead);
   };
 
-  if (warp < 4) {
+  if (warp < C::wV) {
     // ------------------------------------------------ K -> TMEM
-    const uint32_t dst = tmem + ((uint32_t)(warp * 32) << 16);
-    int stage = 0, unit = 0;
+    const int group = warp >> 2, quarter = warp & 3;
+    const uint32_t dst = (uint32_t)(quarter * 32) << 16;
+    int stage = 0, unit = C::UNITS >= C::NK ? group : 0, tile = 0;
     unsigned raw_ph = 0, unit_ph = 1;  // an empty ring's first pass does not wait
     for (; next_seg(); ++seg_no) {
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1; ++t) {
+      for (int t = s.t0; t < s.t1; ++t, ++tile) {
         attn_wait(&sh.raw_full[stage], raw_ph, dead);
-        const uint8_t* rec = smem + C::oRaw + stage * C::RAW + warp * rec_bytes(D);
-#pragma unroll 1
-        for (int u = 0; u < C::UNITS; ++u) {
-          const uint32_t s8 =
-              *reinterpret_cast<const uint32_t*>(rec + off_ks(D) + lane * (D / 16) + u * 4);
-          uint32_t w[32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint4 q4 = *reinterpret_cast<const uint4*>(rec + (2 * u + half) * 512 + lane * 16);
-            const uint32_t sc = e4m3x2(s8 >> (16 * half));
-            const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
-            dequant8(q4.x, s0, w + 16 * half);
-            dequant8(q4.y, s0, w + 16 * half + 4);
-            dequant8(q4.z, s1, w + 16 * half + 8);
-            dequant8(q4.w, s1, w + 16 * half + 12);
+        const uint8_t* rec = smem + C::oRaw + stage * C::RAW + quarter * rec_bytes(D);
+        if (C::UNITS >= C::NK || (tile & 1) == group) {
+          // the next unit's bytes are on their way while this one is converted
+          uint4 lo, hi;
+          uint32_t s8;
+          auto load = [&](int u) {
+            lo = *reinterpret_cast<const uint4*>(rec + 2 * u * 512 + lane * 16);
+            hi = *reinterpret_cast<const uint4*>(rec + (2 * u + 1) * 512 + lane * 16);
+            s8 = *reinterpret_cast<const uint32_t*>(rec + off_ks(D) + lane * (D / 16) + u * 4);
+          };
+          constexpr int STEP = C::UNITS >= C::NK ? C::NK : 1;
+          const int u0 = C::UNITS >= C::NK ? group : 0;
+          if (C::UNITS < C::NK) {
+            // this tile's unit: every other one of the ring
+            unit = tile % C::KU;
+            unit_ph = ((tile / C::KU) & 1) ^ 1;
           }
-          attn_wait(&sh.k_empty[unit], unit_ph, dead);
-          tc::fence_after_sync();
-          tmem_st16(dst + unit * 32, w);
-          tmem_st16(dst + unit * 32 + 16, w + 16);
-          tmem_wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.k_full[unit]);
-          if (++unit == C::KU) unit = 0, unit_ph ^= 1;
+          load(u0);
+#pragma unroll
+          for (int i = 0; i < C::UNITS; i += STEP) {
+            uint32_t w[32];
+            const uint32_t sa = e4m3x2(s8), sb = e4m3x2(s8 >> 16);
+            const uint32_t g0 = __byte_perm(sa, sa, 0x1010), g1 = __byte_perm(sa, sa, 0x3232);
+            const uint32_t g2 = __byte_perm(sb, sb, 0x1010), g3 = __byte_perm(sb, sb, 0x3232);
+            dequant8(lo.x, g0, w);
+            dequant8(lo.y, g0, w + 4);
+            dequant8(lo.z, g1, w + 8);
+            dequant8(lo.w, g1, w + 12);
+            dequant8(hi.x, g2, w + 16);
+            dequant8(hi.y, g2, w + 20);
+            dequant8(hi.z, g3, w + 24);
+            dequant8(hi.w, g3, w + 28);
+            if (i + STEP < C::UNITS) load(u0 + i + STEP);
+            attn_wait(&sh.k_empty[unit], unit_ph, dead);
+            tc::fence_after_sync();
+            tmem_st16(dst + unit * 32, w);
+            tmem_st16(dst + unit * 32 + 16, w + 16);
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.k_full[unit]);
+            if (C::UNITS >= C::NK) {
+              unit += C::NK;
+              if (unit >= C::KU) unit -= C::KU, unit_ph ^= 1;
+            }
+          }
         }
         if (lane == 0) mbar_arrive(&sh.raw_empty[stage]);
         if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < C::wS) {
     // ------------------------------------------------ V^T -> TMEM
-    const int quarter = warp - 4;
-    const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + C::cV;
-    attn_zero(a, Lens{a, sh.len}, D, threadIdx.x - 128);
-    int stage = 0, unit = 0, vb = 0;
-    unsigned vs_ph = 0, unit_ph = 1;
-    for (; next_seg(); ++seg_no) {
+    const int group = (warp - C::wV) >> 2, quarter = warp & 3;
+    const uint32_t dst = ((uint32_t)(quarter * 32) << 16) + C::cV;
+    if (group == 0) attn_zero(a, Lens{a, sh.len}, D, threadIdx.x - 32 * C::wV);
+    const int vt = threadIdx.x - 32 * C::wV;
+    int stage = 0, unit = group, tile = 0;
+    unsigned raw_ph = 0, unit_ph = 1;
+    for (;; ++seg_no) {
+      // all of them go on, or none: they meet at a barrier below
+      if (barrier_any(5, 128 * C::NV, !next_seg())) break;
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1; ++t) {
-        attn_wait(&sh.vs_full[vb], vs_ph, dead);  // the records have landed before
+      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+        attn_wait(&sh.raw_full[stage], raw_ph, dead);
         const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
-        const uint8_t* vs = smem + C::oVS + vb * C::VSB;
+        // the tile's scales to binary16, 8 positions of a group a step; those past
+        // the end, or on a page that is not there, count as 0
+        uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
+        const int ok = sh.tile_ok[tile & 7], end = s.len - t * kTile;
+        const bool full = ok == 15 && end >= kTile;
+#pragma unroll
+        for (int i = vt; i < D; i += 128 * C::NV) {
+          const int r = i / (D / 4), go = i % (D / 4);
+          const uint2 s8 =
+              *reinterpret_cast<const uint2*>(raw + r * rec_bytes(D) + off_vs(D) + go * 8);
+          uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
+          if (!full) {
+            const int n = (ok >> r) & 1 ? end - (r * kRec + (go & 3) * 8) : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = n >= 2 * q + 2 ? w[q] : n == 2 * q + 1 ? (w[q] & 0xffffu) : 0u;
+          }
+          *reinterpret_cast<uint4*>(vs + (go >> 2) * C::VSG + r * 64 + (go & 3) * 16) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        tc::named_barrier(5, 128 * C::NV);  // also: the other buffer's readers are done
 #pragma unroll 1
-        for (int r = 0; r < 4; ++r) {
+        for (int r = group; r < 4; r += C::NV) {
           uint32_t w[C::MB][16];
 #pragma unroll
           for (int mb = 0; mb < C::MB; ++mb) {
@@ -584,34 +782,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.v_full[unit]);
-          if (++unit == C::VU) unit = 0, unit_ph ^= 1;
+          unit += C::NV;
+          if (unit >= C::VU) unit -= C::VU, unit_ph ^= 1;
         }
-        if (lane == 0) mbar_arrive(&sh.raw_empty[stage]), mbar_arrive(&sh.vs_empty[vb]);
-        if (++stage == C::NRAW) stage = 0;
-        if (++vb == 2) vb = 0, vs_ph ^= 1;
+        if (lane == 0) mbar_arrive(&sh.raw_empty[stage]);
+        if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
       }
     }
-  } else if (warp < 16) {
+  } else if (warp < 20) {
     // ------------------------------------------------ softmax and epilogue
-    const int group = (warp - 8) >> 2, quarter = warp & 3;
-    const int c0 = group * C::NH;                  // first row of the group
-    const int gt = (threadIdx.x - 256) & 127;      // thread of the group
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    constexpr int CH = C::NH < 16 ? C::NH : 16;    // columns of one load
+    const int group = (warp - C::wS) >> 2, quarter = warp & 3;
+    const int c0 = group * C::NH;                      // first row of the group
+    const int gt = (threadIdx.x - 32 * C::wS) & 127;   // thread of the group
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
     AttnJoin join = {};
     for (;; ++seg_no) {
-      // all eight warps go on, or none: they meet at barriers below
-      if (barrier_any(3, 256, !next_seg())) break;
-      const int base = s.len - a.N;
-      const int n_lo = s.row0 / a.G;
-      const Row* rows = sh.row[seg_no & 1];
-      attn_wait(&sh.row_full[seg_no & 1], (seg_no >> 1) & 1, dead);
-      if (gt < C::NH) sh.cm[c0 + gt] = make_float2(rows[c0 + gt].c, kNone);
+      // all softmax warps go on, or none: they meet at barriers below
+      if (barrier_any(4, 128 * C::NS, !next_seg())) break;
+      const int rb = seg_no & 1;
+      if (seg_no == 0) {
+        // nothing to do yet: all of them fetch the first queries
+        attn_rows<D, NT>(a, sh, s, smem + C::oQ, 0, warp - C::wS, 4 * C::NS);
+        tc::named_barrier(4, 128 * C::NS);
+        if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full[0]), mbar_arrive(&sh.row_full[0]);
+      }
+      attn_wait(&sh.row_full[rb], (seg_no >> 1) & 1, dead);
+      if (gt < C::NH / 2) {
+        const float2 c = *reinterpret_cast<const float2*>(&sh.row_c[rb][c0 + 2 * gt]);
+        sh.cm[c0 / 2 + gt] = make_float4(c.x, c.y, -kNone, -kNone);
+      }
       tc::named_barrier(1 + group, 128);
-      float l[C::NH];
+      const int base = s.len - a.N, n_lo = s.row0 / a.G;
+      float2 l[C::NH / 2];
 #pragma unroll
-      for (int i = 0; i < C::NH; ++i) l[i] = 0.f;
+      for (int i = 0; i < C::NH / 2; ++i) l[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int buf = tile & 1;
@@ -621,135 +826,136 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int ok = sh.tile_ok[tile & 7];
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
-        const bool masked = ok != 15 || (a.parent != nullptr ? (t + 1) * kTile > base
-                                                             : (t + 1) * kTile - 1 > base + n_lo);
-        unsigned long long vis = ~0ull;
-        if (masked) {
+        unsigned vis = ~0u;
+        if (ok != 15 || (a.parent != nullptr ? (t + 1) * kTile > base
+                                             : (t + 1) * kTile - 1 > base + n_lo)) {
           const int u = t * kTile + quarter * 32 + lane - base;
           if (!((ok >> quarter) & 1)) {
             vis = 0;
           } else if (a.parent == nullptr) {
             // nodes rise with the rows: the first row of node u
             const int64_t from = (int64_t)u * a.G - s.row0 - c0;
-            vis = from <= 0 ? ~0ull : from >= 64 ? 0ull : ~0ull << from;
+            vis = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
           } else if (u >= 0) {
             vis = 0;
             if (u < 64)
 #pragma unroll 1
               for (int r = 0; r < C::NH; ++r) {
-                const Row& w = rows[c0 + r];
-                vis |= (unsigned long long)(((u < 32 ? w.lo : w.hi) >> (u & 31)) & 1) << r;
+                const uint2 w = sh.row_path[rb][c0 + r];
+                vis |= (((u < 32 ? w.x : w.y) >> (u & 31)) & 1) << r;
               }
           }
         }
-        // ---- would any p pass 2^kSlack?  (first tile: yes)
-        bool raise = t == s.t0;
-        if (!raise) {
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int k = 0; k < C::NH; k += CH) {
-            uint32_t x[CH];
-            tmem_load(sa + k, x);
-            tc::tmem_wait_ld(x);
-            const unsigned v = (unsigned)(vis >> k);
-#pragma unroll
-            for (int i = 0; i < CH; i += 2) {
-              const float4 cm = *reinterpret_cast<const float4*>(&sh.cm[c0 + k + i]);
-              float y0 = fmaf(__uint_as_float(x[i]), cm.x, -cm.y);
-              float y1 = fmaf(__uint_as_float(x[i + 1]), cm.z, -cm.w);
-              if (masked) {
-                y0 = (v >> i) & 1 ? y0 : -INFINITY;
-                y1 = (v >> (i + 1)) & 1 ? y1 : -INFINITY;
-              }
-              top = fmaxf(top, fmaxf(y0, y1));
-            }
-          }
-          raise = barrier_any(1 + group, 128, top > kSlack);  // NaN rows stay NaN without it
-        }
-        if (raise) {
-          // ---- new references: the largest logits so far
-#pragma unroll 1
-          for (int k = 0; k < C::NH; k += CH) {
-            uint32_t x[CH];
-            tmem_load(sa + k, x);
-            tc::tmem_wait_ld(x);
-            const unsigned v = (unsigned)(vis >> k);
-            float mine = 0.f;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              float y = __uint_as_float(x[i]) * sh.cm[c0 + k + i].x;
-              y = warp_max((v >> i) & 1 ? y : -INFINITY);
-              if (lane == i) mine = y;
-            }
-            if (lane < CH) sh.wmax[quarter][c0 + k + lane] = mine;
-          }
-          tc::named_barrier(1 + group, 128);
-          if (gt < C::NH) {
-            const int r = c0 + gt;
-            const float old = sh.cm[r].y;
-            float m = old;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float w = sh.wmax[q][r];
-              m = w > m || w != w ? w : m;
-            }
-            sh.cm[r].y = m;
-            sh.alpha[r] = exp2_fast(old - m);
-          }
-          tc::named_barrier(1 + group, 128);
-          if (t != s.t0) {
-            // every product into O^T so far is done: the last one freed its P
-            attn_wait(&sh.p_empty[buf ^ 1], ((tile - 1) >> 1) & 1, dead);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int k = 0; k < C::NH; ++k) l[k] *= sh.alpha[c0 + k];
-#pragma unroll 1
-            for (int k = 0; k < C::MB * C::NH; k += 8) {
-              const int col = c0 + k % C::NH;
-              const uint32_t oa = lane_base + C::cO + k / C::NH * C::NT + col;
-              uint32_t x[8];
-              tc::tmem_ld8(oa, x);
-              tc::tmem_wait_ld(x);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) * sh.alpha[col + i]);
-              tmem_st8(oa, x);
-            }
-            tmem_wait_st();
-          }
-        }
-        // ---- p, its sums, and P as the B operand
+        const bool masked = __any_sync(0xffffffffu, vis != ~0u);
         attn_wait(&sh.p_empty[buf], ph ^ 1, dead);
         uint8_t* prow = smem + C::oP + buf * C::PB + (quarter * 32 + lane) * 128;
+        uint32_t y[C::NH / 16][16];
+        auto load = [&](uint32_t at) {
 #pragma unroll
-        for (int k = 0; k < C::NH; k += CH) {
-          uint32_t x[CH];
-          tmem_load(sa + k, x);
-          tc::tmem_wait_ld(x);
-          uint32_t p[CH / 2];
-          const unsigned v = (unsigned)(vis >> k);
+          for (int k = 0; k < C::NH / 16; ++k) tc::tmem_ld16(at + 16 * k, y[k]);
+          tc::tmem_wait_ld(y[0]);
+          if constexpr (C::NH == 32) tc::tmem_ready(y[1]);
+        };
+        // The first tile sets the references; a later one is tried with those there
+        // are, and done again in the case that some p passed 2^8.
+        bool raise = t == s.t0;
+#pragma unroll 1
+        for (;;) {
+          load(sa);
+          if (raise) {
+            // ---- new references: the largest logits so far
+            float x[C::NH];
 #pragma unroll
-          for (int i = 0; i < CH; i += 2) {
-            const float4 cm = *reinterpret_cast<const float4*>(&sh.cm[c0 + k + i]);
-            float y0 = exp2_fast(fmaf(__uint_as_float(x[i]), cm.x, -cm.y));
-            float y1 = exp2_fast(fmaf(__uint_as_float(x[i + 1]), cm.z, -cm.w));
-            if (masked) {
-              y0 = (v >> i) & 1 ? y0 : 0.f;
-              y1 = (v >> (i + 1)) & 1 ? y1 : 0.f;
+            for (int i = 0; i < C::NH; i += 2) {
+              const float4 cm = sh.cm[(c0 + i) / 2];
+              const float x0 = __uint_as_float(y[i / 16][i % 16]) * cm.x;
+              const float x1 = __uint_as_float(y[i / 16][i % 16 + 1]) * cm.y;
+              x[i] = (vis >> i) & 1 ? x0 : -INFINITY;
+              x[i + 1] = (vis >> (i + 1)) & 1 ? x1 : -INFINITY;
             }
-            l[k + i] += y0;
-            l[k + i + 1] += y1;
-            p[i / 2] = pack_f16x2(y0, y1);
-          }
+            const float top = warp_transpose_reduce(
+                x, [](float p, float q) { return q > p || q != q ? q : p; });
+            if (lane < C::NH) sh.part[quarter][c0 + lane] = top;
+            tc::named_barrier(1 + group, 128);
+            if (gt < C::NH) {
+              const int r = c0 + gt;
+              float* neg = reinterpret_cast<float*>(&sh.cm[r / 2]) + 2 + (r & 1);
+              const float old = -*neg;
+              float m = old;
 #pragma unroll
-          for (int i = 0; i < CH / 8; ++i) {
-            const int col = c0 + k + 8 * i;  // 16-byte chunk of 8 rows, swizzled by position
-            uint8_t* at = prow + (col >> 6) * (kTile * 128) +
-                          ((((col & 63) >> 3) ^ (lane & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) =
-                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+              for (int q = 0; q < 4; ++q) {
+                const float w = sh.part[q][r];
+                m = w > m || w != w ? w : m;
+              }
+              *neg = -m;
+              sh.alpha[r] = exp2_fast(old - m);
+            }
+            tc::named_barrier(1 + group, 128);
+            if (t != s.t0) {
+              // every product into O^T so far is done: the last one freed its P
+              attn_wait(&sh.p_empty[buf ^ 1], ((tile - 1) >> 1) & 1, dead);
+              tc::fence_after_sync();
+#pragma unroll
+              for (int k = 0; k < C::NH / 2; ++k) {
+                l[k].x *= sh.alpha[c0 + 2 * k];
+                l[k].y *= sh.alpha[c0 + 2 * k + 1];
+              }
+#pragma unroll 1
+              for (int k = 0; k < C::MB * C::NH; k += 8) {
+                const int col = c0 + k % C::NH;
+                const uint32_t oa = lane_base + C::cO + k / C::NH * C::NT + col;
+                uint32_t o[8];
+                tc::tmem_ld8(oa, o);
+                tc::tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.alpha[col + i]);
+                tmem_st8(oa, o);
+              }
+              tmem_wait_st();
+            }
+            load(sa);
           }
+          // ---- p, and P as the B operand
+#pragma unroll
+          for (int i = 0; i < C::NH; i += 2) {
+            const float4 cm = sh.cm[(c0 + i) / 2];
+            uint32_t& y0 = y[i / 16][i % 16];
+            uint32_t& y1 = y[i / 16][i % 16 + 1];
+            const float2 z = fma2(make_float2(__uint_as_float(y0), __uint_as_float(y1)),
+                                  make_float2(cm.x, cm.y), make_float2(cm.z, cm.w));
+            y0 = __float_as_uint(exp2_fast(z.x));
+            y1 = __float_as_uint(exp2_fast(z.y));
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < C::NH; ++i)
+              if (!((vis >> i) & 1)) y[i / 16][i % 16] = 0;
+          }
+          unsigned top = 0;
+#pragma unroll
+          for (int k = 0; k < C::NH; k += 8) {
+            uint32_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = k + 2 * i;
+              p[i] = pack_f16x2(__uint_as_float(y[at / 16][at % 16]),
+                                __uint_as_float(y[at / 16][at % 16 + 1]));
+              top = __vmaxu2(top, p[i]);  // p >= 0: ordered as integers
+            }
+            const int col = c0 + k;  // 16-byte chunk of 8 rows, swizzled by position
+            *reinterpret_cast<uint4*>(prow + (col >> 6) * (kTile * 128) +
+                                      ((((col & 63) >> 3) ^ (lane & 7)) << 4)) =
+                make_uint4(p[0], p[1], p[2], p[3]);
+          }
+          if (raise) break;
+          raise = barrier_any(1 + group, 128, max(top & 0xffffu, top >> 16) > kMostP);
+          if (!raise) break;
         }
+#pragma unroll
+        for (int i = 0; i < C::NH; i += 2)
+          l[i / 2] = add2(l[i / 2], make_float2(__uint_as_float(y[i / 16][i % 16]),
+                                                __uint_as_float(y[i / 16][i % 16 + 1])));
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
@@ -758,61 +964,77 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       // ---- epilogue
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       const int64_t item = (int64_t)s.b * a.N * a.Hq + s.h * a.G;  // output row of node 0
-      attn_wait(&sh.o_full, seg_no & 1, dead);
-      tc::fence_after_sync();
-      float* sums = reinterpret_cast<float*>(smem + C::oP) + c0 * 129;  // P is free now
-#pragma unroll
-      for (int k = 0; k < C::NH; ++k) sums[k * 129 + gt] = l[k];
-      tc::named_barrier(1 + group, 128);
       const int64_t slot = 2 * (int64_t)blockIdx.x + (seg_no > 0);
+      {
+        float x[C::NH];
+#pragma unroll
+        for (int i = 0; i < C::NH / 2; ++i) x[2 * i] = l[i].x, x[2 * i + 1] = l[i].y;
+        const float sum = warp_transpose_reduce(x, [](float p, float q) { return p + q; });
+        if (lane < C::NH) sh.part[quarter][c0 + lane] = sum;
+      }
       if (s.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
         join = {item, s.h, s.row0, s.rows, (int)slot, s.last};
+      tc::named_barrier(1 + group, 128);
       if (gt < C::NH) {
         const int r = c0 + gt;
-        float total = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < 128; ++i) total += sums[gt * 129 + i];
-        const float m = sh.cm[r].y;
+        const float total = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
+        const float m = -reinterpret_cast<const float*>(&sh.cm[r / 2])[2 + (r & 1)];
+        float inv = 1.f;
         if (whole) {
-          const float vsc = a.c.v_scale != nullptr ? a.c.v_scale[s.h] : 1.f;
-          sh.inv[r] = total != 0.f ? vsc / total : 0.f;
+          inv = total != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[s.h] : 1.f) / total : 0.f;
           if (a.lse != nullptr && r < s.rows)
-            a.lse[item + rows[r].at] =
+            a.lse[item + sh.row_at[rb][r]] =
                 total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
         } else {
           a.part_ml[slot * NT + r] = make_float2(m, total);
-          sh.inv[r] = 1.f;
         }
+        sh.inv[r] = inv;
       }
-      tc::named_barrier(3, 256);  // both groups' sums are read: P may be written again
+      attn_wait(&sh.o_full, seg_no & 1, dead);
+      tc::fence_after_sync();
+      tc::named_barrier(1 + group, 128);
 #pragma unroll 1
       for (int mb = 0; mb < C::MB; ++mb) {
         const int ch = mb * 128 + quarter * 32 + lane;
-#pragma unroll 1
-        for (int r0 = c0; r0 < c0 + C::NH && r0 < s.rows; r0 += 8) {
-          uint32_t x[8];
-          tc::tmem_ld8(lane_base + C::cO + mb * C::NT + r0, x);
-          tc::tmem_wait_ld(x);
-          if (D < 128 && ch >= D) continue;
+        uint32_t o[C::NH / 16][16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + i;
-            if (r >= s.rows) break;
-            const float o = __uint_as_float(x[i]) * sh.inv[r];
-            if (whole)
-              static_cast<uint16_t*>(a.o)[(item + rows[r].at) * D + ch] =
-                  a.bf16 ? Elem<GDN_BF16>::from(o) : Elem<GDN_F16>::from(o);
-            else
-              a.part_o[(slot * NT + r) * D + ch] = o;
+        for (int k = 0; k < C::NH / 16; ++k)
+          tc::tmem_ld16(lane_base + C::cO + mb * C::NT + c0 + 16 * k, o[k]);
+        tc::tmem_wait_ld(o[0]);
+        if constexpr (C::NH == 32) tc::tmem_ready(o[1]);
+        if (D < 128 && ch >= D) continue;
+        const int rows = s.rows - c0;
+        if (whole) {
+          uint16_t* out = static_cast<uint16_t*>(a.o) + item * D + ch;
+#pragma unroll
+          for (int i = 0; i < C::NH; i += 4) {
+            const int4 at = *reinterpret_cast<const int4*>(&sh.row_at[rb][c0 + i]);
+            const float4 inv = *reinterpret_cast<const float4*>(&sh.inv[c0 + i]);
+            const int at_[4] = {at.x, at.y, at.z, at.w};
+            const float inv_[4] = {inv.x, inv.y, inv.z, inv.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (i + k >= rows) break;
+              const float v = __uint_as_float(o[i / 16][i % 16 + k]) * inv_[k];
+              out[(int64_t)at_[k] * D] =
+                  a.bf16 ? Elem<GDN_BF16>::from(v) : Elem<GDN_F16>::from(v);
+            }
+          }
+        } else {
+          float* out = a.part_o + (slot * NT + c0) * D + ch;
+#pragma unroll
+          for (int i = 0; i < C::NH; ++i) {
+            if (i >= rows) break;
+            out[i * D] = __uint_as_float(o[i / 16][i % 16]);
           }
         }
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.row_empty[seg_no & 1]);
+      if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.row_empty[rb]);
     }
-    if (threadIdx.x == 256) a.join[blockIdx.x] = join;
-  } else if (warp == 16) {
+    if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = join;
+  } else if (warp == 20) {
     // ------------------------------------------------ S^T products (one elected lane)
     constexpr uint32_t id = idesc_f16(NT, false);
     // descriptors advance by 16-byte units in their low word
@@ -852,7 +1074,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       }
       if (++qs == C::NQ) qs = 0, q_ph ^= 1;
     }
-  } else if (warp == 19) {
+  } else if (warp == 21) {
     // ------------------------------------------------ O^T products (one elected lane)
     constexpr uint32_t id = idesc_f16(NT, true);
     const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
@@ -888,16 +1110,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         if ((4 / C::VU) & 1) vu_ph ^= 1;
       }
     }
-  } else if (warp == 17) {
-    // ------------------------------------------------ segments and records in, V scales to binary16
+  } else if (warp == 23) {
+    // ------------------------------------------------ segments and records in
     const Lens lens = {a, sh.len};
     Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
     Seg f = {};  // the copies run ahead of the conversion
-    int f_t = 0, f_seg = 0, f_tile = 0, f_stage = 0;
+    int f_t = 0, f_seg = 0, f_tile = 0, f_stage = 0, page = 0;
     bool f_on = true;
     unsigned empty_ph = 1;
-    auto fetch = [&]() {
-      if (f_t == f.t1 && f_on) {  // publish the next segment
+    // the next tile to copy: its segment published, its page numbers on their way
+    auto look_ahead = [&]() {
+      if (f_t == f.t1) {
         f = attn_seg(a, lens, run);
         f_t = f.t0;
         f_on = f.t1 > 0;
@@ -909,168 +1132,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         }
         ++f_seg;
       }
-      if (!f_on) return;
-      attn_wait(&sh.raw_empty[f_stage], empty_ph, dead);
-      const uint8_t* src = nullptr;
-      bool ok = true;  // past the end: nothing to read, hidden by position
       const int pos = f_t * kTile + lane * kRec;
-      if (lane < 4 && pos < f.len) {
-        src = record(a.c, f.b, f.h, pos);
-        ok = src != nullptr;
-        if (!ok) report(a.c.status, GDN_ERR_PAGE_RANGE);
-      }
-      const unsigned good = __ballot_sync(0xffffffffu, ok) & 15u;
-      const unsigned copies = __ballot_sync(0xffffffffu, src != nullptr);
+      page = f_on && lane < 4 && pos < f.len
+                 ? a.c.table[(int64_t)f.b * a.c.table_stride + pos / a.c.page_tokens]
+                 : -1;
+    };
+    auto fetch = [&]() {
+      attn_wait(&sh.raw_empty[f_stage], empty_ph, dead);
+      const int pos = f_t * kTile + lane * kRec;
+      const bool want = lane < 4 && pos < f.len;  // past the end: nothing to read
+      const bool have = want && page >= 0 && page < a.c.n_pages;
+      if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
+      const unsigned good = __ballot_sync(0xffffffffu, have || !want) & 15u;
+      const unsigned copies = __ballot_sync(0xffffffffu, have);
       if (lane == 0) {
         sh.tile_ok[f_tile & 7] = (int)good;
         mbar_arrive_expect_tx(&sh.raw_full[f_stage], __popc(copies) * rec_bytes(D));
       }
       __syncwarp();
-      if (src != nullptr)
+      if (have) {
+        const int recs = a.c.page_tokens / kRec;
+        const uint8_t* src =
+            static_cast<const uint8_t*>(a.c.pages) + (int64_t)page * a.c.page_stride +
+            ((int64_t)f.h * recs + pos % a.c.page_tokens / kRec) * rec_bytes(D);
         bulk_g2s(smem + C::oRaw + f_stage * C::RAW + lane * rec_bytes(D), src, rec_bytes(D),
                  &sh.raw_full[f_stage]);
+      }
       if (++f_stage == C::NRAW) f_stage = 0, empty_ph ^= 1;
       ++f_tile;
       ++f_t;
+      look_ahead();
     };
-    // the conversion follows the copies NRAW - 2 tiles behind, so that it does not
-    // wait for the readers of the tile before it
-    int stage = 0, vb = 0, tile = 0, t = 0;
-    unsigned raw_ph = 0, vs_ph = 1;
-    const Seg* c = nullptr;
+    look_ahead();
 #pragma unroll 1
-    for (int k = 0;; ++k) {
-      fetch();
-      if (k < C::NRAW - 2) continue;
-      if (tile == f_tile) break;
-      if (c == nullptr || t == c->t1) {  // the segment of this tile
-        c = &sh.seg[seg_no++ & (kSegs - 1)];
-        t = c->t0;
-      }
-      attn_wait(&sh.raw_full[stage], raw_ph, dead);
-      attn_wait(&sh.vs_empty[vb], vs_ph, dead);
-      const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
-      uint8_t* vs = smem + C::oVS + vb * C::VSB;
-      const int ok = sh.tile_ok[tile & 7];
-      const int end = c->len - t * kTile;
-      // 8 scales of a group a step; positions past the end count as 0
-#pragma unroll 2
-      for (int i = lane; i < 4 * (D / 16) * 4; i += 32) {
-        const int r = i / (D / 4), g = (i / 4) % (D / 16), o = i & 3;
-        const uint2 s8 = *reinterpret_cast<const uint2*>(raw + r * rec_bytes(D) + off_vs(D) +
-                                                         g * kRec + o * 8);
-        uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
-        const int n = (ok >> r) & 1 ? end - (r * kRec + o * 8) : 0;  // positions that exist
-        if (n < 8) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = n >= 2 * j + 2 ? w[j] : n == 2 * j + 1 ? (w[j] & 0xffffu) : 0u;
-        }
-        *reinterpret_cast<uint4*>(vs + g * C::VSG + r * 64 + o * 16) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.vs_full[vb]), mbar_arrive(&sh.raw_empty[stage]);
-      if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
-      if (++vb == 2) vb = 0, vs_ph ^= 1;
-      ++t;
-      ++tile;
-    }
+    while (f_on) fetch();
     if (*dead) {  // copies in flight land before the block's memory is given back
       for (int i = 0; i < C::NRAW && i < f_tile; ++i)
         (void)mbar_wait_bounded(&sh.raw_full[i], ((f_tile - i - 1) / C::NRAW) & 1, kWaitPolls);
     }
   } else {
-    // ------------------------------------------------ queries
-    // Copied as they are to where the operand goes, then each lane turns its own
-    // channels into binary16 in place.
-    constexpr int E = D / 32;   // channels of a lane
+    // ------------------------------------------------ queries of the segments after the first
     int qb = 0;
     unsigned ph = 1;
     for (; next_seg(); ++seg_no) {
       attn_wait(&sh.q_empty[qb], ph, dead);
       attn_wait(&sh.row_empty[seg_no & 1], ((seg_no >> 1) & 1) ^ 1, dead);
-      const float ks = a.c.k_scale != nullptr ? a.c.k_scale[s.h] : 1.f;
-      const int ch = lane * E;
-      uint8_t* q = smem + C::oQ + qb * C::QB + (ch >> 6) * (NT * 128) + (ch & 7) * 2;
-      const uint16_t* src0 =
-          static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
-      int n = s.row0 / a.G, g = s.row0 % a.G;
-      const int n0 = n, g0 = g;
-#pragma unroll 1
-      for (int r = 0; r < NT; ++r) {
-        uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
-        if (r < s.rows) {
-          const uint16_t* src = src0 + n * a.q_stride_n + (int64_t)g * D;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)), "l"(src),
-                       "n"(E * 2)
-                       : "memory");
-        } else if constexpr (E == 8) {
-          *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-        } else if constexpr (E == 4) {
-          *reinterpret_cast<uint2*>(at) = make_uint2(0, 0);
-        } else {
-          *reinterpret_cast<uint32_t*>(at) = 0;
-        }
-        if (++g == a.G) g = 0, ++n;
+      if (seg_no > 0) {
+        attn_rows<D, NT>(a, sh, s, smem + C::oQ + qb * C::QB, seg_no & 1, 0, 1);
+        if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.row_full[seg_no & 1]);
       }
-      cp_async_wait_all();
-      n = n0, g = g0;
-#pragma unroll 1
-      for (int r = 0; r < NT; ++r) {
-        uint32_t* at =
-            reinterpret_cast<uint32_t*>(q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4));
-        float f[E];
-        unsigned big = 0;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const uint32_t x = at[i];
-          if (a.bf16) {
-            f[2 * i] = __uint_as_float(x << 16);
-            f[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
-          } else {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x));
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-          }
-          big = max(big, max(__float_as_uint(f[2 * i]) & 0x7fffffffu,
-                             __float_as_uint(f[2 * i + 1]) & 0x7fffffffu));
-        }
-        big = __reduce_max_sync(0xffffffffu, big) >> 23;
-        // the row's largest magnitude to [2^8, 2^9); not for zeros, infinities and NaN
-        const unsigned up = big == 0 || big == 255 ? 127u : min(262u - big, 252u);
-        const float mul = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) at[i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
-        if (lane == 0) {
-          Row info = {a.scale * back * (ks * kLog2e), n * a.Hq + g, 0, 0};
-          if (a.parent != nullptr && r < s.rows) {
-            const int32_t* p = a.parent + (int64_t)s.b * a.N;
-            unsigned long long seen = 0;
-            for (int m = n; m >= 0; m = p[m]) seen |= 1ull << m;
-            info.lo = (unsigned)seen;
-            info.hi = (unsigned)(seen >> 32);
-          }
-          sh.row[seg_no & 1][r] = info;
-        }
-        if (++g == a.G) g = 0, ++n;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.row_full[seg_no & 1]);
       if (++qb == C::NQ) qb = 0, ph ^= 1;
     }
   }
   // every role is done with its loops, hence with its copies and products; after a
   // wait that ran out, products in flight end (bounded) before TMEM is given back
-  if ((warp == 16 || warp == 19) && __any_sync(0xffffffffu, *dead)) {
+  if ((warp == 20 || warp == 21) && __any_sync(0xffffffffu, *dead)) {
     if (elect_one()) tc::mma_commit(&sh.drain);
     (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
   }
   tc::fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *dead) report(a.c.status, GDN_ERR_TIMEOUT);
-  if (warp == 16) {
+  if (warp == 20) {
     tc::fence_after_sync();
     tc::tmem_relinquish();
     tc::tmem_dealloc(sh.tmem, 512);
