@@ -23,10 +23,11 @@
 //   K groups   position = TMEM lane; codes * scale -> binary16 -> TMEM (64 channels a unit)
 //   V groups   channel = TMEM lane; the same for V^T (32 positions a unit)
 //   softmax groups, 32 rows each: S^T from TMEM, p to shared memory (B operand),
-//              sums in registers, and the item's epilogue
-//   and a warp each that issues S^T's products, issues O^T's, turns queries into
-//   the B operand (binary16, scaled by a power of two per row so that any bf16
-//   magnitude fits), and walks the run: segments, bulk copies of the records.
+//              sums in registers, the item's epilogue, and the next item's queries into
+//              the B operand (binary16, scaled by a power of two per row so that any
+//              bf16 magnitude fits)
+//   and a warp each that issues S^T's products, issues O^T's, copies the records' K
+//   halves (and cuts the run into segments), and copies their V halves.
 // Few rows leave the time to the 4-bit operand, many to the softmax, so up to 32
 // rows two groups each dequantise K and V, and 96 rows take three softmax groups.
 //
@@ -74,17 +75,18 @@ struct AttnCfg {
   static constexpr int cS = 32 * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
   static_assert(cV + VU * 16 * MB <= 512, "TMEM");
   // shared memory
-  static constexpr int RAW = 4 * rec_bytes(D);
+  static constexpr int HALF = 18 * D;          // of a record: K's or V's codes and scales
+  static constexpr int RAW = 4 * HALF;         // a stage of either ring
   static constexpr int QB = NT * D * 2;
   static constexpr int PB = (NT > 64 ? 2 : 1) * kTile * 128;
   static constexpr int VSG = 272;  // bytes between the scale rows of two groups (bank offset)
   static constexpr int VSB = D / 16 * VSG;
-  static constexpr int P2 = 2 * PB;
-  static constexpr int ROOM = 224 * 1024 - P2 - 2 * VSB - 4096;
-  static constexpr int NQ = ROOM - 2 * QB >= 2 * RAW ? 2 : 1;
-  static constexpr int NRAW = (ROOM - NQ * QB) / RAW > 4 ? 4 : (ROOM - NQ * QB) / RAW;
-  static_assert(NRAW >= 2, "stages");
-  static constexpr int oQ = 0, oP = oQ + NQ * QB, oRaw = oP + P2, oVS = oRaw + NRAW * RAW;
+  static constexpr int ROOM = (220 * 1024 - QB - 2 * PB - 2 * VSB) / RAW;
+  static constexpr int KR = ROOM / 2 > 6 ? 6 : ROOM / 2;
+  static constexpr int VR = ROOM - KR > 6 ? 6 : ROOM - KR;
+  static_assert(KR >= 2 && VR >= 2, "stages");
+  static constexpr int oQ = 0, oP = oQ + QB, oK = oP + 2 * PB, oV = oK + KR * RAW;
+  static constexpr int oVS = oV + VR * RAW;
   static constexpr int oEnd = oVS + 2 * VSB;
   static constexpr int SMEM = oEnd + 1024;  // + alignment of the swizzled operands
 };
@@ -95,26 +97,27 @@ struct Seg {
   int last;  // block that holds the item's last tile
 };
 
-constexpr int kSegs = 16;    // ring of segments; a block's warps are fewer apart
+constexpr int kSegs = 16;    // ring of segments and of tiles' page checks; a block's warps are
+                             // fewer tiles apart
 constexpr int kLens = 1024;  // lengths kept in shared memory
 
 template <typename C>
 struct AttnShared {
-  uint64_t raw_full[C::NRAW], raw_empty[C::NRAW];
+  uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
   uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-  uint64_t q_full[C::NQ], q_empty[C::NQ], row_full[2], row_empty[2], o_full, o_empty, drain;
+  uint64_t q_full, o_full, o_empty, drain;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int dead;
-  int tile_ok[8];  // records of a tile that could be read, by tile number
+  int k_ok[kSegs], v_ok[kSegs];  // records of a tile that could be read, by tile number
   Seg seg[kSegs];
-  // of the query rows, by segment: c (logit of S: c * S, log2 units), the row of
+  // of the query rows: c (logit of S: c * S, log2 units), the row of
   // the output from the item's first node and head on, and for trees the
   // positions of the block that the row sees
-  alignas(16) float row_c[2][C::NT];
-  alignas(16) int row_at[2][C::NT];
-  uint2 row_path[2][C::NT];
+  alignas(16) float row_c[C::NT];
+  alignas(16) int row_at[C::NT];
+  uint2 row_path[C::NT];
   uint2 path[64];                   // of each node
   alignas(16) float4 cm[C::NT / 2]; // rows in work, by pairs: c, c, -m, -m
   alignas(16) float alpha[C::NT], inv[C::NT];
@@ -347,6 +350,7 @@ __device__ __forceinline__ int64_t warp_cost(const AttnArgs& a, int len) {
 struct Runs {
   int64_t each, extra;
   int parts;
+  Runs() = default;
   __device__ __forceinline__ Runs(int64_t total, int n) {
     parts = total < n ? (int)total : n;  // no empty runs in between
     each = parts > 0 ? total / parts : 0;
@@ -489,26 +493,24 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& len
 }
 
 // ---------------------------------------------------------------- queries
-// Query rows of segment s into the B operand at q, and what goes with them into
-// buffer `rb`: four rows at a time, quads `first`, first + step, ... of a warp.
-// The rows are copied as they are to where the operand goes, then each lane
-// turns its own channels into binary16 in place.
+// Query rows of segment s into the B operand at q, four rows at a time: quads
+// `first`, first + step, ... of a warp.  The rows are copied as they are to where
+// the operand goes (the copies are this thread's cp.async, not waited for).
 template <int D, int NT>
-static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
-                                              const Seg& s, uint8_t* q, int rb, int first,
-                                              int step) {
+static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, const Seg& s, uint8_t* q,
+                                                   int first, int step) {
   constexpr int E = D / 32;  // channels of a lane
-  const int lane = threadIdx.x & 31, ch = lane * E;
+  const int ch = (threadIdx.x & 31) * E;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
-  auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
   const uint16_t* src0 =
       static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
 #pragma unroll 1
   for (int r0 = first * 4; r0 < NT; r0 += step * 4) {
     int n = (s.row0 + r0) / a.G, g = (s.row0 + r0) % a.G;
-#pragma unroll 1
-    for (int r = r0; r < r0 + 4; ++r) {
-      uint8_t* at = place(r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + j;
+      uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
       if (r < s.rows) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)),
                      "l"(src0 + n * a.q_stride_n + (int64_t)g * D), "n"(E * 2)
@@ -520,6 +522,17 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
       if (++g == a.G) g = 0, ++n;
     }
   }
+}
+
+// Then each lane turns its own channels into binary16 in place, and what goes
+// with the rows is written.
+template <int D, int NT>
+static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
+                                              const Seg& s, uint8_t* q, int first, int step) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, ch = lane * E;
+  q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
+  auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
   if (a.parent != nullptr) {
     // path of every node: pointers double their reach in each step
     const int32_t* p = a.parent + (int64_t)s.b * a.N;
@@ -594,9 +607,9 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
     }
     if (lane < 4) {  // a lane a row
       const int r = r0 + lane, row = s.row0 + min(r, s.rows - 1), n = row / a.G;
-      sh.row_c[rb][r] = to_log2 * back;
-      sh.row_at[rb][r] = n * a.Hq + row % a.G;
-      if (a.parent != nullptr) sh.row_path[rb][r] = sh.path[n];
+      sh.row_c[r] = to_log2 * back;
+      sh.row_at[r] = n * a.Hq + row % a.G;
+      if (a.parent != nullptr) sh.row_path[r] = sh.path[n];
     }
   }
   fence_proxy_async_smem();
@@ -614,15 +627,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   volatile int* dead = &sh.dead;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NRAW; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], 4 * (C::NK + C::NV));
+    for (int i = 0; i < C::KR; ++i)
+      mbar_init(&sh.kr_full[i], 1), mbar_init(&sh.kr_empty[i], 4 * C::NK);
+    for (int i = 0; i < C::VR; ++i)
+      mbar_init(&sh.vr_full[i], 1), mbar_init(&sh.vr_empty[i], 4 * C::NV);
     for (int i = 0; i < C::KU; ++i) mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < C::VU; ++i) mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_empty[i], 4 * C::NS);
       mbar_init(&sh.p_full[i], 4 * C::NS), mbar_init(&sh.p_empty[i], 1);
-      mbar_init(&sh.row_full[i], 1), mbar_init(&sh.row_empty[i], 4 * C::NS);
     }
-    for (int i = 0; i < C::NQ; ++i) mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 1);
+    mbar_init(&sh.q_full, 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 23);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.o_empty, 4 * C::NS);
@@ -640,7 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   // the addresses below are column numbers known at compile time
   if (sh.tmem != 0) *dead = 1;
 
-  // every warp but 23 takes the run's segments from the ring
+  // every warp but 22 takes the run's segments from the ring
   int seg_no = 0;
   Seg s;
   auto next_seg = [&]() {
@@ -661,8 +676,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     for (; next_seg(); ++seg_no) {
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        attn_wait(&sh.raw_full[stage], raw_ph, dead);
-        const uint8_t* rec = smem + C::oRaw + stage * C::RAW + quarter * rec_bytes(D);
+        attn_wait(&sh.kr_full[stage], raw_ph, dead);
+        const uint8_t* rec = smem + C::oK + stage * C::RAW + quarter * C::HALF;
         if (C::UNITS >= C::NK || (tile & 1) == group) {
           // the next unit's bytes are on their way while this one is converted
           uint4 lo, hi;
@@ -670,7 +685,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           auto load = [&](int u) {
             lo = *reinterpret_cast<const uint4*>(rec + 2 * u * 512 + lane * 16);
             hi = *reinterpret_cast<const uint4*>(rec + (2 * u + 1) * 512 + lane * 16);
-            s8 = *reinterpret_cast<const uint32_t*>(rec + off_ks(D) + lane * (D / 16) + u * 4);
+            s8 = *reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * (D / 16) + u * 4);
           };
           constexpr int STEP = C::UNITS >= C::NK ? C::NK : 1;
           const int u0 = C::UNITS >= C::NK ? group : 0;
@@ -709,8 +724,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             }
           }
         }
-        if (lane == 0) mbar_arrive(&sh.raw_empty[stage]);
-        if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kr_empty[stage]);
+        if (++stage == C::KR) stage = 0, raw_ph ^= 1;
       }
     }
   } else if (warp < C::wS) {
@@ -726,18 +742,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       if (barrier_any(5, 128 * C::NV, !next_seg())) break;
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        attn_wait(&sh.raw_full[stage], raw_ph, dead);
-        const uint8_t* raw = smem + C::oRaw + stage * C::RAW;
+        attn_wait(&sh.vr_full[stage], raw_ph, dead);
+        const uint8_t* raw = smem + C::oV + stage * C::RAW;
         // the tile's scales to binary16, 8 positions of a group a step; those past
         // the end, or on a page that is not there, count as 0
         uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
-        const int ok = sh.tile_ok[tile & 7], end = s.len - t * kTile;
+        const int ok = sh.v_ok[tile & (kSegs - 1)], end = s.len - t * kTile;
         const bool full = ok == 15 && end >= kTile;
 #pragma unroll
         for (int i = vt; i < D; i += 128 * C::NV) {
           const int r = i / (D / 4), go = i % (D / 4);
           const uint2 s8 =
-              *reinterpret_cast<const uint2*>(raw + r * rec_bytes(D) + off_vs(D) + go * 8);
+              *reinterpret_cast<const uint2*>(raw + r * C::HALF + 16 * D + go * 8);
           uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
           if (!full) {
             const int n = (ok >> r) & 1 ? end - (r * kRec + (go & 3) * 8) : 0;
@@ -757,7 +773,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const int ch = mb * 128 + quarter * 32 + lane;
             if (D >= 128 || ch < D) {
               const uint4 q4 =
-                  *reinterpret_cast<const uint4*>(raw + r * rec_bytes(D) + off_v(D) + ch * 16);
+                  *reinterpret_cast<const uint4*>(raw + r * C::HALF + ch * 16);
               const uint4* sp = reinterpret_cast<const uint4*>(vs + (ch >> 4) * C::VSG + r * 64);
               const uint32_t c4[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
@@ -785,8 +801,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           unit += C::NV;
           if (unit >= C::VU) unit -= C::VU, unit_ph ^= 1;
         }
-        if (lane == 0) mbar_arrive(&sh.raw_empty[stage]);
-        if (++stage == C::NRAW) stage = 0, raw_ph ^= 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.vr_empty[stage]);
+        if (++stage == C::VR) stage = 0, raw_ph ^= 1;
       }
     }
   } else if (warp < 20) {
@@ -797,19 +814,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
     AttnJoin join = {};
+    bool more = next_seg();
+    if (more) attn_rows_copy<D, NT>(a, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
     for (;; ++seg_no) {
       // all softmax warps go on, or none: they meet at barriers below
-      if (barrier_any(4, 128 * C::NS, !next_seg())) break;
-      const int rb = seg_no & 1;
-      if (seg_no == 0) {
-        // nothing to do yet: all of them fetch the first queries
-        attn_rows<D, NT>(a, sh, s, smem + C::oQ, 0, warp - C::wS, 4 * C::NS);
-        tc::named_barrier(4, 128 * C::NS);
-        if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full[0]), mbar_arrive(&sh.row_full[0]);
-      }
-      attn_wait(&sh.row_full[rb], (seg_no >> 1) & 1, dead);
+      if (barrier_any(4, 128 * C::NS, !more)) break;
+      attn_rows<D, NT>(a, sh, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
+      tc::named_barrier(4, 128 * C::NS);
+      if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH / 2) {
-        const float2 c = *reinterpret_cast<const float2*>(&sh.row_c[rb][c0 + 2 * gt]);
+        const float2 c = *reinterpret_cast<const float2*>(&sh.row_c[c0 + 2 * gt]);
         sh.cm[c0 / 2 + gt] = make_float4(c.x, c.y, -kNone, -kNone);
       }
       tc::named_barrier(1 + group, 128);
@@ -823,7 +837,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
         tc::fence_after_sync();
-        const int ok = sh.tile_ok[tile & 7];
+        const int ok = sh.k_ok[tile & (kSegs - 1)];
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
@@ -841,7 +855,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (u < 64)
 #pragma unroll 1
               for (int r = 0; r < C::NH; ++r) {
-                const uint2 w = sh.row_path[rb][c0 + r];
+                const uint2 w = sh.row_path[c0 + r];
                 vis |= (((u < 32 ? w.x : w.y) >> (u & 31)) & 1) << r;
               }
           }
@@ -961,9 +975,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.s_empty[buf]), mbar_arrive(&sh.p_full[buf]);
       }
+      // S^T's products are done, and Q is free: the next rows are on their way
+      // while this item is written
+      const Seg e = s;
+      ++seg_no;
+      more = next_seg();
+      --seg_no;
+      if (more) attn_rows_copy<D, NT>(a, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
       // ---- epilogue
-      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-      const int64_t item = (int64_t)s.b * a.N * a.Hq + s.h * a.G;  // output row of node 0
+      const bool whole = e.t0 == 0 && e.t1 == e.tiles;
+      const int64_t item = (int64_t)e.b * a.N * a.Hq + e.h * a.G;  // output row of node 0
       const int64_t slot = 2 * (int64_t)blockIdx.x + (seg_no > 0);
       {
         float x[C::NH];
@@ -972,8 +993,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const float sum = warp_transpose_reduce(x, [](float p, float q) { return p + q; });
         if (lane < C::NH) sh.part[quarter][c0 + lane] = sum;
       }
-      if (s.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
-        join = {item, s.h, s.row0, s.rows, (int)slot, s.last};
+      if (e.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
+        join = {item, e.h, e.row0, e.rows, (int)slot, e.last};
       tc::named_barrier(1 + group, 128);
       if (gt < C::NH) {
         const int r = c0 + gt;
@@ -981,9 +1002,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const float m = -reinterpret_cast<const float*>(&sh.cm[r / 2])[2 + (r & 1)];
         float inv = 1.f;
         if (whole) {
-          inv = total != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[s.h] : 1.f) / total : 0.f;
-          if (a.lse != nullptr && r < s.rows)
-            a.lse[item + sh.row_at[rb][r]] =
+          inv = total != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[e.h] : 1.f) / total : 0.f;
+          if (a.lse != nullptr && r < e.rows)
+            a.lse[item + sh.row_at[r]] =
                 total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
         } else {
           a.part_ml[slot * NT + r] = make_float2(m, total);
@@ -1003,12 +1024,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         tc::tmem_wait_ld(o[0]);
         if constexpr (C::NH == 32) tc::tmem_ready(o[1]);
         if (D < 128 && ch >= D) continue;
-        const int rows = s.rows - c0;
+        const int rows = e.rows - c0;
         if (whole) {
           uint16_t* out = static_cast<uint16_t*>(a.o) + item * D + ch;
 #pragma unroll
           for (int i = 0; i < C::NH; i += 4) {
-            const int4 at = *reinterpret_cast<const int4*>(&sh.row_at[rb][c0 + i]);
+            const int4 at = *reinterpret_cast<const int4*>(&sh.row_at[c0 + i]);
             const float4 inv = *reinterpret_cast<const float4*>(&sh.inv[c0 + i]);
             const int at_[4] = {at.x, at.y, at.z, at.w};
             const float inv_[4] = {inv.x, inv.y, inv.z, inv.w};
@@ -1031,7 +1052,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.row_empty[rb]);
+      if (lane == 0) mbar_arrive(&sh.o_empty);
     }
     if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = join;
   } else if (warp == 20) {
@@ -1039,11 +1060,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     constexpr uint32_t id = idesc_f16(NT, false);
     // descriptors advance by 16-byte units in their low word
     const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oQ), 16, 1024);
-    int tile = 0, qs = 0, ku = 0;
-    unsigned ku_ph = 0, q_ph = 0;
+    int tile = 0, ku = 0;
+    unsigned ku_ph = 0;
     for (; next_seg(); ++seg_no) {
-      attn_wait(&sh.q_full[qs], q_ph, dead);
-      const uint64_t q = desc + (uint32_t)(qs * (C::QB >> 4));
+      attn_wait(&sh.q_full, seg_no & 1, dead);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int buf = tile & 1;
@@ -1057,12 +1077,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           if (elect_one() && live) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(d, k0 * 32 + k * 8, q + (u * NT * 128 + k * 32) / 16, id, u > 0 || k > 0);
+              mma_ts(d, k0 * 32 + k * 8, desc + (u * NT * 128 + k * 32) / 16, id, u > 0 || k > 0);
             tc::mma_commit(&sh.k_empty[k0]);
-            if (u + 1 == C::UNITS) {
-              tc::mma_commit(&sh.s_full[buf]);
-              if (t + 1 == s.t1) tc::mma_commit(&sh.q_empty[qs]);
-            }
+            if (u + 1 == C::UNITS) tc::mma_commit(&sh.s_full[buf]);
           }
         }
         if (C::UNITS < C::KU) {
@@ -1072,7 +1089,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           ku_ph ^= 1;
         }
       }
-      if (++qs == C::NQ) qs = 0, q_ph ^= 1;
     }
   } else if (warp == 21) {
     // ------------------------------------------------ O^T products (one elected lane)
@@ -1110,78 +1126,70 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         if ((4 / C::VU) & 1) vu_ph ^= 1;
       }
     }
-  } else if (warp == 23) {
-    // ------------------------------------------------ segments and records in
+  } else {
+    // ------------------------------------------------ the records' K halves (and the
+    // run's segments), or their V halves
+    const bool is_k = warp == 22;
     const Lens lens = {a, sh.len};
-    Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
-    Seg f = {};  // the copies run ahead of the conversion
-    int f_t = 0, f_seg = 0, f_tile = 0, f_stage = 0, page = 0;
-    bool f_on = true;
+    Run run;
+    if (is_k) run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    uint64_t* full = is_k ? sh.kr_full : sh.vr_full;
+    uint64_t* empty = is_k ? sh.kr_empty : sh.vr_empty;
+    int* oks = is_k ? sh.k_ok : sh.v_ok;
+    uint8_t* ring = smem + (is_k ? C::oK : C::oV);
+    const int stages = is_k ? C::KR : C::VR;
+    // lanes 2r and 2r + 1: codes and scales of record r
+    const int r = lane >> 1, part = lane & 1;
+    const int from = part == 0 ? (is_k ? 0 : off_v(D)) : (is_k ? off_ks(D) : off_vs(D));
+    const int bytes = part == 0 ? 16 * D : 2 * D;
+    int stage = 0, tile = 0;
     unsigned empty_ph = 1;
-    // the next tile to copy: its segment published, its page numbers on their way
-    auto look_ahead = [&]() {
-      if (f_t == f.t1) {
-        f = attn_seg(a, lens, run);
-        f_t = f.t0;
-        f_on = f.t1 > 0;
-        const int i = f_seg & (kSegs - 1);
-        attn_wait(&sh.seg_empty[i], ((f_seg / kSegs) & 1) ^ 1, dead);
+    for (;; ++seg_no) {
+      if (is_k) {
+        s = attn_seg(a, lens, run);
+        const int i = seg_no & (kSegs - 1);
+        attn_wait(&sh.seg_empty[i], ((seg_no / kSegs) & 1) ^ 1, dead);
         if (lane == 0) {
-          sh.seg[i] = f;
+          sh.seg[i] = s;
           mbar_arrive(&sh.seg_full[i]);
         }
-        ++f_seg;
+        if (s.t1 == 0) break;
+      } else if (!next_seg()) {
+        break;
       }
-      const int pos = f_t * kTile + lane * kRec;
-      page = f_on && lane < 4 && pos < f.len
-                 ? a.c.table[(int64_t)f.b * a.c.table_stride + pos / a.c.page_tokens]
-                 : -1;
-    };
-    auto fetch = [&]() {
-      attn_wait(&sh.raw_empty[f_stage], empty_ph, dead);
-      const int pos = f_t * kTile + lane * kRec;
-      const bool want = lane < 4 && pos < f.len;  // past the end: nothing to read
-      const bool have = want && page >= 0 && page < a.c.n_pages;
-      if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
-      const unsigned good = __ballot_sync(0xffffffffu, have || !want) & 15u;
-      const unsigned copies = __ballot_sync(0xffffffffu, have);
-      if (lane == 0) {
-        sh.tile_ok[f_tile & 7] = (int)good;
-        mbar_arrive_expect_tx(&sh.raw_full[f_stage], __popc(copies) * rec_bytes(D));
-      }
-      __syncwarp();
-      if (have) {
-        const int recs = a.c.page_tokens / kRec;
-        const uint8_t* src =
-            static_cast<const uint8_t*>(a.c.pages) + (int64_t)page * a.c.page_stride +
-            ((int64_t)f.h * recs + pos % a.c.page_tokens / kRec) * rec_bytes(D);
-        bulk_g2s(smem + C::oRaw + f_stage * C::RAW + lane * rec_bytes(D), src, rec_bytes(D),
-                 &sh.raw_full[f_stage]);
-      }
-      if (++f_stage == C::NRAW) f_stage = 0, empty_ph ^= 1;
-      ++f_tile;
-      ++f_t;
-      look_ahead();
-    };
-    look_ahead();
+      const int32_t* table = a.c.table + (int64_t)s.b * a.c.table_stride;
+      const int recs = a.c.page_tokens / kRec;
+      // page numbers are looked up a tile ahead
+      int pos = s.t0 * kTile + r * kRec;
+      int page = lane < 8 && pos < s.len ? table[pos / a.c.page_tokens] : -1;
 #pragma unroll 1
-    while (f_on) fetch();
-    if (*dead) {  // copies in flight land before the block's memory is given back
-      for (int i = 0; i < C::NRAW && i < f_tile; ++i)
-        (void)mbar_wait_bounded(&sh.raw_full[i], ((f_tile - i - 1) / C::NRAW) & 1, kWaitPolls);
-    }
-  } else {
-    // ------------------------------------------------ queries of the segments after the first
-    int qb = 0;
-    unsigned ph = 1;
-    for (; next_seg(); ++seg_no) {
-      attn_wait(&sh.q_empty[qb], ph, dead);
-      attn_wait(&sh.row_empty[seg_no & 1], ((seg_no >> 1) & 1) ^ 1, dead);
-      if (seg_no > 0) {
-        attn_rows<D, NT>(a, sh, s, smem + C::oQ + qb * C::QB, seg_no & 1, 0, 1);
-        if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.row_full[seg_no & 1]);
+      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+        const bool want = lane < 8 && pos < s.len;  // past the end: nothing to read
+        const bool have = want && page >= 0 && page < a.c.n_pages;
+        if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
+        const uint8_t* src = static_cast<const uint8_t*>(a.c.pages);
+        if (have)
+          src += (int64_t)page * a.c.page_stride + from +
+                 ((int64_t)s.h * recs + pos % a.c.page_tokens / kRec) * rec_bytes(D);
+        pos += kTile;
+        page = lane < 8 && t + 1 < s.t1 && pos < s.len ? table[pos / a.c.page_tokens] : -1;
+        const unsigned good = __ballot_sync(0xffffffffu, have || !want);
+        const unsigned copies = __ballot_sync(0xffffffffu, have) & 0x55u;
+        attn_wait(&empty[stage], empty_ph, dead);
+        if (lane == 0) {
+          oks[tile & (kSegs - 1)] =
+              (good & 1) | ((good >> 1) & 2) | ((good >> 2) & 4) | ((good >> 3) & 8);
+          mbar_arrive_expect_tx(&full[stage], __popc(copies) * C::HALF);
+        }
+        __syncwarp();
+        if (have)
+          bulk_g2s(ring + stage * C::RAW + r * C::HALF + part * 16 * D, src, bytes, &full[stage]);
+        if (++stage == stages) stage = 0, empty_ph ^= 1;
       }
-      if (++qb == C::NQ) qb = 0, ph ^= 1;
+    }
+    if (__any_sync(0xffffffffu, *dead)) {  // copies in flight land before the block ends
+      for (int i = 0; i < stages && i < tile; ++i)
+        (void)mbar_wait_bounded(&full[i], ((tile - i - 1) / stages) & 1, kWaitPolls);
     }
   }
   // every role is done with its loops, hence with its copies and products; after a
