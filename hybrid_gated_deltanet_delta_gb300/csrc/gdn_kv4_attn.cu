@@ -21,7 +21,7 @@ int blocks() {
     (void)cudaGetLastError();
     return 0;
   }
-  return sms < 1024 ? sms : 1024;
+  return sms;
 }
 
 void row_tiles(int rows, int* tiles, int* per_tile) {
@@ -60,6 +60,11 @@ int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64
   a.rows_total = N * a.G;
   row_tiles(a.rows_total, &a.row_tiles, &a.rows_per_tile);
   a.bf16 = dtype == GDN_BF16;
+  // the kernels count tiles in 32 bits
+  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128;
+  if ((int64_t)a.row_tiles * c.B > INT32_MAX / c.Hkv ||
+      (int64_t)a.row_tiles * c.B * c.Hkv > INT32_MAX / tiles)
+    return GDN_ERR_UNSUPPORTED;
   const int NT = round_rows(a.rows_per_tile);
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * parts * NT * c.D);

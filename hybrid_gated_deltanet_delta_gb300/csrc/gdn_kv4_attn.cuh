@@ -51,7 +51,6 @@ namespace gdn {
 namespace kv4 {
 
 constexpr int kTile = 128;  // positions of a tile: four records
-constexpr int kAttnThreads = 768;
 constexpr float kNone = -1e30f;      // reference of a row that has seen nothing
 constexpr unsigned kMostP = 0x5c00;  // 2^8 in binary16: the largest p before m moves
 constexpr float kLog2e = 1.4426950408889634f;
@@ -63,17 +62,17 @@ struct AttnCfg {
   static constexpr int MB = D == 256 ? 2 : 1;  // 128-channel blocks of O^T
   static constexpr int NS = NT < 64 ? 1 : NT / 32;  // softmax groups
   static constexpr int NH = NT / NS;                // rows of one
-  static constexpr int NK = NT < 96 ? 2 : 1;        // groups that dequantise K, and V
-  static constexpr int NV = 5 - NS - NK;
-  static constexpr int wV = 4 * NK, wS = wV + 4 * NV;  // first warps of the roles
-  static_assert(NV >= 1 && wS + 4 * NS == 20, "warps");
-  static constexpr int UNITS = D / 64;         // K units of a tile
-  // TMEM columns: K ring, two S^T, O^T, V ring.  The widest case keeps two
-  // stages per ring so that S^T can be double buffered.
-  static constexpr int KU = 3 * NT + 128 + 64 * MB > 512 - (MB - 1) * NT ? 2 : 4;
-  static constexpr int VU = KU;
-  static constexpr int cS = 32 * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
-  static_assert(cV + VU * 16 * MB <= 512, "TMEM");
+  static constexpr int wV = 4, wS = 8;  // first warps of the roles
+  static constexpr int wI = wS + 4 * NS, THREADS = 32 * (wI + 4);
+  // TMEM columns: two K units (KW columns of 2 channels each), two S^T, O^T, two V units
+  // (VW records each).  Large units cost fewer hand-overs; the widest case has no
+  // room for them.
+  static constexpr bool BIG = 128 + 64 * MB + (2 + MB) * NT <= 512;
+  static constexpr int KW = BIG && D >= 128 ? 64 : 32, VW = BIG ? 2 : 1;
+  static constexpr int UNITS = D / 2 / KW, VUNITS = 4 / VW;  // of a tile
+  static constexpr int KU = 2, VU = 2;
+  static constexpr int cS = KW * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
+  static_assert(cV + VU * VW * 16 * MB <= 512, "TMEM");
   // shared memory
   static constexpr int HALF = 18 * D;          // of a record: K's or V's codes and scales
   static constexpr int RAW = 4 * HALF;         // a stage of either ring
@@ -81,7 +80,7 @@ struct AttnCfg {
   static constexpr int PB = (NT > 64 ? 2 : 1) * kTile * 128;
   static constexpr int VSG = 272;  // bytes between the scale rows of two groups (bank offset)
   static constexpr int VSB = D / 16 * VSG;
-  static constexpr int ROOM = (220 * 1024 - QB - 2 * PB - 2 * VSB) / RAW;
+  static constexpr int ROOM = (214 * 1024 - QB - 2 * PB - 2 * VSB) / RAW;
   static constexpr int KR = ROOM / 2 > 6 ? 6 : ROOM / 2;
   static constexpr int VR = ROOM - KR > 6 ? 6 : ROOM - KR;
   static_assert(KR >= 2 && VR >= 2, "stages");
@@ -97,8 +96,32 @@ struct Seg {
   int last;  // block that holds the item's last tile
 };
 
-constexpr int kSegs = 16;    // ring of segments and of tiles' page checks; a block's warps are
-                             // fewer tiles apart
+// Equal runs of `total` tiles for at most `parts` blocks: the first `extra` runs
+// have one tile more.  (The host keeps the count of tiles below 2^31.)
+struct Runs {
+  int each, extra, parts;
+  Runs() = default;
+  __device__ __forceinline__ Runs(int total, int n) {
+    parts = min(total, n);  // no empty runs in between
+    each = parts > 0 ? total / parts : 0;
+    extra = total - each * parts;
+  }
+  __device__ __forceinline__ int start(int part) const { return each * part + min(part, extra); }
+  // the run that holds tile x
+  __device__ __forceinline__ int of(int x) const {
+    const int head = extra * (each + 1);
+    return x < head ? x / (each + 1) : extra + (x - head) / each;
+  }
+};
+
+// Walks the tiles of a block's run, item by item (one warp).
+struct Run {
+  int b, h, rt, t0, at, left;
+  Runs runs;
+};
+
+constexpr int kSegs = 16;    // ring of segments
+constexpr int kTiles = 32;   // ring of tiles' page checks; copies are fewer tiles ahead
 constexpr int kLens = 1024;  // lengths kept in shared memory
 
 template <typename C>
@@ -110,7 +133,7 @@ struct AttnShared {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int dead;
-  int k_ok[kSegs], v_ok[kSegs];  // records of a tile that could be read, by tile number
+  int k_ok[kTiles], v_ok[kTiles];  // records of a tile that could be read, by tile number
   Seg seg[kSegs];
   // of the query rows: c (logit of S: c * S, log2 units), the row of
   // the output from the item's first node and head on, and for trees the
@@ -122,6 +145,7 @@ struct AttnShared {
   alignas(16) float4 cm[C::NT / 2]; // rows in work, by pairs: c, c, -m, -m
   alignas(16) float alpha[C::NT], inv[C::NT];
   float part[4][C::NT];             // of a softmax group's four warps
+  Run run;
   int len[kLens];
 };
 
@@ -295,11 +319,7 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, int len, int rt) {
   return see <= 0 ? 0 : (see + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
 // The lengths the block works with: the first kLens are kept in shared memory.
 struct Lens {
@@ -311,131 +331,104 @@ struct Lens {
 };
 
 // Lengths into shared memory, by all threads: a thread a sequence, or for
-// trees a warp a sequence (its lanes check the nodes).
-__device__ __forceinline__ void attn_lens(const AttnArgs& a, int* kept, bool report_it) {
-  if (a.parent == nullptr) {
+// trees a warp a sequence (its lanes check the nodes).  Returns whether any of
+// this thread's differs from what was there.
+static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, bool report_it) {
+  bool changed = false;
+  const int lane = threadIdx.x & 31, n_kept = min(a.c.B, kLens);
+  const int unit = a.parent == nullptr ? 1 : 32;  // threads of a sequence
 #pragma unroll 1
-    for (int b = threadIdx.x; b < min(a.c.B, kLens); b += blockDim.x)
-      kept[b] = seq_len(a.c, b, report_it);
-    return;
-  }
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int b = threadIdx.x >> 5; b < min(a.c.B, kLens); b += blockDim.x >> 5) {
-    const int32_t* p = a.parent + (int64_t)b * a.N;
+  for (int b = threadIdx.x / unit; b < n_kept; b += blockDim.x / unit) {
     bool ok = true;
-    for (int n = lane; n < a.N; n += 32) ok = ok && (n == 0 ? p[n] == -1 : p[n] >= 0 && p[n] < n);
-    ok = __all_sync(0xffffffffu, ok);
-    if (lane == 0) {
-      const int len = seq_len(a.c, b, report_it);
-      if (report_it && len > 0 && !ok) report(a.c.status, GDN_ERR_BAD_TREE);
-      kept[b] = ok ? len : 0;
+    if (a.parent != nullptr) {
+      const volatile int32_t* p = a.parent + (int64_t)b * a.N;
+#pragma unroll 1
+      for (int n = lane; n < a.N; n += 32) {
+        const int up = p[n];
+        ok = ok && (n == 0 ? up == -1 : up >= 0 && up < n);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane != 0) continue;
     }
+    int len = *(const volatile int32_t*)(a.c.kv_len + b);
+    if (len < 0 || (int64_t)len > (int64_t)a.c.max_pages * a.c.page_tokens) {
+      if (report_it) report(a.c.status, GDN_ERR_ROW_RANGE);
+      len = 0;
+    }
+    if (!ok) {
+      if (report_it && len > 0) report(a.c.status, GDN_ERR_BAD_TREE);
+      len = 0;
+    }
+    changed |= kept[b] != len;
+    kept[b] = len;
   }
   if (report_it)  // the others' reports (their lengths are looked up when needed)
 #pragma unroll 1
     for (int b = kLens + threadIdx.x; b < a.c.B; b += blockDim.x) (void)attn_len(a, b, true);
+  return changed;
 }
 
 // Tiles of sequence b over all heads, by a whole warp.
-__device__ __forceinline__ int64_t warp_cost(const AttnArgs& a, int len) {
-  int64_t t = 0;
+__device__ __forceinline__ int warp_cost(const AttnArgs& a, int len) {
+  int t = 0;
 #pragma unroll 1
   for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_tiles(a, len, rt);
   return warp_sum(t) * a.c.Hkv;
 }
 
-// Equal runs of `total` tiles for at most `parts` blocks: the first `extra` runs
-// have one tile more.
-struct Runs {
-  int64_t each, extra;
-  int parts;
-  Runs() = default;
-  __device__ __forceinline__ Runs(int64_t total, int n) {
-    parts = total < n ? (int)total : n;  // no empty runs in between
-    each = parts > 0 ? total / parts : 0;
-    extra = total - each * parts;
-  }
-  __device__ __forceinline__ int64_t start(int part) const {
-    return each * part + (part < extra ? part : extra);
-  }
-  // the run that holds tile x
-  __device__ __forceinline__ int of(int64_t x) const {
-    const int64_t head = extra * (each + 1);
-    return (int)(x < head ? x / (each + 1) : extra + (x - head) / each);
-  }
-};
-
-// Walks the tiles of a block's run, item by item (one warp).
-struct Run {
-  int b, h, rt, t0;
-  int64_t at, left;
-  Runs runs;
-};
-
 // The run of block `part` of `parts`: the tiles of all sequences are counted,
 // then the sequence that holds the run's first tile is taken apart.
-static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens, int part, int parts) {
+static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens, int part,
+                                            int parts) {
   const int lane = threadIdx.x & 31;
   const bool by_lane = a.row_tiles <= 4;  // a lane a sequence, or the warp a sequence
-  int64_t total = 0;
+  const int step = by_lane ? 32 : 1;
+  // tiles of the sequence b0 + lane, or (of all lanes the same) of b0
+  auto tiles = [&](int b0) {
+    if (!by_lane) return warp_cost(a, lens(b0));
+    int x = 0;
+    if (b0 + lane < a.c.B) {
+      const int len = lens(b0 + lane);
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.c.B; b0 += by_lane ? 32 : 1) {
-    if (by_lane) {
-      if (b0 + lane < a.c.B) {
-        const int len = lens(b0 + lane);
-#pragma unroll 1
-        for (int rt = 0; rt < a.row_tiles; ++rt) total += attn_tiles(a, len, rt);
-      }
-    } else {
-      total += warp_cost(a, lens(b0));
+      for (int rt = 0; rt < a.row_tiles; ++rt) x += attn_tiles(a, len, rt);
     }
+    return x * a.c.Hkv;
+  };
+  int total = 0, mine = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.c.B; b0 += step) {
+    mine = tiles(b0);
+    total += by_lane ? warp_sum(mine) : mine;
   }
-  if (by_lane) total = warp_sum(total) * a.c.Hkv;
-  const Runs runs(total, parts);
-  Run r = {0, 0, 0, 0, 0, 0, runs};
-  if (part >= runs.parts) return r;
-  const int64_t start = runs.start(part);
-  r.at = start;
-  r.left = runs.start(part + 1) - start;
-  int64_t before = 0, its = 0;
+  Run r = {0, 0, 0, 0, 0, 0, Runs(total, parts)};
+  if (part >= r.runs.parts) return r;
+  r.at = r.runs.start(part);
+  r.left = r.runs.start(part + 1) - r.at;
+  int before = 0, its = 0;
 #pragma unroll 1
-  for (int b0 = 0;; b0 += by_lane ? 32 : 1) {
+  for (int b0 = 0;; b0 += step) {
+    if (a.c.B > step) mine = tiles(b0);  // else it is still there
+    int upto = mine;
     if (by_lane) {
-      int64_t mine = 0;
-      if (b0 + lane < a.c.B) {
-        const int len = lens(b0 + lane);
-#pragma unroll 1
-        for (int rt = 0; rt < a.row_tiles; ++rt) mine += attn_tiles(a, len, rt);
-        mine *= a.c.Hkv;
-      }
-      int64_t x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + x > start);
-      if (hit == 0) {
-        before += __shfl_sync(0xffffffffu, x, 31);
-        continue;
-      }
-      const int l = __ffs(hit) - 1;
-      its = __shfl_sync(0xffffffffu, mine, l);
-      before += __shfl_sync(0xffffffffu, x, l) - its;
-      r.b = b0 + l;
-    } else {
-      its = warp_cost(a, lens(b0));
-      if (before + its <= start) {
-        before += its;
-        continue;
-      }
-      r.b = b0;
     }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > r.at);
+    if (hit == 0) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int l = by_lane ? __ffs(hit) - 1 : 0;
+    its = __shfl_sync(0xffffffffu, mine, l);
+    before += __shfl_sync(0xffffffffu, upto, l) - its;
+    r.b = b0 + l;
     break;
   }
-  int in = (int)(start - before);  // of the sequence's its tiles
-  const int per_head = (int)(its / a.c.Hkv), len = lens(r.b);
+  int in = r.at - before;  // of the sequence's `its` tiles
+  const int per_head = its / a.c.Hkv, len = lens(r.b);
   r.h = in / per_head;
   in -= r.h * per_head;
 #pragma unroll 1
@@ -463,7 +456,7 @@ static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens& lens,
     }
     if (tiles <= t0) continue;
     s.b = b, s.h = h, s.t0 = t0, s.tiles = tiles, s.len = len;
-    s.t1 = r.left < tiles - t0 ? t0 + (int)r.left : tiles;
+    s.t1 = min(t0 + r.left, tiles);
     r.left -= s.t1 - t0;
     r.at += s.t1 - t0;
     s.last = s.t1 < tiles ? r.runs.of(r.at + tiles - s.t1 - 1) : 0;
@@ -545,7 +538,7 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
       path[i] = 1ull << m;
     }
 #pragma unroll 1
-    for (int k = 0; k < 6; ++k) {
+    while (__any_sync(0xffffffffu, to[0] >= 0 || to[1] >= 0)) {
       int next[2];
       unsigned long long more[2];
 #pragma unroll
@@ -618,7 +611,7 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
 
 // ---------------------------------------------------------------- the kernel
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   using C = AttnCfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShared<C> sh;
@@ -628,9 +621,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KR; ++i)
-      mbar_init(&sh.kr_full[i], 1), mbar_init(&sh.kr_empty[i], 4 * C::NK);
+      mbar_init(&sh.kr_full[i], 1), mbar_init(&sh.kr_empty[i], 4);
     for (int i = 0; i < C::VR; ++i)
-      mbar_init(&sh.vr_full[i], 1), mbar_init(&sh.vr_empty[i], 4 * C::NV);
+      mbar_init(&sh.vr_full[i], 1), mbar_init(&sh.vr_empty[i], 4);
     for (int i = 0; i < C::KU; ++i) mbar_init(&sh.k_full[i], 4), mbar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < C::VU; ++i) mbar_init(&sh.v_full[i], 4), mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -638,18 +631,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       mbar_init(&sh.p_full[i], 4 * C::NS), mbar_init(&sh.p_empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], 23);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], C::wI + 3);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.o_empty, 4 * C::NS);
     mbar_init(&sh.drain, 2);
     sh.dead = 0;
     mbar_init_fence();
   }
-  if (warp == 20) tc::tmem_alloc(&sh.tmem, 512);
-  pdl_enter();
-  attn_lens(a, sh.len, blockIdx.x == 0);
-  tc::fence_before_sync();
+  if (warp == C::wI) tc::tmem_alloc(&sh.tmem, 512);
+  // The block's run follows from the lengths alone.  It is worked out before the
+  // wait on the kernel before this one, from the lengths as they read then, and
+  // again after it in the case that one of them has changed (with more sequences
+  // than are kept, always).
+  const Lens lens = {a, sh.len};
+  const bool kept = a.c.B <= kLens;
+  (void)attn_lens(a, sh.len, false);
   __syncthreads();
+  if (warp == C::wI + 2 && kept) {
+    const Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    if (lane == 0) sh.run = run;
+  }
+  __syncthreads();
+  pdl_enter();
+  const bool changed = attn_lens(a, sh.len, blockIdx.x == 0);
+  tc::fence_before_sync();
+  const bool again = __syncthreads_or(changed) || !kept;
   tc::fence_after_sync();
   // all 512 columns are this block's, so its tensor memory begins at address 0, and
   // the addresses below are column numbers known at compile time
@@ -669,77 +675,61 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 
   if (warp < C::wV) {
     // ------------------------------------------------ K -> TMEM
-    const int group = warp >> 2, quarter = warp & 3;
-    const uint32_t dst = (uint32_t)(quarter * 32) << 16;
-    int stage = 0, unit = C::UNITS >= C::NK ? group : 0, tile = 0;
+    // A unit in two halves of 32 channels: the first is on its way to TMEM, and the
+    // next one's bytes to registers, while the second is converted.
+    const uint32_t dst = (uint32_t)(warp * 32) << 16;
+    int stage = 0, unit = 0;
     unsigned raw_ph = 0, unit_ph = 1;  // an empty ring's first pass does not wait
     for (; next_seg(); ++seg_no) {
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+      for (int t = s.t0; t < s.t1; ++t) {
         attn_wait(&sh.kr_full[stage], raw_ph, dead);
-        const uint8_t* rec = smem + C::oK + stage * C::RAW + quarter * C::HALF;
-        if (C::UNITS >= C::NK || (tile & 1) == group) {
-          // the next unit's bytes are on their way while this one is converted
-          uint4 lo, hi;
-          uint32_t s8;
-          auto load = [&](int u) {
-            lo = *reinterpret_cast<const uint4*>(rec + 2 * u * 512 + lane * 16);
-            hi = *reinterpret_cast<const uint4*>(rec + (2 * u + 1) * 512 + lane * 16);
-            s8 = *reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * (D / 16) + u * 4);
-          };
-          constexpr int STEP = C::UNITS >= C::NK ? C::NK : 1;
-          const int u0 = C::UNITS >= C::NK ? group : 0;
-          if (C::UNITS < C::NK) {
-            // this tile's unit: every other one of the ring
-            unit = tile % C::KU;
-            unit_ph = ((tile / C::KU) & 1) ^ 1;
-          }
-          load(u0);
+        const uint8_t* rec = smem + C::oK + stage * C::RAW + warp * C::HALF + lane * 16;
+        const uint8_t* scales = smem + C::oK + stage * C::RAW + warp * C::HALF + 16 * D +
+                                lane * (D / 16);
+        uint4 q4 = *reinterpret_cast<const uint4*>(rec);
 #pragma unroll
-          for (int i = 0; i < C::UNITS; i += STEP) {
-            uint32_t w[32];
-            const uint32_t sa = e4m3x2(s8), sb = e4m3x2(s8 >> 16);
-            const uint32_t g0 = __byte_perm(sa, sa, 0x1010), g1 = __byte_perm(sa, sa, 0x3232);
-            const uint32_t g2 = __byte_perm(sb, sb, 0x1010), g3 = __byte_perm(sb, sb, 0x3232);
-            dequant8(lo.x, g0, w);
-            dequant8(lo.y, g0, w + 4);
-            dequant8(lo.z, g1, w + 8);
-            dequant8(lo.w, g1, w + 12);
-            dequant8(hi.x, g2, w + 16);
-            dequant8(hi.y, g2, w + 20);
-            dequant8(hi.z, g3, w + 24);
-            dequant8(hi.w, g3, w + 28);
-            if (i + STEP < C::UNITS) load(u0 + i + STEP);
-            attn_wait(&sh.k_empty[unit], unit_ph, dead);
-            tc::fence_after_sync();
-            tmem_st16(dst + unit * 32, w);
-            tmem_st16(dst + unit * 32 + 16, w + 16);
-            tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.k_full[unit]);
-            if (C::UNITS >= C::NK) {
-              unit += C::NK;
-              if (unit >= C::KU) unit -= C::KU, unit_ph ^= 1;
+        for (int u = 0; u < C::UNITS; ++u) {
+#pragma unroll
+          for (int k = 0; k < C::KW / 16; ++k) {  // 32 channels: one 16-byte chunk
+            const int chunk = u * (C::KW / 16) + k;
+            const uint4 now = q4;
+            if (chunk + 1 < D / 32) q4 = *reinterpret_cast<const uint4*>(rec + (chunk + 1) * 512);
+            const uint32_t sc =
+                e4m3x2(*reinterpret_cast<const uint16_t*>(scales + 2 * chunk));
+            const uint32_t g = __byte_perm(sc, sc, 0x1010), h = __byte_perm(sc, sc, 0x3232);
+            uint32_t w[16];
+            dequant8(now.x, g, w);
+            dequant8(now.y, g, w + 4);
+            dequant8(now.z, h, w + 8);
+            dequant8(now.w, h, w + 12);
+            if (k == 0) {
+              attn_wait(&sh.k_empty[unit], unit_ph, dead);
+              tc::fence_after_sync();
             }
+            tmem_st16(dst + unit * C::KW + k * 16, w);
           }
+          tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.k_full[unit]);
+          if (++unit == C::KU) unit = 0, unit_ph ^= 1;
         }
-        __syncwarp();
         if (lane == 0) mbar_arrive(&sh.kr_empty[stage]);
         if (++stage == C::KR) stage = 0, raw_ph ^= 1;
       }
     }
   } else if (warp < C::wS) {
     // ------------------------------------------------ V^T -> TMEM
-    const int group = (warp - C::wV) >> 2, quarter = warp & 3;
+    const int quarter = warp & 3;
     const uint32_t dst = ((uint32_t)(quarter * 32) << 16) + C::cV;
-    if (group == 0) attn_zero(a, Lens{a, sh.len}, D, threadIdx.x - 32 * C::wV);
     const int vt = threadIdx.x - 32 * C::wV;
-    int stage = 0, unit = group, tile = 0;
+    attn_zero(a, lens, D, vt);
+    int stage = 0, unit = 0, tile = 0;
     unsigned raw_ph = 0, unit_ph = 1;
     for (;; ++seg_no) {
       // all of them go on, or none: they meet at a barrier below
-      if (barrier_any(5, 128 * C::NV, !next_seg())) break;
+      if (barrier_any(5, 128, !next_seg())) break;
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         attn_wait(&sh.vr_full[stage], raw_ph, dead);
@@ -747,10 +737,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         // the tile's scales to binary16, 8 positions of a group a step; those past
         // the end, or on a page that is not there, count as 0
         uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
-        const int ok = sh.v_ok[tile & (kSegs - 1)], end = s.len - t * kTile;
+        const int ok = sh.v_ok[tile & (kTiles - 1)], end = s.len - t * kTile;
         const bool full = ok == 15 && end >= kTile;
 #pragma unroll
-        for (int i = vt; i < D; i += 128 * C::NV) {
+        for (int i = vt; i < D; i += 128) {
           const int r = i / (D / 4), go = i % (D / 4);
           const uint2 s8 =
               *reinterpret_cast<const uint2*>(raw + r * C::HALF + 16 * D + go * 8);
@@ -764,49 +754,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           *reinterpret_cast<uint4*>(vs + (go >> 2) * C::VSG + r * 64 + (go & 3) * 16) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
-        tc::named_barrier(5, 128 * C::NV);  // also: the other buffer's readers are done
-#pragma unroll 1
-        for (int r = group; r < 4; r += C::NV) {
-          uint32_t w[C::MB][16];
+        tc::named_barrier(5, 128);  // also: the other buffer's readers are done
+        const int ch = quarter * 32 + lane;
+        const bool mine = D >= 128 || ch < D;  // D = 64: the upper lanes hold zeros
+        const uint8_t* codes = raw + (mine ? ch * 16 : 0);
+        const uint8_t* scales = vs + (ch >> 4) * C::VSG;
+        uint4 q4 = *reinterpret_cast<const uint4*>(codes);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
 #pragma unroll
           for (int mb = 0; mb < C::MB; ++mb) {
-            const int ch = mb * 128 + quarter * 32 + lane;
-            if (D >= 128 || ch < D) {
-              const uint4 q4 =
-                  *reinterpret_cast<const uint4*>(raw + r * C::HALF + ch * 16);
-              const uint4* sp = reinterpret_cast<const uint4*>(vs + (ch >> 4) * C::VSG + r * 64);
-              const uint32_t c4[4] = {q4.x, q4.y, q4.z, q4.w};
+            const uint32_t c4[4] = {q4.x, q4.y, q4.z, q4.w};
+            // the next 16 bytes: the other channel block's, or the next record's
+            const int next = r * C::MB + mb + 1;
+            if (next < 4 * C::MB)
+              q4 = *reinterpret_cast<const uint4*>(codes + next / C::MB * C::HALF +
+                                                   next % C::MB * 2048);
+            uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint4 s4 = sp[i];
-                w[mb][4 * i] = hmul2(e2m1x2<0>(c4[i]), s4.x);
-                w[mb][4 * i + 1] = hmul2(e2m1x2<1>(c4[i]), s4.y);
-                w[mb][4 * i + 2] = hmul2(e2m1x2<2>(c4[i]), s4.z);
-                w[mb][4 * i + 3] = hmul2(e2m1x2<3>(c4[i]), s4.w);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[mb][i] = 0;
+            for (int i = 0; i < 4; ++i) {
+              const uint4 s4 = mine ? *reinterpret_cast<const uint4*>(
+                                          scales + mb * 8 * C::VSG + r * 64 + i * 16)
+                                    : make_uint4(0, 0, 0, 0);
+              w[4 * i] = hmul2(e2m1x2<0>(c4[i]), s4.x);
+              w[4 * i + 1] = hmul2(e2m1x2<1>(c4[i]), s4.y);
+              w[4 * i + 2] = hmul2(e2m1x2<2>(c4[i]), s4.z);
+              w[4 * i + 3] = hmul2(e2m1x2<3>(c4[i]), s4.w);
             }
+            if (mb == 0 && r % C::VW == 0) {
+              attn_wait(&sh.v_empty[unit], unit_ph, dead);
+              tc::fence_after_sync();
+            }
+            tmem_st16(dst + ((unit * C::VW + r % C::VW) * C::MB + mb) * 16, w);
           }
-          attn_wait(&sh.v_empty[unit], unit_ph, dead);
-          tc::fence_after_sync();
-#pragma unroll
-          for (int mb = 0; mb < C::MB; ++mb)
-            tmem_st16(dst + unit * 16 * C::MB + mb * 16, w[mb]);
-          tmem_wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.v_full[unit]);
-          unit += C::NV;
-          if (unit >= C::VU) unit -= C::VU, unit_ph ^= 1;
+          if (r % C::VW == C::VW - 1) {
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_full[unit]);
+            if (++unit == C::VU) unit = 0, unit_ph ^= 1;
+          }
         }
-        __syncwarp();
         if (lane == 0) mbar_arrive(&sh.vr_empty[stage]);
         if (++stage == C::VR) stage = 0, raw_ph ^= 1;
       }
     }
-  } else if (warp < 20) {
+  } else if (warp < C::wI) {
     // ------------------------------------------------ softmax and epilogue
     const int group = (warp - C::wS) >> 2, quarter = warp & 3;
     const int c0 = group * C::NH;                      // first row of the group
@@ -837,7 +830,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
         tc::fence_after_sync();
-        const int ok = sh.k_ok[tile & (kSegs - 1)];
+        const int ok = sh.k_ok[tile & (kTiles - 1)];
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
@@ -1055,7 +1048,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(&sh.o_empty);
     }
     if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = join;
-  } else if (warp == 20) {
+  } else if (warp == C::wI) {
     // ------------------------------------------------ S^T products (one elected lane)
     constexpr uint32_t id = idesc_f16(NT, false);
     // descriptors advance by 16-byte units in their low word
@@ -1069,32 +1062,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int buf = tile & 1;
         attn_wait(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1, dead);
         const uint32_t d = C::cS + buf * NT;
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < C::UNITS; ++u) {
-          const int k0 = C::UNITS >= C::KU ? u % C::KU : ku + u;
-          const bool live = attn_wait(&sh.k_full[k0], ku_ph ^ (C::UNITS > C::KU && u >= C::KU), dead);
+          const bool live = attn_wait(&sh.k_full[ku], ku_ph, dead);
           tc::fence_after_sync();
+          const uint64_t q = desc + (uint32_t)(u * (C::KW / 32) * NT * 8);
+          const uint32_t ka = ku * C::KW;
           if (elect_one() && live) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(d, k0 * 32 + k * 8, desc + (u * NT * 128 + k * 32) / 16, id, u > 0 || k > 0);
-            tc::mma_commit(&sh.k_empty[k0]);
+            for (int k = 0; k < C::KW / 8; ++k)
+              mma_ts(d, ka + k * 8, q + (k / 4 * NT * 128 + k % 4 * 32) / 16, id, u > 0 || k > 0);
+            tc::mma_commit(&sh.k_empty[ku]);
             if (u + 1 == C::UNITS) tc::mma_commit(&sh.s_full[buf]);
           }
-        }
-        if (C::UNITS < C::KU) {
-          ku += C::UNITS;
-          if (ku == C::KU) ku = 0, ku_ph ^= 1;
-        } else if ((C::UNITS / C::KU) & 1) {
-          ku_ph ^= 1;
+          if (++ku == C::KU) ku = 0, ku_ph ^= 1;
         }
       }
     }
-  } else if (warp == 21) {
+  } else if (warp == C::wI + 1) {
     // ------------------------------------------------ O^T products (one elected lane)
     constexpr uint32_t id = idesc_f16(NT, true);
     const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
-    int tile = 0;
+    int tile = 0, vu = 0;
     unsigned vu_ph = 0;
     for (; next_seg(); ++seg_no) {
       attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
@@ -1103,36 +1092,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int buf = tile & 1;
         attn_wait(&sh.p_full[buf], (tile >> 1) & 1, dead);
         const uint64_t p = desc + (uint32_t)(buf * (C::PB >> 4));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          constexpr int VU = C::VU;
-          const int vu = r % VU;
-          const bool live = attn_wait(&sh.v_full[vu], vu_ph ^ (r >= VU), dead);
+#pragma unroll 1
+        for (int u = 0; u < C::VUNITS; ++u) {
+          const bool live = attn_wait(&sh.v_full[vu], vu_ph, dead);
           tc::fence_after_sync();
+          const uint64_t pu = p + (uint32_t)(u * C::VW * 256);
+          const uint32_t va = C::cV + vu * C::VW * C::MB * 16;
           if (elect_one() && live) {
 #pragma unroll
-            for (int mb = 0; mb < C::MB; ++mb) {
-              const uint32_t d = C::cO + mb * NT, va = C::cV + (vu * C::MB + mb) * 16;
-              mma_ts(d, va, p + r * 256, id, t > s.t0 || r > 0);
-              mma_ts(d, va + 8, p + r * 256 + 128, id, 1);
-            }
+            for (int r = 0; r < C::VW; ++r)
+#pragma unroll
+              for (int mb = 0; mb < C::MB; ++mb) {
+                const uint32_t d = C::cO + mb * NT, v = va + (r * C::MB + mb) * 16;
+                mma_ts(d, v, pu + r * 256, id, t > s.t0 || u > 0 || r > 0);
+                mma_ts(d, v + 8, pu + r * 256 + 128, id, 1);
+              }
             tc::mma_commit(&sh.v_empty[vu]);
-            if (r == 3) {
+            if (u + 1 == C::VUNITS) {
               tc::mma_commit(&sh.p_empty[buf]);
               if (t + 1 == s.t1) tc::mma_commit(&sh.o_full);
             }
           }
+          if (++vu == C::VU) vu = 0, vu_ph ^= 1;
         }
-        if ((4 / C::VU) & 1) vu_ph ^= 1;
       }
     }
   } else {
     // ------------------------------------------------ the records' K halves (and the
     // run's segments), or their V halves
-    const bool is_k = warp == 22;
-    const Lens lens = {a, sh.len};
-    Run run;
-    if (is_k) run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    const bool is_k = warp == C::wI + 2;
+    Run run = sh.run;
+    if (is_k && again) run = attn_run(a, lens, blockIdx.x, gridDim.x);
     uint64_t* full = is_k ? sh.kr_full : sh.vr_full;
     uint64_t* empty = is_k ? sh.kr_empty : sh.vr_empty;
     int* oks = is_k ? sh.k_ok : sh.v_ok;
@@ -1158,26 +1148,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         break;
       }
       const int32_t* table = a.c.table + (int64_t)s.b * a.c.table_stride;
-      const int recs = a.c.page_tokens / kRec;
-      // page numbers are looked up a tile ahead
+      const uint8_t* head = static_cast<const uint8_t*>(a.c.pages) + from +
+                            (int64_t)s.h * (a.c.page_tokens / kRec) * rec_bytes(D);
+      // this lane's position, as an entry of the table and an offset in the page, two
+      // tiles ahead of the copies: the page numbers are looked up that early
       int pos = s.t0 * kTile + r * kRec;
-      int page = lane < 8 && pos < s.len ? table[pos / a.c.page_tokens] : -1;
+      int entry = pos / a.c.page_tokens, off = pos % a.c.page_tokens;
+      const int entries = kTile / a.c.page_tokens, rest = kTile % a.c.page_tokens;
+      int page[3], offs[3];
+      auto look_up = [&](int i, int t) {
+        page[i] = lane < 8 && t < s.t1 && t * kTile + r * kRec < s.len ? table[entry] : -1;
+        offs[i] = off;
+        entry += entries;
+        off += rest;
+        if (off >= a.c.page_tokens) off -= a.c.page_tokens, ++entry;
+      };
+      look_up(0, s.t0);
+      look_up(1, s.t0 + 1);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const bool want = lane < 8 && pos < s.len;  // past the end: nothing to read
-        const bool have = want && page >= 0 && page < a.c.n_pages;
+        look_up(2, t + 2);
+        const bool have = want && page[0] >= 0 && page[0] < a.c.n_pages;
         if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
-        const uint8_t* src = static_cast<const uint8_t*>(a.c.pages);
+        const uint8_t* src = head;
         if (have)
-          src += (int64_t)page * a.c.page_stride + from +
-                 ((int64_t)s.h * recs + pos % a.c.page_tokens / kRec) * rec_bytes(D);
+          src += (int64_t)page[0] * a.c.page_stride + offs[0] / kRec * rec_bytes(D);
         pos += kTile;
-        page = lane < 8 && t + 1 < s.t1 && pos < s.len ? table[pos / a.c.page_tokens] : -1;
+        page[0] = page[1], offs[0] = offs[1], page[1] = page[2], offs[1] = offs[2];
         const unsigned good = __ballot_sync(0xffffffffu, have || !want);
         const unsigned copies = __ballot_sync(0xffffffffu, have) & 0x55u;
         attn_wait(&empty[stage], empty_ph, dead);
         if (lane == 0) {
-          oks[tile & (kSegs - 1)] =
+          oks[tile & (kTiles - 1)] =
               (good & 1) | ((good >> 1) & 2) | ((good >> 2) & 4) | ((good >> 3) & 8);
           mbar_arrive_expect_tx(&full[stage], __popc(copies) * C::HALF);
         }
@@ -1194,14 +1197,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   }
   // every role is done with its loops, hence with its copies and products; after a
   // wait that ran out, products in flight end (bounded) before TMEM is given back
-  if ((warp == 20 || warp == 21) && __any_sync(0xffffffffu, *dead)) {
+  if ((warp == C::wI || warp == C::wI + 1) && __any_sync(0xffffffffu, *dead)) {
     if (elect_one()) tc::mma_commit(&sh.drain);
     (void)mbar_wait_bounded(&sh.drain, 0, kWaitPolls);
   }
   tc::fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *dead) report(a.c.status, GDN_ERR_TIMEOUT);
-  if (warp == 20) {
+  if (warp == C::wI) {
     tc::fence_after_sync();
     tc::tmem_relinquish();
     tc::tmem_dealloc(sh.tmem, 512);
@@ -1209,77 +1212,69 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- join
-// Grid (blocks of the main kernel, rows): the item that block x left unfinished,
-// if any, row by row: the parts of blocks x .. last, in that order.  A thread
-// has four channels of every NP-th part.
+// Grid (blocks of the main kernel, pieces of the rows): the item that block x
+// left unfinished, if any: the parts of blocks x .. last, in that order.  A thread
+// has four channels, of one row; with few rows (NT = 16) the block's threads share
+// one row and take every NP-th part each, else each D/4 of them take a row.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;      // grid rows; more rows are taken in turn
-constexpr int kJoinParts = 1024;   // parts kept in shared memory: as many blocks at most
 
-template <int D>
+template <int D, bool ONE_ROW>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const __grid_constant__ AttnArgs a, int NT) {
-  constexpr int Q = D / 4, NP = kJoinThreads / Q;
-  __shared__ float weight[kJoinParts];
-  __shared__ float red[kJoinThreads / 32][2];
-  __shared__ __align__(16) float acc[NP][D];
+  constexpr int Q = D / 4, NP = kJoinThreads / Q, STEP = ONE_ROW ? NP : 1;
+  __shared__ __align__(16) float acc[ONE_ROW ? NP : 1][D];
+  __shared__ float sums[NP];
   pdl_enter();
   const AttnJoin j = a.join[blockIdx.x];
-  const int parts = j.rows > 0 ? j.last - (int)blockIdx.x + 1 : 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = threadIdx.x % Q, group = threadIdx.x / Q;
-  auto slot = [&](int i) { return i == 0 ? (int64_t)j.slot : 2 * ((int64_t)blockIdx.x + i); };
-  const float vsc = a.c.v_scale != nullptr ? a.c.v_scale[j.h] : 1.f;
-#pragma unroll 1
-  for (int r = blockIdx.y; r < j.rows; r += kJoinRows) {
-    float top = kNone;
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-      const float m = a.part_ml[slot(i) * NT + r].x;
-      top = m > top || m != m ? m : top;
-    }
-    top = warp_max(top);
-    if (lane == 0) red[warp][0] = top;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      const float m = red[w][0];
-      top = m > top || m != m ? m : top;
-    }
-    float sum = 0.f;
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-      const float2 ml = a.part_ml[slot(i) * NT + r];
-      const float w = exp2_fast(ml.x - top);
-      weight[i] = w;
-      sum += w * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[warp][1] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < kJoinThreads / 32; ++w) sum += red[w][1];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = group; i < parts; i += NP) {
-      const float4 p =
-          __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * NT + r) * D) + quad);
-      const float w = weight[i];
-      o.x += w * p.x, o.y += w * p.y, o.z += w * p.z, o.w += w * p.w;
-    }
-    *reinterpret_cast<float4*>(&acc[group][quad * 4]) = o;
-    __syncthreads();
-    const int row = j.row0 + r;
-    const int64_t at = j.item + (int64_t)(row / a.G) * a.Hq + row % a.G;
-    if (threadIdx.x < D) {
-      float x = 0.f;
-      for (int g = 0; g < NP; ++g) x += acc[g][threadIdx.x];
-      x *= sum != 0.f ? vsc / sum : 0.f;
-      static_cast<uint16_t*>(a.o)[at * D + threadIdx.x] =
-          a.bf16 ? Elem<GDN_BF16>::from(x) : Elem<GDN_F16>::from(x);
-      if (a.lse != nullptr && threadIdx.x == 0)
-        a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    }
-    __syncthreads();
+  const int r = ONE_ROW ? blockIdx.y : blockIdx.y * NP + group;
+  if (r >= j.rows) return;  // ONE_ROW: all of the block
+  const int parts = j.last - (int)blockIdx.x + 1;
+  auto at = [&](int i) {
+    return (i == 0 ? (int64_t)j.slot : 2 * ((int64_t)blockIdx.x + i)) * NT + r;
+  };
+  float top = kNone;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) {
+    const float m = a.part_ml[at(i)].x;
+    top = m > top || m != m ? m : top;
   }
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = ONE_ROW ? group : 0; i < parts; i += STEP) {
+    const float2 ml = a.part_ml[at(i)];
+    const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
+    const float w = exp2_fast(ml.x - top);
+    sum += w * ml.y;
+    o.x += w * p.x, o.y += w * p.y, o.z += w * p.z, o.w += w * p.w;
+  }
+  if constexpr (ONE_ROW) {
+    *reinterpret_cast<float4*>(&acc[group][quad * 4]) = o;
+    if (quad == 0) sums[group] = sum;
+    __syncthreads();
+    if (group != 0) return;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < NP; ++g) {
+      const float4 p = *reinterpret_cast<const float4*>(&acc[g][quad * 4]);
+      o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w;
+      sum += sums[g];
+    }
+  }
+  const int row = j.row0 + r;
+  const int64_t out = j.item + (int64_t)(row / a.G) * a.Hq + row % a.G;
+  const float inv =
+      sum != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[j.h] : 1.f) / sum : 0.f;
+  const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = a.bf16 ? Elem<GDN_BF16>::from(v[i]) : Elem<GDN_F16>::from(v[i]);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + out * D + quad * 4) =
+      make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+  if (a.lse != nullptr && quad == 0)
+    a.lse[out] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, int NT>
@@ -1290,10 +1285,14 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
     (void)cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  const int rc = launch_pdl(attn_kernel<D, NT>, dim3(parts), dim3(kAttnThreads), C::SMEM, s, a);
+  const int rc = launch_pdl(attn_kernel<D, NT>, dim3(parts), dim3(C::THREADS), C::SMEM, s, a);
   if (rc != GDN_OK) return rc;
-  return launch_pdl(join_kernel<D>, dim3(parts, min(NT, kJoinRows)), dim3(kJoinThreads), 0, s, a,
-                    NT);
+  const dim3 block(kJoinThreads);
+  if (NT == 16)
+    return launch_pdl(join_kernel<D, true>, dim3(parts, a.rows_per_tile), block, 0, s, a, NT);
+  constexpr int NP = kJoinThreads / (D / 4);
+  return launch_pdl(join_kernel<D, false>, dim3(parts, (a.rows_per_tile + NP - 1) / NP), block, 0,
+                    s, a, NT);
 }
 
 template <int D>
