@@ -648,8 +648,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   (void)attn_lens(a, sh.len, false);
   __syncthreads();
   if (warp == C::wI + 2 && kept) {
-    const Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
-    if (lane == 0) sh.run = run;
+    Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    const Seg first = attn_seg(a, lens, run);
+    if (lane == 0) sh.run = run, sh.seg[0] = first;
   }
   __syncthreads();
   pdl_enter();
@@ -1136,7 +1137,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     unsigned empty_ph = 1;
     for (;; ++seg_no) {
       if (is_k) {
-        s = attn_seg(a, lens, run);
+        const bool ready = seg_no == 0 && !again;  // since before the wait
+        s = ready ? sh.seg[0] : attn_seg(a, lens, run);
         const int i = seg_no & (kSegs - 1);
         attn_wait(&sh.seg_empty[i], ((seg_no / kSegs) & 1) ^ 1, dead);
         if (lane == 0) {
@@ -1223,7 +1225,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const __grid_constant__ AttnArgs a, int NT) {
   constexpr int Q = D / 4, NP = kJoinThreads / Q, STEP = ONE_ROW ? NP : 1;
   __shared__ __align__(16) float acc[ONE_ROW ? NP : 1][D];
-  __shared__ float sums[NP];
+  __shared__ float2 sums[NP];
   pdl_enter();
   const AttnJoin j = a.join[blockIdx.x];
   const int quad = threadIdx.x % Q, group = threadIdx.x / Q;
@@ -1233,34 +1235,54 @@ join_kernel(const __grid_constant__ AttnArgs a, int NT) {
   auto at = [&](int i) {
     return (i == 0 ? (int64_t)j.slot : 2 * ((int64_t)blockIdx.x + i)) * NT + r;
   };
-  float top = kNone;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float m = a.part_ml[at(i)].x;
-    top = m > top || m != m ? m : top;
-  }
+  // a running maximum, so that nothing is read twice and the reads overlap
+  float top = kNone, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int i = ONE_ROW ? group : 0; i < parts; i += STEP) {
-    const float2 ml = a.part_ml[at(i)];
-    const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
-    const float w = exp2_fast(ml.x - top);
-    sum += w * ml.y;
-    o.x += w * p.x, o.y += w * p.y, o.z += w * p.z, o.w += w * p.w;
+  auto larger = [](float p, float q) { return q > p || q != q ? q : p; };  // NaN stays
+  constexpr int U = 8;
+#pragma unroll 1
+  for (int i0 = ONE_ROW ? group : 0; i0 < parts; i0 += U * STEP) {
+    float2 ml[U];
+    float4 p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * STEP;
+      ml[u] = make_float2(kNone, 0.f);
+      p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < parts) {
+        ml[u] = a.part_ml[at(i)];
+        p[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
+      }
+    }
+    float m = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = larger(m, ml[u].x);
+    const float keep = exp2_fast(top - m);
+    top = m;
+    sum *= keep;
+    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = exp2_fast(ml[u].x - m);
+      sum += w * ml[u].y;
+      o.x += w * p[u].x, o.y += w * p[u].y, o.z += w * p[u].z, o.w += w * p[u].w;
+    }
   }
   if constexpr (ONE_ROW) {
     *reinterpret_cast<float4*>(&acc[group][quad * 4]) = o;
-    if (quad == 0) sums[group] = sum;
+    if (quad == 0) sums[group] = make_float2(top, sum);
     __syncthreads();
     if (group != 0) return;
+#pragma unroll
+    for (int g = 0; g < NP; ++g) top = larger(top, sums[g].x);
     o = make_float4(0.f, 0.f, 0.f, 0.f);
     sum = 0.f;
 #pragma unroll
     for (int g = 0; g < NP; ++g) {
       const float4 p = *reinterpret_cast<const float4*>(&acc[g][quad * 4]);
-      o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w;
-      sum += sums[g];
+      const float w = exp2_fast(sums[g].x - top);
+      o.x += w * p.x, o.y += w * p.y, o.z += w * p.z, o.w += w * p.w;
+      sum += w * sums[g].y;
     }
   }
   const int row = j.row0 + r;
