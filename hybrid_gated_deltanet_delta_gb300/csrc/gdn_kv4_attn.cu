@@ -61,7 +61,7 @@ int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64
   row_tiles(a.rows_total, &a.row_tiles, &a.rows_per_tile);
   a.bf16 = dtype == GDN_BF16;
   // the kernels count tiles in 32 bits
-  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128;
+  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128 + 8;
   if ((int64_t)a.row_tiles * c.B > INT32_MAX / c.Hkv ||
       (int64_t)a.row_tiles * c.B * c.Hkv > INT32_MAX / tiles)
     return GDN_ERR_UNSUPPORTED;
