@@ -98,10 +98,10 @@ struct Seg {
 
 // What a block's work is measured in: an item's tiles, and kLead more before them
 // for what an item costs beside its tiles (its queries, first references and
-// output: about 4.5 us against 0.9 us a tile for decoded tokens, 8 us against
-// 2 us at 96 rows).  Without the lead, blocks with many short items took
-// twice the others' time (48 sequences of 0 to 8192 tokens: 150 us, with it 84 us).
-constexpr int kLead = 4;
+// output).  Measured: without the lead 48 sequences of 0 to 8192 tokens took 150 us,
+// the blocks with many short ones twice the others' time; with 2, 4, 8 and 12 it is
+// 109, 85, 85 and 87 us, and eight verified chains of 16 take 78, 75, 71 and 72 us.
+constexpr int kLead = 8;
 
 // Equal runs of `total` units for at most `parts` blocks: the first `extra` runs
 // have one unit more.  (The host keeps the count below 2^31.)

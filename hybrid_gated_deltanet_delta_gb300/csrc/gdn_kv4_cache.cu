@@ -19,17 +19,53 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- append
 // Grid (records a block can touch, Hkv, B).  A thread quantises 16 channels of
-// one token: K codes are 8 contiguous bytes and go straight to the record; V
-// codes are staged one byte each in shared memory ([token][channel]) and then
-// packed by the thread that owns the channel, 16 bytes of 32 tokens, merged
-// with the record's old bytes where the block covers only part of it.
+// two neighbouring tokens, the two that share the bytes of V codes.  K codes are 8
+// contiguous bytes a token and go straight to the record; V codes are staged as
+// bytes ([token pair][channel]) in shared memory and gathered by the thread that
+// owns the channel, 16 bytes of 32 tokens, merged with the record's old bytes where
+// the block covers only part of it.  Bound by the reads of k and v: 8,192 tokens
+// of 4 heads of 256 channels (43 MB) were 30 us with a token a thread and a byte a
+// code in shared memory, and are 15 us this way.
+struct Codes {
+  uint32_t w[2];  // 16 codes
+  uint32_t scale;
+};
+
+// Quantises 16 values; `bad` is set by a NaN or an infinity.
+__device__ __forceinline__ Codes quantise(float (&x)[2][8], float inv, bool& bad) {
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float y = x[j >> 3][j & 7];
+    bad |= !(fabsf(y) <= 3.4028235e38f);
+    y *= inv;
+    y = y == y ? fminf(fmaxf(y, -2688.f), 2688.f) : 0.f;
+    a = fmaxf(a, fabsf(y));
+    x[j >> 3][j & 7] = y;
+  }
+  Codes c = {{0, 0}, to_e4m3(a * (1.0f / 6.0f))};
+  const float s = e4m3((uint8_t)c.scale);
+  const float r = s > 0.f ? 1.0f / s : 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2)
+    c.w[j >> 3] |= to_e2m1x2(x[j >> 3][j & 7] * r, x[j >> 3][(j & 7) + 1] * r) << (4 * (j & 7));
+  return c;
+}
+
+// 8 codes of two tokens (a word each) as 8 bytes, the first token in the low halves.
+__device__ __forceinline__ uint2 pair_bytes(uint32_t a, uint32_t b) {
+  const uint32_t even = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;   // channels 0, 2, 4, 6
+  const uint32_t odd = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);    // channels 1, 3, 5, 7
+  return make_uint2(__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362));
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads)
 append_kernel(gdn_kv4_cache c, const void* __restrict__ kin, const void* __restrict__ vin,
               int64_t ksb, int64_t ksn, int64_t vsb, int64_t vsn, int N) {
   constexpr int G = D / 16;  // scale groups
   using T = typename Elem<DT>::T;
-  __shared__ __align__(16) uint8_t code[kRec][D];
+  __shared__ __align__(16) uint8_t code[kRec / 2][D];
   pdl_enter();
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = seq_len(c, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
@@ -44,73 +80,88 @@ append_kernel(gdn_kv4_cache c, const void* __restrict__ kin, const void* __restr
   }
   const float inv_k = c.k_scale != nullptr ? 1.0f / c.k_scale[h] : 1.0f;
   const float inv_v = c.v_scale != nullptr ? 1.0f / c.v_scale[h] : 1.0f;
+  const int pair0 = lo >> 1, pairs = ((hi + 1) >> 1) - pair0;
   bool bad = false;
-  for (int i = threadIdx.x; i < 2 * (hi - lo) * G; i += kThreads) {
-    const bool is_v = i >= (hi - lo) * G;
-    const int u = is_v ? i - (hi - lo) * G : i;
-    const int slot = lo + u / G, g = u % G;
-    const int64_t n = t0 + slot - base;
-    const T* src = is_v ? static_cast<const T*>(vin) + b * vsb + n * vsn + (int64_t)h * D + g * 16
-                        : static_cast<const T*>(kin) + b * ksb + n * ksn + (int64_t)h * D + g * 16;
-    float x[2][8];
-    load8<DT>(src, x[0]);
-    load8<DT>(src + 8, x[1]);
-    const float inv = is_v ? inv_v : inv_k;
-    float a = 0.f;
+  for (int i = threadIdx.x; i < 2 * pairs * G; i += kThreads) {
+    const bool is_v = i >= pairs * G;
+    const int u = is_v ? i - pairs * G : i, pair = pair0 + u / G, g = u % G;
+    const T* src = is_v ? static_cast<const T*>(vin) + b * vsb : static_cast<const T*>(kin) + b * ksb;
+    const int64_t step = is_v ? vsn : ksn;
+    float x[2][2][8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float y = x[j >> 3][j & 7];
-      bad |= !(fabsf(y) <= 3.4028235e38f);
-      y *= inv;
-      y = y == y ? fminf(fmaxf(y, -2688.f), 2688.f) : 0.f;
-      a = fmaxf(a, fabsf(y));
-      x[j >> 3][j & 7] = y;
-    }
-    const uint32_t s8 = to_e4m3(a * (1.0f / 6.0f));
-    const float s = e4m3((uint8_t)s8);
-    const float r = s > 0.f ? 1.0f / s : 0.f;
-    uint32_t w[2] = {0, 0};
+    for (int t = 0; t < 2; ++t) {
+      const int slot = 2 * pair + t;
+      if (slot >= lo && slot < hi) {
+        const T* p = src + (int64_t)(t0 + slot - base) * step + (int64_t)h * D + g * 16;
+        load8<DT>(p, x[t][0]);
+        load8<DT>(p + 8, x[t][1]);
+      } else {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2)
-      w[j >> 3] |= to_e2m1x2(x[j >> 3][j & 7] * r, x[j >> 3][(j & 7) + 1] * r) << (4 * (j & 7));
-    if (is_v) {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // 4 codes -> 4 bytes
-        const uint32_t n4 = w[j >> 1] >> (16 * (j & 1));
-        o[j] = (n4 & 0xfu) | ((n4 & 0xf0u) << 4) | ((n4 & 0xf00u) << 8) | ((n4 & 0xf000u) << 12);
+        for (int j = 0; j < 16; ++j) x[t][j >> 3][j & 7] = 0.f;
       }
-      *reinterpret_cast<uint4*>(&code[slot][g * 16]) = make_uint4(o[0], o[1], o[2], o[3]);
-      rec[off_vs(D) + g * kRec + slot] = (uint8_t)s8;
-    } else {
-      *reinterpret_cast<uint2*>(rec + (g >> 1) * 512 + slot * 16 + (g & 1) * 8) =
-          make_uint2(w[0], w[1]);
-      rec[off_ks(D) + slot * G + g] = (uint8_t)s8;
+    }
+    Codes q[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      q[t] = quantise(x[t], is_v ? inv_v : inv_k, bad);
+      const int slot = 2 * pair + t;
+      if (slot < lo || slot >= hi) continue;
+      if (is_v) {
+        rec[off_vs(D) + g * kRec + slot] = (uint8_t)q[t].scale;
+      } else {
+        *reinterpret_cast<uint2*>(rec + (g >> 1) * 512 + slot * 16 + (g & 1) * 8) =
+            make_uint2(q[t].w[0], q[t].w[1]);
+        rec[off_ks(D) + slot * G + g] = (uint8_t)q[t].scale;
+      }
+    }
+    if (is_v) {
+      const uint2 first = pair_bytes(q[0].w[0], q[1].w[0]), second = pair_bytes(q[0].w[1], q[1].w[1]);
+      *reinterpret_cast<uint4*>(&code[pair][g * 16]) =
+          make_uint4(first.x, first.y, second.x, second.y);
     }
   }
   if (bad) report(c.status, GDN_ERR_NONFINITE);
   __syncthreads();
+  // nibbles of the block in each word of 8 tokens
+  uint32_t mine[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int from = min(max(lo - 8 * w, 0), 8), to = min(max(hi - 8 * w, 0), 8);
+    mine[w] = (uint32_t)(((1ull << (4 * to)) - 1) & ~((1ull << (4 * from)) - 1));
+  }
   for (int ch = threadIdx.x; ch < D; ch += kThreads) {
     uint4* at = reinterpret_cast<uint4*>(rec + off_v(D) + ch * 16);
-    uint32_t w[4] = {0, 0, 0, 0}, m[4] = {0, 0, 0, 0};
+    uint32_t w[4];
 #pragma unroll
-    for (int t = 0; t < kRec; ++t)
-      if (t >= lo && t < hi) {
-        w[t >> 3] |= (uint32_t)code[t][ch] << (4 * (t & 7));
-        m[t >> 3] |= 0xfu << (4 * (t & 7));
-      }
+    for (int k = 0; k < 4; ++k)
+      w[k] = (code[4 * k][ch] | (uint32_t)code[4 * k + 1][ch] << 8 |
+              (uint32_t)code[4 * k + 2][ch] << 16 | (uint32_t)code[4 * k + 3][ch] << 24) & mine[k];
     if (lo != 0 || hi != kRec) {
       const uint4 old = *at;
-      w[0] |= old.x & ~m[0], w[1] |= old.y & ~m[1], w[2] |= old.z & ~m[2], w[3] |= old.w & ~m[3];
+      w[0] |= old.x & ~mine[0], w[1] |= old.y & ~mine[1];
+      w[2] |= old.z & ~mine[2], w[3] |= old.w & ~mine[3];
     }
     *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 // ---------------------------------------------------------------- read back
-// Grid as append.  K: a thread takes 8 channels of a token (4 bytes); V: a
-// thread takes a channel (16 bytes, 32 tokens), so that a warp's stores of one
-// token are consecutive channels.
+// Grid as append.  K: a thread takes 8 channels of a token (4 bytes); V: 4
+// channels of 8 tokens (a word of each), so that either's stores are 16 bytes (or 8)
+// and a warp's are contiguous.  Bound by the stores: 67 MB of fp32 for 8,192
+// tokens of 4 heads of 256 channels, 35 us with a value a store, 17.5 us so.
+template <int DT>
+__device__ __forceinline__ void store4(void* p, const float (&x)[4]) {
+  if constexpr (DT == GDN_F32) {
+    st_f4(static_cast<float*>(p), x[0], x[1], x[2], x[3]);
+  } else {
+    using E = Elem<DT>;
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(E::from(x[0]) | (uint32_t)E::from(x[1]) << 16,
+                   E::from(x[2]) | (uint32_t)E::from(x[3]) << 16);
+  }
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads)
 read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, int N) {
@@ -146,14 +197,21 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
       s = e4m3(rec[off_ks(D) + slot * (D / 16) + (p >> 1)]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = E::from(e2m1((w >> (4 * j)) & 15u) * s * gk);
+    for (int half = 0; half < 2; ++half) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = e2m1((w >> (16 * half + 4 * j)) & 15u) * s * gk;
+      store4<DT>(out + 4 * half, x);
+    }
   }
-  for (int i = threadIdx.x; i < 4 * D; i += kThreads) {
-    const int ch = i % D, quarter = i / D;  // 8 tokens
-    uint32_t w = 0;
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    const int ch = i % (D / 4) * 4, quarter = i / (D / 4);  // 8 tokens
+    uint32_t w[4] = {0, 0, 0, 0};
     uint2 s8 = make_uint2(0, 0);
     if (rec != nullptr) {
-      w = *reinterpret_cast<const uint32_t*>(rec + off_v(D) + ch * 16 + quarter * 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = *reinterpret_cast<const uint32_t*>(rec + off_v(D) + (ch + k) * 16 + quarter * 4);
       s8 = *reinterpret_cast<const uint2*>(rec + off_vs(D) + (ch >> 4) * kRec + quarter * 8);
     }
 #pragma unroll
@@ -161,109 +219,166 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
       const int slot = quarter * 8 + j;
       if (slot < lo || slot >= hi) continue;
       const float s = e4m3((uint8_t)((j < 4 ? s8.x : s8.y) >> (8 * (j & 3))));
-      vo[(int64_t)(t0 + slot - base) * step + ch] = E::from(e2m1((w >> (4 * j)) & 15u) * s * gv);
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = e2m1((w[k] >> (4 * j)) & 15u) * s * gv;
+      store4<DT>(vo + (int64_t)(t0 + slot - base) * step + ch, x);
     }
   }
 }
 
 // ---------------------------------------------------------------- commit
-// Grid (Hkv, B, layers).  A block of up to 64 nodes lies in at most three
-// records.  K codes and scales are moved by word, each word position by one
-// thread along the path in order (a node's source is never an earlier node's
-// destination, since the i-th node of a path has index >= i); a V channel's
-// nibbles are moved by the thread that owns the channel, in a shared-memory copy
-// of its rows.
+// Grid (pieces of the (layer, head) pairs, B).  A block of up to 64 nodes lies in at
+// most three records.  The path is found once a block of threads, in shared memory;
+// then each warp moves K and the scales, or 128 channels of V, of one (layer, head)
+// pair at a time.  K codes and scales are moved by word, each word position by one lane, eight path nodes read
+// before they are written (a node's source is never an earlier node's destination,
+// since the i-th node of a path has index >= i).  A V channel's codes are gathered
+// nibble by nibble by the lane that owns the channel, from its rows in shared
+// memory; the places are the same for all channels, so a warp's lanes read one
+// word each of one row.  Bound by latency: few bytes have to move, but the rows of V
+// that hold them are read and written whole.  64 trees of 22 nodes, 8 heads of 128
+// channels, 16 layers: 38 us with a block a (layer, head) pair that walks the path
+// in global memory, 31 us with four layers to a block and the path in shared memory,
+// 26 us this way (one tree: 6.2, 9.0 and 4.9 us).
 constexpr int kMaxNodes = 64;
 constexpr int kWindow = 3;
+constexpr int kCommitWarps = kThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int N, const int32_t* parent,
+commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const int32_t* parent,
               const int32_t* accept, int32_t* len_out) {
-  __shared__ int path[kMaxNodes];
-  __shared__ int count;
-  __shared__ uint8_t* recs[kWindow];
-  __shared__ __align__(16) uint8_t vrow[D][kWindow * 16];
+  __shared__ int up[kMaxNodes], path[kMaxNodes];
+  __shared__ int count, bad_tree;
+  __shared__ uint8_t* recs[kWindow];  // of head 0, layer 0
+  __shared__ uint32_t rows[kCommitWarps][kWindow * 4][32];
   pdl_enter();
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool lead = blockIdx.x == 0;
+  if (parent != nullptr) {
+    if (threadIdx.x == 0) bad_tree = 0;
+    __syncthreads();
+    for (int n = threadIdx.x; n < N; n += kThreads) {
+      const int p = parent[(int64_t)b * N + n];
+      up[n] = p;
+      if (n == 0 ? p != -1 : p < 0 || p >= n) bad_tree = 1;
+    }
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
-    const bool lead = h == 0 && blockIdx.z == 0;
     const int len = seq_len(c, b, lead), a = accept[b];
     int err = GDN_OK, m = 0;
     if (a < 0 || a >= N) err = GDN_ERR_ACCEPT_RANGE;
     else if (len < N) err = GDN_ERR_ROW_RANGE;
     else if (parent == nullptr) m = a + 1;
-    else if (!tree_ok(parent + (int64_t)b * N, N)) err = GDN_ERR_BAD_TREE;
+    else if (bad_tree) err = GDN_ERR_BAD_TREE;
     if (err == GDN_OK && parent != nullptr) {
-      for (int n = a; n >= 0; n = parent[(int64_t)b * N + n]) ++m;
+      for (int n = a; n >= 0; n = up[n]) ++m;
       int i = m;
-      for (int n = a; n >= 0; n = parent[(int64_t)b * N + n]) path[--i] = n;
+      for (int n = a; n >= 0; n = up[n]) path[--i] = n;
     }
     if (lead) {
       if (err != GDN_OK) report(c.status, err);
       len_out[b] = err == GDN_OK ? len - N + m : c.kv_len[b];
     }
-    if (parent == nullptr) m = 0;  // a chain's path is where it is
-    while (m > 0 && path[m - 1] == m - 1) --m;  // only a prefix moves nothing: then m = 0
-    count = err == GDN_OK ? m : 0;
+    // a chain's path is where it is, and so is one of the nodes 0 .. m - 1
+    if (err != GDN_OK || parent == nullptr || path[m - 1] == m - 1) m = 0;
     for (int w = 0; w < kWindow; ++w) {
       const int pos = ((len - N) / kRec + w) * kRec;
       recs[w] = nullptr;
-      if (count > 0 && pos < len) {
-        recs[w] = record(c, b, h, pos);
+      if (m > 0 && pos < len) {
+        recs[w] = record(c, b, 0, pos);
         if (recs[w] == nullptr) {
           if (lead) report(c.status, GDN_ERR_PAGE_RANGE);
-          count = 0;
-        } else {
-          recs[w] += blockIdx.z * layer_stride;
+          m = 0;
         }
       }
     }
+    count = m;
   }
   __syncthreads();
   const int m = count;
   if (m == 0) return;
   const int off = (c.kv_len[b] - N) % kRec;
+  int first = 0;  // nodes before it stay
+  while (path[first] == first) ++first;
   constexpr int kw = D / 8, sw = D / 64;  // words of a token's K codes, K scales
-  for (int i = threadIdx.x; i < kw + sw + D / 16; i += kThreads) {
-    for (int e = 0; e < m; ++e) {
-      if (path[e] == e) continue;
-      const int from = off + path[e], to = off + e;
-      const uint8_t* s = recs[from / kRec];
-      uint8_t* d = recs[to / kRec];
-      const int fs = from % kRec, ts = to % kRec;
-      if (i < kw) {
-        *reinterpret_cast<uint32_t*>(d + (i >> 2) * 512 + ts * 16 + (i & 3) * 4) =
-            *reinterpret_cast<const uint32_t*>(s + (i >> 2) * 512 + fs * 16 + (i & 3) * 4);
-      } else if (i < kw + sw) {
-        const int j = (i - kw) * 4;
-        *reinterpret_cast<uint32_t*>(d + off_ks(D) + ts * (D / 16) + j) =
-            *reinterpret_cast<const uint32_t*>(s + off_ks(D) + fs * (D / 16) + j);
-      } else {
-        const int g = (i - kw - sw) * kRec;
-        d[off_vs(D) + g + ts] = s[off_vs(D) + g + fs];
+  const int rec0 = (off + first) / kRec, rec1 = (off + m - 1) / kRec;  // written
+  const int last = (off + path[m - 1]) / kRec;                         // read
+  const int64_t head_stride = (int64_t)(c.page_tokens / kRec) * rec_bytes(D);
+  // a warp's work: a (layer, head) pair's K and scales, or 128 channels of its V
+  constexpr int CH = D / 32 < 4 ? D / 32 : 4, PARTS = 1 + D / (32 * CH);
+  for (int i = blockIdx.x * kCommitWarps + warp; i < n_layers * c.Hkv * PARTS;
+       i += gridDim.x * kCommitWarps) {
+    const int part = i % PARTS, pair = i / PARTS;
+    const int64_t at0 = pair / c.Hkv * layer_stride + pair % c.Hkv * head_stride;
+    for (int j = part == 0 ? lane : D; j < kw + sw + D / 16; j += 32) {
+      // where this lane's word (or V scale) of a token is
+      const bool byte = j >= kw + sw;
+      const int64_t at = at0 + (j < kw ? (j >> 2) * 512 + (j & 3) * 4
+                                       : !byte ? off_ks(D) + (j - kw) * 4
+                                               : off_vs(D) + (j - kw - sw) * kRec);
+      const int step = j < kw ? 16 : !byte ? D / 16 : 1;
+      for (int e0 = first; e0 < m; e0 += 8) {
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (e0 + k >= m) break;
+          const int from = off + path[e0 + k];
+          const uint8_t* s = recs[from / kRec] + at + from % kRec * step;
+          x[k] = byte ? *s : *reinterpret_cast<const uint32_t*>(s);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (e0 + k >= m) break;
+          const int to = off + e0 + k;
+          uint8_t* d = recs[to / kRec] + at + to % kRec * step;
+          if (byte) *d = (uint8_t)x[k];
+          else *reinterpret_cast<uint32_t*>(d) = x[k];
+        }
       }
     }
-  }
-  for (int ch = threadIdx.x; ch < D; ch += kThreads) {
-    uint8_t* row = vrow[ch];
-    const int last = (off + path[m - 1]) / kRec;
+    if (part > 0) {
+      const int c0 = (part - 1) * 32 * CH + lane;
+      uint4 v[CH][kWindow];
 #pragma unroll
-    for (int w = 0; w < kWindow; ++w)
-      if (w <= last)
-        *reinterpret_cast<uint4*>(row + w * 16) =
-            *reinterpret_cast<const uint4*>(recs[w] + off_v(D) + ch * 16);
-    for (int e = 0; e < m; ++e) {
-      const int from = off + path[e], to = off + e;
-      const uint32_t x = (row[from >> 1] >> (4 * (from & 1))) & 15u;
-      const uint32_t keep = row[to >> 1] & (to & 1 ? 0x0fu : 0xf0u);
-      row[to >> 1] = (uint8_t)(keep | (x << (4 * (to & 1))));
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int w = 0; w < kWindow; ++w)
+          if (w >= rec0 && w <= last)
+            v[k][w] = *reinterpret_cast<const uint4*>(recs[w] + at0 + off_v(D) +
+                                                      (c0 + 32 * k) * 16);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        uint32_t(&row)[kWindow * 4][32] = rows[warp];
+#pragma unroll
+        for (int w = 0; w < kWindow; ++w)
+          if (w >= rec0 && w <= last) {
+            row[w * 4][lane] = v[k][w].x, row[w * 4 + 1][lane] = v[k][w].y;
+            row[w * 4 + 2][lane] = v[k][w].z, row[w * 4 + 3][lane] = v[k][w].w;
+          }
+        // words of 8 tokens, in order: a word's sources are at or after it
+        for (int w = (off + first) >> 3; w <= (off + m - 1) >> 3; ++w) {
+          uint32_t x = row[w][lane];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const int e = 8 * w + t - off;
+            if (e < first || e >= m) continue;
+            const int from = off + path[e];
+            const uint32_t code = row[from >> 3][lane] >> (4 * (from & 7)) & 15u;
+            x = (x & ~(15u << (4 * t))) | code << (4 * t);
+          }
+          row[w][lane] = x;
+        }
+#pragma unroll
+        for (int w = 0; w < kWindow; ++w)
+          if (w >= rec0 && w <= rec1)
+            *reinterpret_cast<uint4*>(recs[w] + at0 + off_v(D) + (c0 + 32 * k) * 16) =
+                make_uint4(row[w * 4][lane], row[w * 4 + 1][lane], row[w * 4 + 2][lane],
+                           row[w * 4 + 3][lane]);
+      }
     }
-#pragma unroll
-    for (int w = 0; w < kWindow; ++w)
-      if (w <= (off + m - 1) / kRec)
-        *reinterpret_cast<uint4*>(recs[w] + off_v(D) + ch * 16) =
-            *reinterpret_cast<const uint4*>(row + w * 16);
   }
 }
 
@@ -313,12 +428,18 @@ int launch_kv4_read(const gdn_kv4_cache& c, void* k, void* v, int dtype, int N, 
 int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers, int N,
                       const int32_t* parent, const int32_t* accept, int32_t* len_out,
                       cudaStream_t s) {
-  // a chain moves nothing: one block per sequence writes its length
-  const dim3 grid(parent != nullptr ? c.Hkv : 1, c.B, parent != nullptr ? n_layers : 1);
+  // A pair a warp while the blocks are few, up to four then (their path is found
+  // once); a chain moves nothing: one block per sequence writes its length.
+  const int64_t pairs = (int64_t)n_layers * c.Hkv * (c.D == 256 ? 3 : 2);
+  const int warps = pairs * c.B <= 8192 ? kCommitWarps : 4 * kCommitWarps;
+  const dim3 grid(parent != nullptr ? (unsigned)((pairs + warps - 1) / warps) : 1, c.B);
   switch (c.D) {
-    case 64: return launch_pdl(commit_kernel<64>, grid, dim3(kThreads), 0, s, c, layer_stride, N, parent, accept, len_out);
-    case 128: return launch_pdl(commit_kernel<128>, grid, dim3(kThreads), 0, s, c, layer_stride, N, parent, accept, len_out);
-    default: return launch_pdl(commit_kernel<256>, grid, dim3(kThreads), 0, s, c, layer_stride, N, parent, accept, len_out);
+    case 64: return launch_pdl(commit_kernel<64>, grid, dim3(kThreads), 0, s, c, layer_stride, n_layers, N,
+                                parent, accept, len_out);
+    case 128: return launch_pdl(commit_kernel<128>, grid, dim3(kThreads), 0, s, c, layer_stride, n_layers, N,
+                                parent, accept, len_out);
+    default: return launch_pdl(commit_kernel<256>, grid, dim3(kThreads), 0, s, c, layer_stride, n_layers, N,
+                                parent, accept, len_out);
   }
 }
 
