@@ -26,10 +26,8 @@
 //              sums in registers, the item's epilogue, and the next item's queries into
 //              the B operand (binary16, scaled by a power of two per row so that any
 //              bf16 magnitude fits)
-//   and a warp each that issues S^T's products, issues O^T's, copies the records' K
-//   halves (and cuts the run into segments), and copies their V halves.
-// Few rows leave the time to the 4-bit operand, many to the softmax, so up to 32
-// rows two groups each dequantise K and V, and 96 rows take three softmax groups.
+//   and a warp each that issues S^T's products, issues O^T's, and cuts the run into
+//   segments and copies the records (with few rows, a warp each for K and V halves).
 //
 // The reference m is moved only when some p would pass 2^8 (p is at most 65504
 // in binary16): the sums and O^T are then multiplied by 2^(old - new), which
@@ -63,7 +61,8 @@ struct AttnCfg {
   static constexpr int NS = NT < 64 ? 1 : NT / 32;  // softmax groups
   static constexpr int NH = NT / NS;                // rows of one
   static constexpr int wV = 4, wS = 8;  // first warps of the roles
-  static constexpr int wI = wS + 4 * NS, THREADS = 32 * (wI + 4);
+  static constexpr int wI = wS + 4 * NS, FW = NT < 64 ? 2 : 1;  // warps that copy: a tile of few rows is short
+  static constexpr int THREADS = 32 * (wI + 2 + FW);
   // TMEM columns: two K units (KW columns of 2 channels each), two S^T, O^T, two V units
   // (VW records each).  Large units cost fewer hand-overs; the widest case has no
   // room for them.
@@ -140,7 +139,7 @@ struct AttnShared {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int dead;
-  int k_ok[kTiles], v_ok[kTiles];  // records of a tile that could be read, by tile number
+  int tile_ok[2][kTiles];  // records of a tile that could be read, by tile number
   Seg seg[kSegs];
   // of the query rows: c (logit of S: c * S, log2 units), the row of
   // the output from the item's first node and head on, and for trees the
@@ -644,7 +643,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       mbar_init(&sh.p_full[i], 4 * C::NS), mbar_init(&sh.p_empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], C::wI + 3);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&sh.seg_full[i], 1), mbar_init(&sh.seg_empty[i], C::wI + 1 + C::FW);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.o_empty, 4 * C::NS);
     mbar_init(&sh.drain, 2);
@@ -675,7 +674,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   // the addresses below are column numbers known at compile time
   if (sh.tmem != 0) *dead = 1;
 
-  // every warp but 22 takes the run's segments from the ring
+  // every warp but the one that cuts them takes the run's segments from the ring
   int seg_no = 0;
   Seg s;
   auto next_seg = [&]() {
@@ -751,7 +750,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         // the tile's scales to binary16, 8 positions of a group a step; those past
         // the end, or on a page that is not there, count as 0
         uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
-        const int ok = sh.v_ok[tile & (kTiles - 1)], end = s.len - t * kTile;
+        const int ok = sh.tile_ok[1][tile & (kTiles - 1)], end = s.len - t * kTile;
         const bool full = ok == 15 && end >= kTile;
 #pragma unroll
         for (int i = vt; i < D; i += 128) {
@@ -844,7 +843,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
         tc::fence_after_sync();
-        const int ok = sh.k_ok[tile & (kTiles - 1)];
+        const int ok = sh.tile_ok[0][tile & (kTiles - 1)];
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
@@ -1132,24 +1131,21 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       }
     }
   } else {
-    // ------------------------------------------------ the records' K halves (and the
-    // run's segments), or their V halves
-    const bool is_k = warp == C::wI + 2;
+    // ------------------------------------------------ the run's segments, the records in
+    const bool lead = warp == C::wI + 2, do_k = C::FW == 1 || lead, do_v = C::FW == 1 || !lead;
     Run run = sh.run;
-    if (is_k && again) run = attn_run(a, lens, blockIdx.x, gridDim.x);
-    uint64_t* full = is_k ? sh.kr_full : sh.vr_full;
-    uint64_t* empty = is_k ? sh.kr_empty : sh.vr_empty;
-    int* oks = is_k ? sh.k_ok : sh.v_ok;
-    uint8_t* ring = smem + (is_k ? C::oK : C::oV);
-    const int stages = is_k ? C::KR : C::VR;
-    // lanes 2r and 2r + 1: codes and scales of record r
-    const int r = lane >> 1, part = lane & 1;
+    if (lead && again) run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    // lanes 2r and 2r + 1: codes and scales of record r's K half, lanes 8 + 2r and
+    // 9 + 2r: of its V half (the first eight lanes where a warp has V alone)
+    const int lanes = C::FW == 1 ? 16 : 8;
+    const bool is_k = C::FW == 1 ? lane < 8 : lead;
+    const int r = (lane & 7) >> 1, part = lane & 1;
     const int from = part == 0 ? (is_k ? 0 : off_v(D)) : (is_k ? off_ks(D) : off_vs(D));
     const int bytes = part == 0 ? 16 * D : 2 * D;
-    int stage = 0, tile = 0;
-    unsigned empty_ph = 1;
+    int k_stage = 0, v_stage = 0, tile = 0;
+    unsigned k_ph = 1, v_ph = 1;
     for (;; ++seg_no) {
-      if (is_k) {
+      if (lead) {
         const bool ready = seg_no == 0 && !again;  // since before the wait
         s = ready ? sh.seg[0] : attn_seg(a, lens, run);
         const int i = seg_no & (kSegs - 1);
@@ -1172,7 +1168,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       const int entries = kTile / a.c.page_tokens, rest = kTile % a.c.page_tokens;
       int page[3], offs[3];
       auto look_up = [&](int i, int t) {
-        page[i] = lane < 8 && t < s.t1 && t * kTile + r * kRec < s.len ? table[entry] : -1;
+        page[i] = lane < lanes && t < s.t1 && t * kTile + r * kRec < s.len ? table[entry] : -1;
         offs[i] = off;
         entry += entries;
         off += rest;
@@ -1182,7 +1178,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       look_up(1, s.t0 + 1);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        const bool want = lane < 8 && pos < s.len;  // past the end: nothing to read
+        const bool want = lane < lanes && pos < s.len;  // past the end: nothing to read
         look_up(2, t + 2);
         const bool have = want && page[0] >= 0 && page[0] < a.c.n_pages;
         if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
@@ -1192,22 +1188,39 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         pos += kTile;
         page[0] = page[1], offs[0] = offs[1], page[1] = page[2], offs[1] = offs[2];
         const unsigned good = __ballot_sync(0xffffffffu, have || !want);
-        const unsigned copies = __ballot_sync(0xffffffffu, have) & 0x55u;
-        attn_wait(&empty[stage], empty_ph, dead);
-        if (lane == 0) {
-          oks[tile & (kTiles - 1)] =
-              (good & 1) | ((good >> 1) & 2) | ((good >> 2) & 4) | ((good >> 3) & 8);
-          mbar_arrive_expect_tx(&full[stage], __popc(copies) * C::HALF);
+        const unsigned tx = __popc(__ballot_sync(0xffffffffu, have) & 0x55u) * C::HALF;
+        const int ok = (good & 1) | ((good >> 1) & 2) | ((good >> 2) & 4) | ((good >> 3) & 8);
+        if (do_k) {
+          attn_wait(&sh.kr_empty[k_stage], k_ph, dead);
+          if (lane == 0) {
+            sh.tile_ok[0][tile & (kTiles - 1)] = ok;
+            mbar_arrive_expect_tx(&sh.kr_full[k_stage], tx);
+          }
+          __syncwarp();
+          if (have && is_k)
+            bulk_g2s(smem + C::oK + k_stage * C::RAW + r * C::HALF + part * 16 * D, src, bytes,
+                     &sh.kr_full[k_stage]);
         }
-        __syncwarp();
-        if (have)
-          bulk_g2s(ring + stage * C::RAW + r * C::HALF + part * 16 * D, src, bytes, &full[stage]);
-        if (++stage == stages) stage = 0, empty_ph ^= 1;
+        if (do_v) {
+          attn_wait(&sh.vr_empty[v_stage], v_ph, dead);
+          if (lane == 0) {
+            sh.tile_ok[1][tile & (kTiles - 1)] = ok;
+            mbar_arrive_expect_tx(&sh.vr_full[v_stage], tx);
+          }
+          __syncwarp();
+          if (have && !is_k)
+            bulk_g2s(smem + C::oV + v_stage * C::RAW + r * C::HALF + part * 16 * D, src, bytes,
+                     &sh.vr_full[v_stage]);
+        }
+        if (++k_stage == C::KR) k_stage = 0, k_ph ^= 1;
+        if (++v_stage == C::VR) v_stage = 0, v_ph ^= 1;
       }
     }
     if (__any_sync(0xffffffffu, *dead)) {  // copies in flight land before the block ends
-      for (int i = 0; i < stages && i < tile; ++i)
-        (void)mbar_wait_bounded(&full[i], ((tile - i - 1) / stages) & 1, kWaitPolls);
+      for (int i = 0; do_k && i < C::KR && i < tile; ++i)
+        (void)mbar_wait_bounded(&sh.kr_full[i], ((tile - i - 1) / C::KR) & 1, kWaitPolls);
+      for (int i = 0; do_v && i < C::VR && i < tile; ++i)
+        (void)mbar_wait_bounded(&sh.vr_full[i], ((tile - i - 1) / C::VR) & 1, kWaitPolls);
     }
   }
   // every role is done with its loops, hence with its copies and products; after a
