@@ -582,3 +582,98 @@ def test_pool_refusals(gpu_lib):
         call()
         assert int(status.item()) == gpu_lib.GDN_ERR_ROW_RANGE
         assert all(t.equal(x, y) for x, y in zip((table, kv_len, count), before))
+
+
+# ------------------------------------------------------------------ streams and graphs
+def test_attention_in_a_graph_follows_the_lengths(gpu_lib):
+    """A captured append + attention replayed with other lengths equals fresh calls."""
+    rng, t = np.random.default_rng(40), torch()
+    s = Setup(rng, [300, 40, 700], 2, 128, 64, slack=40)
+    s.fill(rng)
+    kw = s.gpu()
+    q = t.from_numpy(rng.standard_normal((3, 4, 8, 128))).cuda().to(t.bfloat16)
+    k = t.from_numpy(rng.standard_normal((3, 4, 2, 128))).cuda().to(t.bfloat16)
+    o = t.empty_like(q)
+    ws = t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(3, 4, 8, 2, 128), dtype=t.uint8,
+                 device="cuda")
+
+    def step(out, stream=None):
+        gpu_lib.gdn_kv4_append(k, k, s.g_pages, s.g_table, s.g_len, stream=stream, **kw)
+        gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, out, ws, scale=0.09,
+                                  stream=stream, **kw)
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    step(o, side)
+    side.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g, stream=side):
+        step(o)
+    for lens in ([304, 44, 704], [308, 3, 0], [20, 48, 708]):   # written positions only
+        s.g_len.copy_(i32(lens))
+        t.cuda.synchronize()
+        o.fill_(9)
+        g.replay()
+        t.cuda.synchronize()
+        fresh = t.empty_like(q)
+        step(fresh)
+        assert t.equal(o, fresh)
+    assert int(s.status.item()) == 0
+
+
+def test_lengths_rewritten_on_the_stream_between_calls(gpu_lib):
+    """Calls issued back to back, each after a kernel that rewrites the lengths, each
+    follow theirs (the run of a block is worked out early, and again on a change)."""
+    rng, t = np.random.default_rng(41), torch()
+    s = Setup(rng, [3000, 2500], 2, 128, 64)
+    kw = s.gpu()
+    x = t.randn(2, 3000, 2, 128, device="cuda")
+    gpu_lib.gdn_kv4_append(x, x, s.g_pages, s.g_table, s.g_len, **kw)
+    q = t.randn(2, 1, 8, 128, device="cuda").to(t.bfloat16)
+    ws = t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(2, 1, 8, 2, 128), dtype=t.uint8,
+                 device="cuda")
+    plans = [i32([3000 - 311 * i, 1 + 350 * i]) for i in range(8)]
+    outs = [t.empty_like(q) for _ in plans]
+    t.cuda.synchronize()
+    for plan, o in zip(plans, outs):
+        s.g_len.copy_(plan)
+        gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.09, **kw)
+    t.cuda.synchronize()
+    for plan, o in zip(plans, outs):
+        s.g_len.copy_(plan)
+        t.cuda.synchronize()
+        alone = t.empty_like(q)
+        gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, alone, ws, scale=0.09, **kw)
+        t.cuda.synchronize()
+        assert t.equal(o, alone)
+    assert int(s.status.item()) == 0
+
+
+def test_more_sequences_than_are_kept(gpu_lib):
+    """Over a thousand sequences (lengths looked up instead of kept), some empty, with trees."""
+    rng, t = np.random.default_rng(42), torch()
+    B, N = 1100, 3
+    lens = [int(n) for n in rng.integers(0, 90, B)]
+    s = Setup(rng, lens, 1, 64, 32)
+    kw = s.gpu()
+    x = t.randn(B, 90, 1, 64, device="cuda")
+    gpu_lib.gdn_kv4_append(x, -x, s.g_pages, s.g_table, s.g_len, **kw)
+    q = t.randn(B, N, 2, 64, device="cuda").to(t.bfloat16)
+    parent = i32(np.tile([-1, 0, 0], (B, 1)))
+    ws = t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(B, N, 2, 1, 64), dtype=t.uint8,
+                 device="cuda")
+    o, one = t.full_like(q, 3), t.full_like(q, 3)
+    gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.1, parent=parent,
+                              **kw)
+    for b in range(0, B, 100):    # in pieces
+        n = min(100, B - b)
+        gpu_lib.gdn_kv4_attention(q[b:b + n], s.g_pages, s.g_table[b:b + n], s.g_len[b:b + n],
+                                  one[b:b + n], ws, scale=0.1, parent=parent[b:b + n], **kw)
+    assert int(s.status.item()) == 0
+    # other runs, other orders of the sums: equal up to the probabilities' rounding
+    assert bool(((o.float() - one.float()).abs() <= 2.0 ** -7 * one.float().abs() + 2.0 ** -8).all())
+    assert not o[[b for b in range(B) if lens[b] == 0]].any()
+    bad = parent.clone()
+    bad[1050, 1] = 7
+    gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.1, parent=bad, **kw)
+    assert int(s.status.item()) == (gpu_lib.GDN_ERR_BAD_TREE if lens[1050] else 0)
