@@ -49,7 +49,7 @@ namespace gdn {
 namespace kv4 {
 
 constexpr int kTile = 128;  // positions of a tile: four records
-constexpr float kNone = -1e30f;      // reference of a row that has seen nothing
+constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen nothing
 constexpr unsigned kMostP = 0x5c00;  // 2^8 in binary16: the largest p before m moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaitPolls = 1 << 20;  // bound of every wait
@@ -293,15 +293,6 @@ __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t* out) 
   out[1] = hmul2(e2m1x2<1>(w), s);
   out[2] = hmul2(e2m1x2<2>(w), s);
   out[3] = hmul2(e2m1x2<3>(w), s);
-}
-
-// Maximum over the warp (NaN wins over every number).
-__device__ __forceinline__ float warp_max(float x) {
-  int i = __float_as_int(x);
-  i ^= (i >> 31) & 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  i ^= (i >> 31) & 0x7fffffff;
-  return __int_as_float(i);
 }
 
 // ---------------------------------------------------------------- work

@@ -60,7 +60,7 @@ __device__ __forceinline__ uint2 pair_bytes(uint32_t a, uint32_t b) {
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 append_kernel(gdn_kv4_cache c, const void* __restrict__ kin, const void* __restrict__ vin,
               int64_t ksb, int64_t ksn, int64_t vsb, int64_t vsn, int N) {
   constexpr int G = D / 16;  // scale groups
@@ -187,17 +187,19 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
   if (rec == nullptr && threadIdx.x == 0) report(c.status, GDN_ERR_PAGE_RANGE);
   const float gk = c.k_scale != nullptr ? c.k_scale[h] : 1.0f;
   const float gv = c.v_scale != nullptr ? c.v_scale[h] : 1.0f;
-  for (int i = threadIdx.x; i < (hi - lo) * (D / 8); i += kThreads) {
-    const int slot = lo + i / (D / 8), p = i % (D / 8);
-    T* out = ko + (int64_t)(t0 + slot - base) * step + p * 8;
+  constexpr int CH = 16 / (int)sizeof(T), PER = D / CH;  // channels of a K thread
+  for (int i = threadIdx.x; i < (hi - lo) * PER; i += kThreads) {
+    const int slot = lo + i / PER, ch = i % PER * CH;
+    T* out = ko + (int64_t)(t0 + slot - base) * step + ch;
     uint32_t w = 0;
     float s = 0.f;
     if (rec != nullptr) {
-      w = *reinterpret_cast<const uint32_t*>(rec + (p >> 2) * 512 + slot * 16 + (p & 3) * 4);
-      s = e4m3(rec[off_ks(D) + slot * (D / 16) + (p >> 1)]);
+      const uint8_t* at = rec + (ch >> 5) * 512 + slot * 16 + ((ch & 31) >> 1);
+      w = CH == 4 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
+      s = e4m3(rec[off_ks(D) + slot * (D / 16) + (ch >> 4)]);
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < CH / 4; ++half) {
       float x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = e2m1((w >> (16 * half + 4 * j)) & 15u) * s * gk;
@@ -205,7 +207,7 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
     }
   }
   for (int i = threadIdx.x; i < D; i += kThreads) {
-    const int ch = i % (D / 4) * 4, quarter = i / (D / 4);  // 8 tokens
+    const int ch = i / 4 * 4, quarter = i % 4;  // 8 tokens
     uint32_t w[4] = {0, 0, 0, 0};
     uint2 s8 = make_uint2(0, 0);
     if (rec != nullptr) {
@@ -249,13 +251,15 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
 commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const int32_t* parent,
               const int32_t* accept, int32_t* len_out) {
-  __shared__ int up[kMaxNodes], path[kMaxNodes];
+  __shared__ int up[kMaxNodes], back[kMaxNodes];  // parents; the path from its end
   __shared__ int count, bad_tree;
   __shared__ uint8_t* recs[kWindow];  // of head 0, layer 0
   __shared__ uint32_t rows[kCommitWarps][kWindow * 4][32];
   pdl_enter();
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool lead = blockIdx.x == 0;
+  // what the path needs is read at once: length, node, parents, pages
+  const int len = seq_len(c, b, lead && threadIdx.x == 0), a = accept[b];
   if (parent != nullptr) {
     if (threadIdx.x == 0) bad_tree = 0;
     __syncthreads();
@@ -264,48 +268,44 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
       up[n] = p;
       if (n == 0 ? p != -1 : p < 0 || p >= n) bad_tree = 1;
     }
+    if (threadIdx.x >= kMaxNodes && threadIdx.x < kMaxNodes + kWindow && len >= N) {
+      const int w = threadIdx.x - kMaxNodes, pos = ((len - N) / kRec + w) * kRec;
+      recs[w] = pos < len ? record(c, b, 0, pos) : nullptr;
+    }
     __syncthreads();
   }
   if (threadIdx.x == 0) {
-    const int len = seq_len(c, b, lead), a = accept[b];
     int err = GDN_OK, m = 0;
     if (a < 0 || a >= N) err = GDN_ERR_ACCEPT_RANGE;
     else if (len < N) err = GDN_ERR_ROW_RANGE;
     else if (parent == nullptr) m = a + 1;
     else if (bad_tree) err = GDN_ERR_BAD_TREE;
-    if (err == GDN_OK && parent != nullptr) {
-      for (int n = a; n >= 0; n = up[n]) ++m;
-      int i = m;
-      for (int n = a; n >= 0; n = up[n]) path[--i] = n;
-    }
+    if (err == GDN_OK && parent != nullptr)
+      for (int n = a; n >= 0; n = up[n]) back[m++] = n;
     if (lead) {
       if (err != GDN_OK) report(c.status, err);
       len_out[b] = err == GDN_OK ? len - N + m : c.kv_len[b];
     }
     // a chain's path is where it is, and so is one of the nodes 0 .. m - 1
-    if (err != GDN_OK || parent == nullptr || path[m - 1] == m - 1) m = 0;
-    for (int w = 0; w < kWindow; ++w) {
-      const int pos = ((len - N) / kRec + w) * kRec;
-      recs[w] = nullptr;
-      if (m > 0 && pos < len) {
-        recs[w] = record(c, b, 0, pos);
-        if (recs[w] == nullptr) {
+    if (err != GDN_OK || parent == nullptr || a == m - 1) m = 0;
+    if (m > 0)
+      for (int w = 0; w < kWindow; ++w)
+        if (((len - N) / kRec + w) * kRec < len && recs[w] == nullptr) {
           if (lead) report(c.status, GDN_ERR_PAGE_RANGE);
           m = 0;
         }
-      }
-    }
     count = m;
   }
   __syncthreads();
   const int m = count;
   if (m == 0) return;
-  const int off = (c.kv_len[b] - N) % kRec;
+  auto path = [&](int i) { return back[m - 1 - i]; };
+  const int off = (len - N) % kRec;
   int first = 0;  // nodes before it stay
-  while (path[first] == first) ++first;
+  while (path(first) == first) ++first;
   constexpr int kw = D / 8, sw = D / 64;  // words of a token's K codes, K scales
   const int rec0 = (off + first) / kRec, rec1 = (off + m - 1) / kRec;  // written
-  const int last = (off + path[m - 1]) / kRec;                         // read
+  const int last = (off + path(m - 1)) / kRec;                         // read
   const int64_t head_stride = (int64_t)(c.page_tokens / kRec) * rec_bytes(D);
   // a warp's work: a (layer, head) pair's K and scales, or 128 channels of its V
   constexpr int CH = D / 32 < 4 ? D / 32 : 4, PARTS = 1 + D / (32 * CH);
@@ -325,7 +325,7 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (e0 + k >= m) break;
-          const int from = off + path[e0 + k];
+          const int from = off + path(e0 + k);
           const uint8_t* s = recs[from / kRec] + at + from % kRec * step;
           x[k] = byte ? *s : *reinterpret_cast<const uint32_t*>(s);
         }
@@ -365,7 +365,7 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
           for (int t = 0; t < 8; ++t) {
             const int e = 8 * w + t - off;
             if (e < first || e >= m) continue;
-            const int from = off + path[e];
+            const int from = off + path(e);
             const uint32_t code = row[from >> 3][lane] >> (4 * (from & 7)) & 15u;
             x = (x & ~(15u << (4 * t))) | code << (4 * t);
           }
@@ -428,11 +428,13 @@ int launch_kv4_read(const gdn_kv4_cache& c, void* k, void* v, int dtype, int N, 
 int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers, int N,
                       const int32_t* parent, const int32_t* accept, int32_t* len_out,
                       cudaStream_t s) {
-  // A pair a warp while the blocks are few, up to four then (their path is found
-  // once); a chain moves nothing: one block per sequence writes its length.
-  const int64_t pairs = (int64_t)n_layers * c.Hkv * (c.D == 256 ? 3 : 2);
-  const int warps = pairs * c.B <= 8192 ? kCommitWarps : 4 * kCommitWarps;
-  const dim3 grid(parent != nullptr ? (unsigned)((pairs + warps - 1) / warps) : 1, c.B);
+  // A unit of work a warp while the blocks are one wave, else one wave of blocks with
+  // more units each (their path is found once), up to eight; a chain moves nothing:
+  // one block per sequence writes its length.
+  const int64_t units = (int64_t)n_layers * c.Hkv * (c.D == 256 ? 3 : 2);
+  const int64_t wave = 152 * 3, most = (units + kCommitWarps - 1) / kCommitWarps;
+  const int64_t few = wave / c.B > (most + 7) / 8 ? wave / c.B : (most + 7) / 8;
+  const dim3 grid(parent == nullptr ? 1 : (unsigned)(most < few ? most : few), c.B);
   switch (c.D) {
     case 64: return launch_pdl(commit_kernel<64>, grid, dim3(kThreads), 0, s, c, layer_stride, n_layers, N,
                                 parent, accept, len_out);

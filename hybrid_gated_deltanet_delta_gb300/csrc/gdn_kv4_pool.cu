@@ -53,6 +53,10 @@ __global__ void __launch_bounds__(kThreads)
 fork_kernel(gdn_kv4_pool p, const int32_t* src, const int32_t* dst) {
   pdl_enter();
   const int from = src[blockIdx.x], to = dst[blockIdx.x];
+  // the first entries are read beside the lengths, not after them
+  int ahead = -1;
+  if (from >= 0 && from < p.n_rows && (int)threadIdx.x < p.max_pages)
+    ahead = p.table[(int64_t)from * p.table_stride + threadIdx.x];
   if (!row_ok(p, from) || !row_ok(p, to) || p.kv_len[to] != 0) {
     if (threadIdx.x == 0) report(p.status, GDN_ERR_ROW_RANGE);
     return;
@@ -61,7 +65,7 @@ fork_kernel(gdn_kv4_pool p, const int32_t* src, const int32_t* dst) {
   int32_t* d = p.table + (int64_t)to * p.table_stride;
   const int len = p.kv_len[from], held = pages_of(p, len);
   for (int j = threadIdx.x; j < p.max_pages; j += kThreads) {
-    const int page = j < held ? s[j] : -1;
+    const int page = j >= held ? -1 : j < kThreads ? ahead : s[j];
     if (j < held) {
       if (page_ok(p, page)) atomicAdd(p.ref + page, 1);
       else report(p.status, GDN_ERR_PAGE_RANGE);
@@ -73,14 +77,16 @@ fork_kernel(gdn_kv4_pool p, const int32_t* src, const int32_t* dst) {
 }
 
 // ---------------------------------------------------------------- reserve
-constexpr int kPlan = 1024;
+constexpr int kPlan = 512;
 
-// What the copy kernel does for a row: nothing when `records` is 0.
+// What the copy kernel does for a row: nothing when `records` is 0.  While the plan
+// is made: -1 for a row that is not served, and the row's first rank among the free
+// pages in `start`.
 struct Copy {
-  int from, to, records, start;  // start: the row's first rank among the free pages (plan only)
+  int from, to, records, start;
 };
 
-// Inclusive sums over the block (1024 threads); `total` is the block's.
+// Inclusive sums over the block (kPlan threads); `total` is the block's.
 __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -91,7 +97,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   __syncthreads();
   if (lane == 31) warp_sum[w] = x;
   __syncthreads();
-  int s = warp_sum[lane];
+  int s = lane < kPlan / 32 ? warp_sum[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, s, o);
@@ -105,6 +111,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
 struct Need {
   bool ok, copy;
   int row, old_len, new_len, lowest, want;  // entries lowest .. want-1 are new
+  int from;                                 // the shared last page, to be copied
 };
 
 __device__ __forceinline__ Need need_of(const gdn_kv4_pool& p, const int32_t* rows,
@@ -125,82 +132,157 @@ __device__ __forceinline__ Need need_of(const gdn_kv4_pool& p, const int32_t* ro
       n.ok = false;
     } else if (p.ref[tail] > 1) {
       n.copy = true;
+      n.from = tail;
       --n.lowest;
     }
   }
   return n;
 }
 
+// Which of the kScan pages from `at` on have no holder, by bits.
+constexpr int kScan = 8;
+
+struct Counts {
+  int4 x[2];
+};
+
+__device__ __forceinline__ Counts load_counts(const gdn_kv4_pool& p, int at) {
+  Counts c;
+  const bool vec = (reinterpret_cast<uintptr_t>(p.ref) & 15u) == 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i, at += 4) {
+    c.x[i] = make_int4(1, 1, 1, 1);
+    if (vec && at + 4 <= p.n_pages) {
+      c.x[i] = *reinterpret_cast<const int4*>(p.ref + at);
+    } else if (at < p.n_pages) {
+      c.x[i].x = p.ref[at];
+      if (at + 1 < p.n_pages) c.x[i].y = p.ref[at + 1];
+      if (at + 2 < p.n_pages) c.x[i].z = p.ref[at + 2];
+      if (at + 3 < p.n_pages) c.x[i].w = p.ref[at + 3];
+    }
+  }
+  return c;
+}
+
+__device__ __forceinline__ unsigned free_bits(const Counts& c) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    m |= ((c.x[i].x == 0) | (c.x[i].y == 0) << 1 | (c.x[i].z == 0) << 2 | (c.x[i].w == 0) << 3)
+         << (4 * i);
+  return m;
+}
+
+struct PlanRow {
+  int start, row, lowest, served;
+};
+
 // One block: the rows' needs in order, the number of free pages, which rows
-// are served, and then the pages themselves.
-__global__ void __launch_bounds__(kPlan)
+// are served, and then the pages themselves.  Bound by latency: the rows' chain of
+// dependent reads (row, length, tail page, its holders) runs under the read of the
+// counts, 8 consecutive pages a thread, so that a pool of 4096 pages takes one read
+// and one scan; the free pages then go to shared memory by rank and a thread serves
+// one rank, with what it needs of the row in shared memory as well.
+__global__ void __launch_bounds__(kPlan, 1)
 plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, Copy* plan) {
   __shared__ int warp_sum[32];
+  __shared__ PlanRow kept[kPlan];              // of the first kPlan rows
+  __shared__ uint16_t by_rank[kPlan * kScan];  // free pages of a chunk
   pdl_enter();
   const int tid = threadIdx.x;
+  constexpr int kChunk = kPlan * kScan;
+  Counts counts = load_counts(p, tid * kScan);
+  // needs, by the counts before the call; the first kPlan rows stay in registers and
+  // shared memory (row tid: `own`), the others in the plan
+  auto look = [&](int f) {
+    const Need n = need_of(p, rows, new_len, f);
+    if (!n.ok) report(p.status, GDN_ERR_ROW_RANGE);
+    return n;
+  };
+  auto records = [&](const Need& n) {
+    return !n.ok ? -1 : n.copy ? (n.old_len % p.page_tokens + kv4::kRec - 1) / kv4::kRec : 0;
+  };
   int asked = 0, have = 0, total;
-  // needs, by the counts before the call
+  Need own = {};
   for (int f0 = 0; f0 < F; f0 += kPlan) {
     const int f = f0 + tid;
     Need n = {};
-    if (f < F) {
-      n = need_of(p, rows, new_len, f);
-      if (!n.ok) report(p.status, GDN_ERR_ROW_RANGE);
-    }
+    if (f < F) n = look(f);
     const int mine = n.ok ? n.want - n.lowest : 0;
-    const int upto = block_scan(mine, warp_sum, total);
-    if (f < F) {
-      Copy c = {-1, -1, 0, asked + upto - mine};
-      if (n.copy) {
-        c.from = p.table[(int64_t)n.row * p.table_stride + n.lowest];
-        c.records = (n.old_len % p.page_tokens + kv4::kRec - 1) / kv4::kRec;
-      }
-      if (!n.ok) c.to = -2;  // not served
-      plan[f] = c;
+    const int at = asked + block_scan(mine, warp_sum, total) - mine;
+    if (f0 == 0) {
+      own = n;
+      kept[tid] = {at, n.row, n.lowest, n.ok};
+    } else if (f < F) {
+      plan[f] = {n.from, -1, records(n), at};
     }
     asked += total;
   }
-  for (int i0 = 0; i0 < p.n_pages; i0 += kPlan) {
-    const int i = i0 + tid;
-    have += __syncthreads_count(i < p.n_pages && p.ref[i] == 0);
+  auto start = [&](int f) { return f < kPlan ? kept[f].start : plan[f].start; };
+  // this thread's free pages and their first rank, of the last chunk of pages
+  unsigned mine = 0;
+  int rank = 0;
+  for (int i0 = 0; i0 < p.n_pages; i0 += kChunk) {
+    if (i0 > 0) counts = load_counts(p, i0 + tid * kScan);
+    mine = free_bits(counts);
+    rank = block_scan(__popc(mine), warp_sum, total) - __popc(mine);
+    have += total;
   }
   // rows that do not fit: they and all later ones that need pages
+  __syncthreads();
   for (int f = tid; f < F; f += kPlan) {
-    if (plan[f].to == -2) continue;
-    const int end = f + 1 < F ? plan[f + 1].start : asked;
-    if (end > plan[f].start && end > have) {
-      plan[f].to = -2;
+    if (f < kPlan ? !own.ok : plan[f].records < 0) continue;
+    const int end = f + 1 < F ? start(f + 1) : asked;
+    if (end > start(f) && end > have) {
+      if (f < kPlan) own.ok = false, kept[f].served = 0;
+      else plan[f].records = -1;
       report(p.status, GDN_ERR_POOL_EMPTY);
     }
   }
-  __syncthreads();
   // hand out the free pages by rank
   int rank0 = 0;
-  for (int i0 = 0; i0 < p.n_pages && rank0 < asked; i0 += kPlan) {
-    const int i = i0 + tid;
-    const int is_free = i < p.n_pages && p.ref[i] == 0;
-    const int rank = rank0 + block_scan(is_free, warp_sum, total) - 1;
-    if (is_free && rank < asked) {
-      int lo = 0, hi = F - 1;  // the last row whose first rank is <= rank
+  for (int i0 = 0; i0 < p.n_pages && rank0 < asked; i0 += kChunk) {
+    total = have;
+    if (p.n_pages > kChunk) {
+      mine = free_bits(load_counts(p, i0 + tid * kScan));
+      rank = block_scan(__popc(mine), warp_sum, total) - __popc(mine);
+    }
+    for (; mine != 0; mine &= mine - 1) by_rank[rank++] = (uint16_t)(tid * kScan + __ffs(mine) - 1);
+    __syncthreads();
+    for (int k = tid; k < total && rank0 + k < asked; k += kPlan) {
+      int lo = 0, hi = F - 1;  // the last row whose first rank is <= this one
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (plan[mid].start <= rank) lo = mid;
+        if (start(mid) <= rank0 + k) lo = mid;
         else hi = mid - 1;
       }
-      const Copy c = plan[lo];
-      if (c.to != -2) {
-        const int row = rows[lo];
-        const int lowest = pages_of(p, p.kv_len[row]) - (c.records > 0);
-        p.table[(int64_t)row * p.table_stride + lowest + rank - c.start] = i;
-        if (c.records > 0 && rank == c.start) plan[lo].to = i;
+      PlanRow r;
+      if (lo < kPlan) {
+        r = kept[lo];
+      } else {
+        const int row = rows[lo], recs = plan[lo].records;
+        r = {plan[lo].start, row, pages_of(p, p.kv_len[row]) - (recs > 0), recs >= 0};
+      }
+      if (r.served) {
+        const int i = i0 + by_rank[k];
+        p.table[(int64_t)r.row * p.table_stride + r.lowest + rank0 + k - r.start] = i;
+        if (rank0 + k == r.start) plan[lo].to = i;  // of use when there is a tail to copy
         p.ref[i] = 1;
       }
     }
     rank0 += total;
+    __syncthreads();
   }
-  __syncthreads();
   for (int f = tid; f < F; f += kPlan) {
-    if (plan[f].to == -2) {
+    if (f < kPlan) {
+      const int recs = records(own);
+      plan[f].from = own.from;
+      plan[f].records = recs < 0 ? 0 : recs;
+      if (recs > 0) atomicSub(p.ref + own.from, 1);
+      if (recs >= 0) p.kv_len[own.row] = own.new_len;
+      continue;
+    }
+    if (plan[f].records < 0) {
       plan[f].records = 0;
       continue;
     }

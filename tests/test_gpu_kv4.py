@@ -677,3 +677,65 @@ def test_more_sequences_than_are_kept(gpu_lib):
     bad[1050, 1] = 7
     gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.1, parent=bad, **kw)
     assert int(s.status.item()) == (gpu_lib.GDN_ERR_BAD_TREE if lens[1050] else 0)
+
+
+def test_parents_rewritten_on_the_stream_between_calls(gpu_lib):
+    """The same for the trees: a malformed one between two good ones, back to back."""
+    rng, t = np.random.default_rng(43), torch()
+    s = Setup(rng, [900, 700], 2, 128, 64)
+    kw = s.gpu()
+    x = t.randn(2, 900, 2, 128, device="cuda")
+    gpu_lib.gdn_kv4_append(x, x, s.g_pages, s.g_table, s.g_len, **kw)
+    N = 22
+    q = t.randn(2, N, 4, 128, device="cuda").to(t.bfloat16)
+    ws = t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(2, N, 4, 2, 128), dtype=t.uint8,
+                 device="cuda")
+    plans = [i32(rand_trees(rng, 2, N)) for _ in range(6)]
+    plans[2][1, 5] = 9
+    outs, parent = [t.empty_like(q) for _ in plans], plans[-1].clone()
+    t.cuda.synchronize()
+    for plan, o in zip(plans, outs):
+        parent.copy_(plan)
+        gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.09,
+                                  parent=parent, **kw)
+    t.cuda.synchronize()
+    assert int(s.status.item()) == gpu_lib.GDN_ERR_BAD_TREE
+    for plan, o in zip(plans, outs):
+        alone = t.empty_like(q)
+        t.cuda.synchronize()
+        gpu_lib.gdn_kv4_attention(q, s.g_pages, s.g_table, s.g_len, alone, ws, scale=0.09,
+                                  parent=plan, **kw)
+        t.cuda.synchronize()
+        assert t.equal(o, alone)
+    assert not outs[2][1].any() and outs[2][0].any()
+
+
+@pytest.mark.parametrize("n_pages, F, offset, short", [
+    (4095, 1, 0, False), (4096, 40, 1, False), (8193, 40, 0, True), (20011, 1300, 3, False),
+    (20011, 1300, 0, True), (7, 2, 1, False), (3100, 1024, 0, True)])
+def test_reserve_of_large_pools(gpu_lib, n_pages, F, offset, short):
+    """Pools over several reads of the counts, counts at any 4-byte address, more rows
+    than one pass takes, too few pages: as the plain pool."""
+    rng, t = np.random.default_rng(n_pages + F + offset), torch()
+    P, width = 32, 3
+    table, kv_len = np.full((F, width), -1, np.int64), np.zeros(F, np.int64)
+    want = rng.integers(1, width * P + 1, F)
+    need = int((-(-want // P)).sum())
+    held = rng.permutation(n_pages)[:n_pages - (need - 2 if short else min(n_pages, need + 1))]
+    count = np.zeros(n_pages, np.int64)
+    count[held] = rng.integers(1, 4, len(held))
+    room = t.zeros(n_pages + offset, dtype=t.int32, device="cuda")
+    room[offset:] = i32(count)
+    g = (i32(table), i32(kv_len), room[offset:])
+    pages = t.zeros(n_pages, 1, 1, 36 * 64, dtype=t.uint8, device="cuda")
+    status = status_word()
+    ws = t.empty(gpu_lib.gdn_kv4_reserve_workspace_bytes(F), dtype=t.uint8, device="cuda")
+    order = [int(r) for r in rng.permutation(F)]
+    new = [int(want[r]) for r in order]
+    pool = ref.Pool(table, kv_len, count, P)
+    failed = pool.reserve(order, new)
+    gpu_lib.gdn_kv4_reserve(pages, *g, i32(order), i32(new), ws, status=status)
+    for got, exp in zip(g, (table, kv_len, count)):
+        assert np.array_equal(got.cpu().numpy(), exp)
+    assert bool(failed) == short
+    assert int(status.item()) == (gpu_lib.GDN_ERR_POOL_EMPTY if short else 0)
