@@ -23,25 +23,45 @@ constexpr int kThreads = 256;
 // contiguous bytes a token and go straight to the record; V codes are staged as
 // bytes ([token pair][channel]) in shared memory and gathered by the thread that
 // owns the channel, 16 bytes of 32 tokens, merged with the record's old bytes where
-// the block covers only part of it.  Bound by the reads of k and v: 8,192 tokens
-// of 4 heads of 256 channels (43 MB) were 30 us with a token a thread and a byte a
-// code in shared memory, and are 15 us this way.
+// the block covers only part of it.  Bound by the instructions on each value and
+// the latency of a block's length, page and values: 8,192 tokens of 4 heads of 256
+// channels (43 MB) were 30 us with a token a thread and a byte a code in shared
+// memory, 17.7 us with every value clamped and checked by itself, and are 14.8 us
+// this way.  Four blocks an SM (64 registers): with three 18.0 us, with five 16.9.
+// Whole 32-byte sectors a store, by exchanges between lanes, gave 14.7 us and were
+// left out.
 struct Codes {
   uint32_t w[2];  // 16 codes
   uint32_t scale;
 };
 
-// Quantises 16 values; `bad` is set by a NaN or an infinity.
+// The larger of a and |x|; NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float x) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(x)));
+  return d;
+}
+
+// Quantises 16 values; `bad` is set by a NaN or an infinity.  The product with
+// `inv` is monotone, so the largest |x| gives the largest |y|, and only where that
+// passes the bound (or is no number) are the values looked at one by one.
 __device__ __forceinline__ Codes quantise(float (&x)[2][8], float inv, bool& bad) {
   float a = 0.f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float y = x[j >> 3][j & 7];
-    bad |= !(fabsf(y) <= 3.4028235e38f);
-    y *= inv;
-    y = y == y ? fminf(fmaxf(y, -2688.f), 2688.f) : 0.f;
-    a = fmaxf(a, fabsf(y));
-    x[j >> 3][j & 7] = y;
+  for (int j = 0; j < 16; ++j) a = max_abs(a, x[j >> 3][j & 7]);
+  bad |= !(a <= 3.4028235e38f);
+  a *= fabsf(inv);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) x[j >> 3][j & 7] *= inv;
+  if (!(a <= 2688.f)) {
+    a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float y = x[j >> 3][j & 7];
+      y = y == y ? fminf(fmaxf(y, -2688.f), 2688.f) : 0.f;
+      a = fmaxf(a, fabsf(y));
+      x[j >> 3][j & 7] = y;
+    }
   }
   Codes c = {{0, 0}, to_e4m3(a * (1.0f / 6.0f))};
   const float s = e4m3((uint8_t)c.scale);
@@ -146,10 +166,12 @@ append_kernel(gdn_kv4_cache c, const void* __restrict__ kin, const void* __restr
 }
 
 // ---------------------------------------------------------------- read back
-// Grid as append.  K: a thread takes 8 channels of a token (4 bytes); V: 4
-// channels of 8 tokens (a word of each), so that either's stores are 16 bytes (or 8)
-// and a warp's are contiguous.  Bound by the stores: 67 MB of fp32 for 8,192
-// tokens of 4 heads of 256 channels, 35 us with a value a store, 17.5 us so.
+// Grid as append.  K: a thread takes 16 bytes of output of a token, four tokens'
+// codes in flight; V: 4 channels of 8 tokens (a word of each), four lanes beside
+// each other the same channels, so that a warp's reads and stores are whole sectors.
+// Bound by the stores: 67 MB of fp32 for 8,192 tokens of 4 heads of 256 channels,
+// 35 us with a value a store, 16.4 us so; 16 tokens of 8 sequences 3.6 us with one
+// token's codes in flight, 3.0 us with four.
 template <int DT>
 __device__ __forceinline__ void store4(void* p, const float (&x)[4]) {
   if constexpr (DT == GDN_F32) {
@@ -188,22 +210,34 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
   const float gk = c.k_scale != nullptr ? c.k_scale[h] : 1.0f;
   const float gv = c.v_scale != nullptr ? c.v_scale[h] : 1.0f;
   constexpr int CH = 16 / (int)sizeof(T), PER = D / CH;  // channels of a K thread
-  for (int i = threadIdx.x; i < (hi - lo) * PER; i += kThreads) {
-    const int slot = lo + i / PER, ch = i % PER * CH;
-    T* out = ko + (int64_t)(t0 + slot - base) * step + ch;
-    uint32_t w = 0;
-    float s = 0.f;
-    if (rec != nullptr) {
-      const uint8_t* at = rec + (ch >> 5) * 512 + slot * 16 + ((ch & 31) >> 1);
-      w = CH == 4 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
-      s = e4m3(rec[off_ks(D) + slot * (D / 16) + (ch >> 4)]);
+  constexpr int U = 4;  // loads in flight before their stores
+  for (int i0 = threadIdx.x; i0 < (hi - lo) * PER; i0 += U * kThreads) {
+    uint32_t w[U];
+    uint8_t s8[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads, slot = lo + i / PER, ch = i % PER * CH;
+      w[u] = 0, s8[u] = 0;
+      if (rec != nullptr && i < (hi - lo) * PER) {
+        const uint8_t* at = rec + (ch >> 5) * 512 + slot * 16 + ((ch & 31) >> 1);
+        w[u] = CH == 4 ? *reinterpret_cast<const uint16_t*>(at)
+                       : *reinterpret_cast<const uint32_t*>(at);
+        s8[u] = rec[off_ks(D) + slot * (D / 16) + (ch >> 4)];
+      }
     }
 #pragma unroll
-    for (int half = 0; half < CH / 4; ++half) {
-      float x[4];
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads, slot = lo + i / PER, ch = i % PER * CH;
+      if (i >= (hi - lo) * PER) break;
+      const float s = e4m3(s8[u]);
+      T* out = ko + (int64_t)(t0 + slot - base) * step + ch;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = e2m1((w >> (16 * half + 4 * j)) & 15u) * s * gk;
-      store4<DT>(out + 4 * half, x);
+      for (int half = 0; half < CH / 4; ++half) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = e2m1((w[u] >> (16 * half + 4 * j)) & 15u) * s * gk;
+        store4<DT>(out + 4 * half, x);
+      }
     }
   }
   for (int i = threadIdx.x; i < D; i += kThreads) {
@@ -242,7 +276,8 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
 // that hold them are read and written whole.  64 trees of 22 nodes, 8 heads of 128
 // channels, 16 layers: 38 us with a block a (layer, head) pair that walks the path
 // in global memory, 31 us with four layers to a block and the path in shared memory,
-// 26 us this way (one tree: 6.2, 9.0 and 4.9 us).
+// 26 us with blocks that do not all fit at once, 23.7 us this way (one tree: 6.2, 9.0,
+// 4.9 and 4.6 us).  Four blocks an SM spill: 27 us.
 constexpr int kMaxNodes = 64;
 constexpr int kWindow = 3;
 constexpr int kCommitWarps = kThreads / 32;
