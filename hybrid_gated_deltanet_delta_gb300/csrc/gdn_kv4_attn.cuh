@@ -60,6 +60,7 @@ struct AttnCfg {
   static constexpr int MB = D == 256 ? 2 : 1;  // 128-channel blocks of O^T
   static constexpr int NS = NT < 64 ? 1 : NT / 32;  // softmax groups
   static constexpr int NH = NT / NS;                // rows of one
+  static constexpr int ROWS = NT / (4 * NS);        // query rows that a softmax warp brings in
   static constexpr int wV = 4, wS = 8;  // first warps of the roles
   static constexpr int wI = wS + 4 * NS, FW = NT < 64 ? 2 : 1;  // warps that copy: a tile of few rows is short
   static constexpr int THREADS = 32 * (wI + 2 + FW);
@@ -152,6 +153,9 @@ struct AttnShared {
   alignas(16) float alpha[C::NT], inv[C::NT];
   float part[4][C::NT];             // of a softmax group's four warps
   Run run;
+  // for the functions that are not inlined: a reference to the kernel's parameters
+  // themselves is read through global memory
+  AttnArgs args;
   int len[kLens];
 };
 
@@ -489,47 +493,74 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& len
 }
 
 // ---------------------------------------------------------------- queries
-// Query rows of segment s into the B operand at q, four rows at a time: quads
-// `first`, first + step, ... of a warp.  The rows are copied as they are to where
-// the operand goes (the copies are this thread's cp.async, not waited for).
+// The query rows of a segment go to the B operand at q, ROWS neighbouring rows a
+// softmax warp.  They are copied as they are to where the operand goes (the copies
+// are this thread's cp.async, not waited for); a lane works out one row's place.
 template <int D, int NT>
 static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, const Seg& s, uint8_t* q,
-                                                   int first, int step) {
-  constexpr int E = D / 32;  // channels of a lane
-  const int ch = (threadIdx.x & 31) * E;
+                                                   int warp) {
+  constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;  // channels of a lane
+  const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
+  const int row = s.row0 + r0 + lane % ROWS, n = row / a.G;
+  const int64_t mine = s.b * a.q_stride_b + n * a.q_stride_n +
+                       (int64_t)(s.h * a.G + row - n * a.G) * D;
+  const int rows = s.rows;
+  const uint16_t* src = static_cast<const uint16_t*>(a.q) + ch;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
-  const uint16_t* src0 =
-      static_cast<const uint16_t*>(a.q) + s.b * a.q_stride_b + (int64_t)s.h * a.G * D + ch;
-#pragma unroll 1
-  for (int r0 = first * 4; r0 < NT; r0 += step * 4) {
-    int n = (s.row0 + r0) / a.G, g = (s.row0 + r0) % a.G;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + j;
-      uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
-      if (r < s.rows) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)),
-                     "l"(src0 + n * a.q_stride_n + (int64_t)g * D), "n"(E * 2)
-                     : "memory");
-      } else {
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + i;
+    uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
+    const int64_t from = __shfl_sync(0xffffffffu, mine, i);
+    if (r < rows) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_addr(at)),
+                   "l"(src + from), "n"(E * 2)
+                   : "memory");
+    } else {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) reinterpret_cast<uint32_t*>(at)[i] = 0;
-      }
-      if (++g == a.G) g = 0, ++n;
+      for (int k = 0; k < E / 2; ++k) reinterpret_cast<uint32_t*>(at)[k] = 0;
     }
   }
 }
 
+// One lane's channels of a row in the B operand: 4, 8 or 16 bytes.
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&x)[W]) {
+  if constexpr (W == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  } else {
+    x[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&x)[W]) {
+  if constexpr (W == 4) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+  } else if constexpr (W == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(x[0], x[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = x[0];
+  }
+}
+
 // Then each lane turns its own channels into binary16 in place, and what goes
-// with the rows is written.
+// with the rows is written, a lane a row.
 template <int D, int NT>
 static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
-                                              const Seg& s, uint8_t* q, int first, int step) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, ch = lane * E;
+                                              const Seg& s, uint8_t* q, int warp,
+                                              float to_log2) {
+  const int row0 = s.row0, rows = s.rows, G = a.G, Hq = a.Hq;
+  const bool bf16 = a.bf16, tree = a.parent != nullptr;
+  constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;
+  const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
   auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
-  if (a.parent != nullptr) {
+  if (tree) {
     // path of every node: pointers double their reach in each step
     const int32_t* p = a.parent + (int64_t)s.b * a.N;
     int to[2];
@@ -562,17 +593,16 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
       sh.path[lane + 32 * i] = make_uint2((unsigned)path[i], (unsigned)(path[i] >> 32));
     __syncwarp();
   }
-  const float to_log2 = a.scale * ((a.c.k_scale != nullptr ? a.c.k_scale[s.h] : 1.f) * kLog2e);
+  const int row = row0 + min(r0 + lane % ROWS, rows - 1), n = row / G;
   cp_async_wait_all();
-#pragma unroll 1
-  for (int r0 = first * 4; r0 < NT; r0 += step * 4) {
+  float back = 1.f;
+#pragma unroll
+  for (int i0 = 0; i0 < ROWS; i0 += 4) {
     // four rows at a time, for their latencies to overlap
     uint32_t x[4][E / 2];
     unsigned big[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) x[j][i] = reinterpret_cast<uint32_t*>(place(r0 + j))[i];
+    for (int j = 0; j < 4; ++j) load_words<E / 2>(place(r0 + i0 + j), x[j]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -580,33 +610,33 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
         big[j] = max(big[j], max(x[j][i] & 0x7fffu, (x[j][i] >> 16) & 0x7fffu));
       big[j] = __reduce_max_sync(0xffffffffu, big[j]);
     }
-    float back = 1.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float top = a.bf16 ? __uint_as_float(big[j] << 16)
+      const float top = bf16 ? __uint_as_float(big[j] << 16)
                                : __half2float(__ushort_as_half((unsigned short)big[j]));
       const unsigned e = __float_as_uint(top) >> 23;
       // the row's largest magnitude to [2^8, 2^9); not for zeros, infinities and NaN
       const unsigned up = e == 0 || e == 255 ? 127u : min(262u - e, 252u);
       const float mul = __uint_as_float(up << 23);
-      if (lane == j) back = __uint_as_float((254u - up) << 23);
+      if (lane == i0 + j) back = __uint_as_float((254u - up) << 23);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         float2 f;
-        if (a.bf16) {
+        if (bf16) {
           f = make_float2(__uint_as_float(x[j][i] << 16), __uint_as_float(x[j][i] & 0xffff0000u));
         } else {
           f = __half22float2(*reinterpret_cast<const __half2*>(&x[j][i]));
         }
-        reinterpret_cast<uint32_t*>(place(r0 + j))[i] = pack_f16x2(f.x * mul, f.y * mul);
+        x[j][i] = pack_f16x2(f.x * mul, f.y * mul);
       }
+      store_words<E / 2>(place(r0 + i0 + j), x[j]);
     }
-    if (lane < 4) {  // a lane a row
-      const int r = r0 + lane, row = s.row0 + min(r, s.rows - 1), n = row / a.G;
-      sh.row_c[r] = to_log2 * back;
-      sh.row_at[r] = n * a.Hq + row % a.G;
-      if (a.parent != nullptr) sh.row_path[r] = sh.path[n];
-    }
+  }
+  if (lane < ROWS) {
+    const int r = r0 + lane;
+    sh.row_c[r] = to_log2 * back;
+    sh.row_at[r] = n * Hq + row - n * G;
+    if (tree) sh.row_path[r] = sh.path[n];
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -622,6 +652,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* dead = &sh.dead;
 
+  static_assert(sizeof(AttnArgs) / 4 <= 64 && 64 <= C::THREADS, "a word a thread");
+  if (threadIdx.x < sizeof(AttnArgs) / 4)
+    reinterpret_cast<uint32_t*>(&sh.args)[threadIdx.x] =
+        reinterpret_cast<const uint32_t*>(&a)[threadIdx.x];
+  __syncthreads();
+  const AttnArgs& args = sh.args;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KR; ++i)
       mbar_init(&sh.kr_full[i], 1), mbar_init(&sh.kr_empty[i], 4);
@@ -646,18 +682,26 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   // wait on the kernel before this one, from the lengths as they read then, and
   // again after it in the case that one of them has changed (with more sequences
   // than are kept, always).
-  const Lens lens = {a, sh.len};
+  const Lens lens = {args, sh.len};
   const bool kept = a.c.B <= kLens;
-  (void)attn_lens(a, sh.len, false);
+  (void)attn_lens(args, sh.len, false);
   __syncthreads();
   if (warp == C::wI + 2 && kept) {
-    Run run = attn_run(a, lens, blockIdx.x, gridDim.x);
-    const Seg first = attn_seg(a, lens, run);
+    Run run = attn_run(args, lens, blockIdx.x, gridDim.x);
+    const Seg first = attn_seg(args, lens, run);
     if (lane == 0) sh.run = run, sh.seg[0] = first;
   }
   __syncthreads();
   pdl_enter();
-  const bool changed = attn_lens(a, sh.len, blockIdx.x == 0);
+  // the first segment's queries are on their way while the lengths are read again
+  const bool softmax = warp >= C::wS && warp < C::wI;
+  auto head_scale = [&](int h) { return a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.f; };
+  float k_scale = 1.f;
+  if (softmax && kept && sh.seg[0].t1 > 0) {
+    k_scale = head_scale(sh.seg[0].h);
+    attn_rows_copy<D, NT>(args, sh.seg[0], smem + C::oQ, warp - C::wS);
+  }
+  const bool changed = attn_lens(args, sh.len, blockIdx.x == 0);
   tc::fence_before_sync();
   const bool again = __syncthreads_or(changed) || !kept;
   tc::fence_after_sync();
@@ -670,7 +714,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   Seg s;
   auto next_seg = [&]() {
     const int i = seg_no & (kSegs - 1);
-    attn_wait(&sh.seg_full[i], (seg_no / kSegs) & 1, dead);
+    if (seg_no > 0 || again)  // the first one is there since before the wait
+      attn_wait(&sh.seg_full[i], (seg_no / kSegs) & 1, dead);
     s = sh.seg[i];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.seg_empty[i]);
@@ -728,7 +773,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int quarter = warp & 3;
     const uint32_t dst = ((uint32_t)(quarter * 32) << 16) + C::cV;
     const int vt = threadIdx.x - 32 * C::wV;
-    attn_zero(a, lens, D, vt);
+    attn_zero(args, lens, D, vt);
     int stage = 0, unit = 0, tile = 0;
     unsigned raw_ph = 0, unit_ph = 1;
     for (;; ++seg_no) {
@@ -812,11 +857,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     int tile = 0;
     AttnJoin join = {};
     bool more = next_seg();
-    if (more) attn_rows_copy<D, NT>(a, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
+    if (again) {
+      cp_async_wait_all();  // of the early copy, to the same place
+      if (more) {
+        k_scale = head_scale(s.h);
+        attn_rows_copy<D, NT>(args, s, smem + C::oQ, warp - C::wS);
+      }
+    }
     for (;; ++seg_no) {
       // all softmax warps go on, or none: they meet at barriers below
       if (barrier_any(4, 128 * C::NS, !more)) break;
-      attn_rows<D, NT>(a, sh, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
+      attn_rows<D, NT>(args, sh, s, smem + C::oQ, warp - C::wS, a.scale * (k_scale * kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH / 2) {
@@ -978,7 +1029,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       ++seg_no;
       more = next_seg();
       --seg_no;
-      if (more) attn_rows_copy<D, NT>(a, s, smem + C::oQ, warp - C::wS, 4 * C::NS);
+      if (more) {
+        k_scale = head_scale(s.h);
+        attn_rows_copy<D, NT>(args, s, smem + C::oQ, warp - C::wS);
+      }
       // ---- epilogue
       const bool whole = e.t0 == 0 && e.t1 == e.tiles;
       const int64_t item = (int64_t)e.b * a.N * a.Hq + e.h * a.G;  // output row of node 0
@@ -1051,6 +1105,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty);
     }
+    cp_async_wait_all();  // (only where a wait ran out are there any)
     if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = join;
   } else if (warp == C::wI) {
     // ------------------------------------------------ S^T products (one elected lane)
@@ -1125,7 +1180,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     // ------------------------------------------------ the run's segments, the records in
     const bool lead = warp == C::wI + 2, do_k = C::FW == 1 || lead, do_v = C::FW == 1 || !lead;
     Run run = sh.run;
-    if (lead && again) run = attn_run(a, lens, blockIdx.x, gridDim.x);
+    if (lead && again) run = attn_run(args, lens, blockIdx.x, gridDim.x);
     // lanes 2r and 2r + 1: codes and scales of record r's K half, lanes 8 + 2r and
     // 9 + 2r: of its V half (the first eight lanes where a warp has V alone)
     const int lanes = C::FW == 1 ? 16 : 8;
@@ -1137,12 +1192,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     unsigned k_ph = 1, v_ph = 1;
     for (;; ++seg_no) {
       if (lead) {
-        const bool ready = seg_no == 0 && !again;  // since before the wait
-        s = ready ? sh.seg[0] : attn_seg(a, lens, run);
+        const bool ready = seg_no == 0 && !again;
+        s = ready ? sh.seg[0] : attn_seg(args, lens, run);
         const int i = seg_no & (kSegs - 1);
-        attn_wait(&sh.seg_empty[i], ((seg_no / kSegs) & 1) ^ 1, dead);
+        // (the ring's first pass: empty, and the first segment's readers may be ahead)
+        if (seg_no >= kSegs) attn_wait(&sh.seg_empty[i], ((seg_no / kSegs) & 1) ^ 1, dead);
         if (lane == 0) {
-          sh.seg[i] = s;
+          if (!ready) sh.seg[i] = s;
           mbar_arrive(&sh.seg_full[i]);
         }
         if (s.t1 == 0) break;
