@@ -99,9 +99,10 @@ struct Seg {
 // What a block's work is measured in: an item's tiles, and kLead more before them
 // for what an item costs beside its tiles (its queries, first references and
 // output).  Measured: without the lead 48 sequences of 0 to 8192 tokens took 150 us,
-// the blocks with many short ones twice the others' time; with 2, 4, 8 and 12 it is
-// 109, 85, 85 and 87 us, and eight verified chains of 16 take 78, 75, 71 and 72 us.
-constexpr int kLead = 8;
+// the blocks with many short ones twice the others' time; with 4, 6, 8 and 10 it is
+// 80.5, 80.6, 81.9 and 83.7 us, eight verified chains of 16 take 69.8, 68.8, 69.0 and
+// 68.9 us, a tree of 22 nodes 45.7, 44.7, 45.2 and 44.3 us.
+constexpr int kLead = 6;
 
 // Equal runs of `total` units for at most `parts` blocks: the first `extra` runs
 // have one unit more.  (The host keeps the count below 2^31.)
