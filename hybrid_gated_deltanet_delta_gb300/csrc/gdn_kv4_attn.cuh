@@ -498,14 +498,13 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& len
 // softmax warp.  They are copied as they are to where the operand goes (the copies
 // are this thread's cp.async, not waited for); a lane works out one row's place.
 template <int D, int NT>
-static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, const Seg& s, uint8_t* q,
-                                                   int warp) {
+static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, int b, int h, int row0,
+                                                   int rows, uint8_t* q, int warp) {
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;  // channels of a lane
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
-  const int row = s.row0 + r0 + lane % ROWS, n = row / a.G;
-  const int64_t mine = s.b * a.q_stride_b + n * a.q_stride_n +
-                       (int64_t)(s.h * a.G + row - n * a.G) * D;
-  const int rows = s.rows;
+  const int row = row0 + r0 + lane % ROWS, n = row / a.G;
+  const int64_t mine = b * a.q_stride_b + n * a.q_stride_n +
+                       (int64_t)(h * a.G + row - n * a.G) * D;
   const uint16_t* src = static_cast<const uint16_t*>(a.q) + ch;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
 #pragma unroll
@@ -553,9 +552,9 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&x)[W]) 
 // with the rows is written, a lane a row.
 template <int D, int NT>
 static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
-                                              const Seg& s, uint8_t* q, int warp,
+                                              int b, int row0, int rows, uint8_t* q, int warp,
                                               float to_log2) {
-  const int row0 = s.row0, rows = s.rows, G = a.G, Hq = a.Hq;
+  const int G = a.G, Hq = a.Hq;
   const bool bf16 = a.bf16, tree = a.parent != nullptr;
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
@@ -563,7 +562,7 @@ static __device__ __noinline__ void attn_rows(const AttnArgs& a, AttnShared<Attn
   auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
   if (tree) {
     // path of every node: pointers double their reach in each step
-    const int32_t* p = a.parent + (int64_t)s.b * a.N;
+    const int32_t* p = a.parent + (int64_t)b * a.N;
     int to[2];
     unsigned long long path[2];
 #pragma unroll
@@ -700,7 +699,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   float k_scale = 1.f;
   if (softmax && kept && sh.seg[0].t1 > 0) {
     k_scale = head_scale(sh.seg[0].h);
-    attn_rows_copy<D, NT>(args, sh.seg[0], smem + C::oQ, warp - C::wS);
+    attn_rows_copy<D, NT>(args, sh.seg[0].b, sh.seg[0].h, sh.seg[0].row0, sh.seg[0].rows,
+                          smem + C::oQ, warp - C::wS);
   }
   const bool changed = attn_lens(args, sh.len, blockIdx.x == 0);
   tc::fence_before_sync();
@@ -856,19 +856,20 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int gt = (threadIdx.x - 32 * C::wS) & 127;   // thread of the group
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
-    AttnJoin join = {};
+    if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = AttnJoin{};
     bool more = next_seg();
     if (again) {
       cp_async_wait_all();  // of the early copy, to the same place
       if (more) {
         k_scale = head_scale(s.h);
-        attn_rows_copy<D, NT>(args, s, smem + C::oQ, warp - C::wS);
+        attn_rows_copy<D, NT>(args, s.b, s.h, s.row0, s.rows, smem + C::oQ, warp - C::wS);
       }
     }
     for (;; ++seg_no) {
       // all softmax warps go on, or none: they meet at barriers below
       if (barrier_any(4, 128 * C::NS, !more)) break;
-      attn_rows<D, NT>(args, sh, s, smem + C::oQ, warp - C::wS, a.scale * (k_scale * kLog2e));
+      attn_rows<D, NT>(args, sh, s.b, s.row0, s.rows, smem + C::oQ, warp - C::wS,
+                       a.scale * (k_scale * kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH / 2) {
@@ -1032,7 +1033,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       --seg_no;
       if (more) {
         k_scale = head_scale(s.h);
-        attn_rows_copy<D, NT>(args, s, smem + C::oQ, warp - C::wS);
+        attn_rows_copy<D, NT>(args, s.b, s.h, s.row0, s.rows, smem + C::oQ, warp - C::wS);
       }
       // ---- epilogue
       const bool whole = e.t0 == 0 && e.t1 == e.tiles;
@@ -1046,7 +1047,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         if (lane < C::NH) sh.part[quarter][c0 + lane] = sum;
       }
       if (e.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
-        join = {item, e.h, e.row0, e.rows, (int)slot, e.last};
+        if (threadIdx.x == 32 * C::wS)
+          a.join[blockIdx.x] = {item, e.h, e.row0, e.rows, (int)slot, e.last};
       tc::named_barrier(1 + group, 128);
       if (gt < C::NH) {
         const int r = c0 + gt;
@@ -1107,7 +1109,6 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       if (lane == 0) mbar_arrive(&sh.o_empty);
     }
     cp_async_wait_all();  // (only where a wait ran out are there any)
-    if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = join;
   } else if (warp == C::wI) {
     // ------------------------------------------------ S^T products (one elected lane)
     constexpr uint32_t id = idesc_f16(NT, false);
