@@ -292,6 +292,12 @@ __device__ __forceinline__ float warp_transpose_reduce(float (&v)[N], Op op) {
   return v[0];
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+
 // 8 codes (one word) times the scale pair(s): four f16x2 words.
 __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t* out) {
   out[0] = hmul2(e2m1x2<0>(w), s);
@@ -857,18 +863,25 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
     if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = AttnJoin{};
-    bool more = next_seg();
+    // (the segment stays in the ring until its item is written: registers are short)
+    auto find_seg = [&](int no) {
+      if (no > 0 || again) attn_wait(&sh.seg_full[no & (kSegs - 1)], (no / kSegs) & 1, dead);
+      return sh.seg[no & (kSegs - 1)].t1 > 0 && !__any_sync(0xffffffffu, *dead);
+    };
+    auto fetch_rows = [&](const Seg& n) {
+      k_scale = head_scale(n.h);
+      attn_rows_copy<D, NT>(args, n.b, n.h, n.row0, n.rows, smem + C::oQ, warp - C::wS);
+    };
+    bool more = find_seg(0);
     if (again) {
       cp_async_wait_all();  // of the early copy, to the same place
-      if (more) {
-        k_scale = head_scale(s.h);
-        attn_rows_copy<D, NT>(args, s.b, s.h, s.row0, s.rows, smem + C::oQ, warp - C::wS);
-      }
+      if (more) fetch_rows(sh.seg[0]);
     }
     for (;; ++seg_no) {
       // all softmax warps go on, or none: they meet at barriers below
       if (barrier_any(4, 128 * C::NS, !more)) break;
-      attn_rows<D, NT>(args, sh, s.b, s.row0, s.rows, smem + C::oQ, warp - C::wS,
+      const Seg& e = sh.seg[seg_no & (kSegs - 1)];
+      attn_rows<D, NT>(args, sh, e.b, e.row0, e.rows, smem + C::oQ, warp - C::wS,
                        a.scale * (k_scale * kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
@@ -877,12 +890,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         sh.cm[c0 / 2 + gt] = make_float4(c.x, c.y, -kNone, -kNone);
       }
       tc::named_barrier(1 + group, 128);
-      const int base = s.len - a.N, n_lo = s.row0 / a.G;
+      const int base = e.len - a.N, n_lo = e.row0 / a.G;
       float2 l[C::NH / 2];
 #pragma unroll
       for (int i = 0; i < C::NH / 2; ++i) l[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1; ++t, ++tile) {
+      for (int t = e.t0; t < e.t1; ++t, ++tile) {
         const int buf = tile & 1;
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
@@ -898,7 +911,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
             vis = 0;
           } else if (a.parent == nullptr) {
             // nodes rise with the rows: the first row of node u
-            const int64_t from = (int64_t)u * a.G - s.row0 - c0;
+            const int64_t from = (int64_t)u * a.G - e.row0 - c0;
             vis = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
           } else if (u >= 0) {
             vis = 0;
@@ -912,7 +925,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         }
         const bool masked = __any_sync(0xffffffffu, vis != ~0u);
         attn_wait(&sh.p_empty[buf], ph ^ 1, dead);
-        uint8_t* prow = smem + C::oP + buf * C::PB + (quarter * 32 + lane) * 128;
+        const uint32_t prow = smem_addr(smem) + C::oP + buf * C::PB + (quarter * 32 + lane) * 128;
         uint32_t y[C::NH / 16][16];
         auto load = [&](uint32_t at) {
 #pragma unroll
@@ -922,7 +935,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         };
         // The first tile sets the references; a later one is tried with those there
         // are, and done again in the case that some p passed 2^8.
-        bool raise = t == s.t0;
+        bool raise = t == e.t0;
 #pragma unroll 1
         for (;;) {
           load(sa);
@@ -955,7 +968,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
               sh.alpha[r] = exp2_fast(old - m);
             }
             tc::named_barrier(1 + group, 128);
-            if (t != s.t0) {
+            if (t != e.t0) {
               // every product into O^T so far is done: the last one freed its P
               attn_wait(&sh.p_empty[buf ^ 1], ((tile - 1) >> 1) & 1, dead);
               tc::fence_after_sync();
@@ -1008,9 +1021,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
               top = __vmaxu2(top, p[i]);  // p >= 0: ordered as integers
             }
             const int col = c0 + k;  // 16-byte chunk of 8 rows, swizzled by position
-            *reinterpret_cast<uint4*>(prow + (col >> 6) * (kTile * 128) +
-                                      ((((col & 63) >> 3) ^ (lane & 7)) << 4)) =
-                make_uint4(p[0], p[1], p[2], p[3]);
+            st_shared16(prow + (col >> 6) * (kTile * 128) +
+                            ((((col & 63) >> 3) ^ (lane & 7)) << 4), p);
           }
           if (raise) break;
           raise = barrier_any(1 + group, 128, max(top & 0xffffu, top >> 16) > kMostP);
@@ -1027,14 +1039,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       }
       // S^T's products are done, and Q is free: the next rows are on their way
       // while this item is written
-      const Seg e = s;
-      ++seg_no;
-      more = next_seg();
-      --seg_no;
-      if (more) {
-        k_scale = head_scale(s.h);
-        attn_rows_copy<D, NT>(args, s.b, s.h, s.row0, s.rows, smem + C::oQ, warp - C::wS);
-      }
+      more = find_seg(seg_no + 1);
+      if (more) fetch_rows(sh.seg[(seg_no + 1) & (kSegs - 1)]);
       // ---- epilogue
       const bool whole = e.t0 == 0 && e.t1 == e.tiles;
       const int64_t item = (int64_t)e.b * a.N * a.Hq + e.h * a.G;  // output row of node 0
@@ -1106,7 +1112,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_empty);
+      if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.seg_empty[seg_no & (kSegs - 1)]);
     }
     cp_async_wait_all();  // (only where a wait ran out are there any)
   } else if (warp == C::wI) {
