@@ -19,15 +19,17 @@
 // starts or ends inside an item writes that part's O, m and l to the workspace,
 // and join_kernel adds the parts in block order; whole items are written at once.
 //
-// Warps of a block (24, in groups of four), connected by mbarriers only:
-//   K groups   position = TMEM lane; codes * scale -> binary16 -> TMEM (64 channels a unit)
-//   V groups   channel = TMEM lane; the same for V^T (32 positions a unit)
-//   softmax groups, 32 rows each: S^T from TMEM, p to shared memory (B operand),
-//              sums in registers, the item's epilogue, and the next item's queries into
-//              the B operand (binary16, scaled by a power of two per row so that any
-//              bf16 magnitude fits)
-//   and a warp each that issues S^T's products, issues O^T's, and cuts the run into
-//   segments and copies the records (with few rows, a warp each for K and V halves).
+// Warps of a block, connected by mbarriers only:
+//   4 of K      position = TMEM lane; codes * scale -> binary16 -> TMEM, in units of 64 or
+//               128 channels
+//   4 of V      channel = TMEM lane; the same for V^T, in units of 32 or 64 positions
+//   4 or more of softmax, a group of four for 16 or 32 rows: S^T from TMEM, p to shared
+//               memory (B operand), sums in registers, the item's epilogue, and the next
+//               item's queries into the B operand (binary16, scaled by powers of two so
+//               that any bf16 magnitude fits)
+//   1 that issues S^T's products, 1 that issues O^T's (products into one accumulator
+//               come from one thread: across threads they have no order)
+//   1 or 2 that cut the run into segments and copy the records
 //
 // The reference m is moved only when some p would pass 2^8 (p is at most 65504
 // in binary16): the sums and O^T are then multiplied by 2^(old - new), which
@@ -35,6 +37,18 @@
 // one FMA, one maximum, one exp2 and one addition per logit and no reduction
 // across lanes.  p is rounded to binary16 for the product (2^-11; bf16 would
 // give 2^-8); code * scale needs 6 significand bits, so K and V are exact.
+//
+// What bounds it.  With few rows the bytes: a tile of 36.8 KB (D = 256) takes 0.93 us a
+// block, 39.6 GB/s an SM of 43.8 measured for a copy; 131072 tokens of 4 heads take
+// 37.7 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
+// item's output and the join.  With 96 rows the softmax warps: 1.6 us a tile, of which 0.5
+// us is the exponentials' issue at 80 registers, the tensor pipe 0.8 us; a 2048-token piece
+// of a prompt at 8192 tokens runs at 985 TFLOP/s of 1,880 measured.
+// Measured and left out (us for 131072 tokens / the prompt, against the figure of the
+// time): the products issued by the K and V warps themselves, 55 / 500 against 50 / 464;
+// two streams of tiles, each with softmax warps, 58 / 693 against 50 / 464; steps of two
+// tiles with few rows, 41.8 against 39.9; a second group of K and V warps with few rows,
+// 170 against 152 for 48 sequences; softmax groups of 24 rows, - / 500 against 401.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -63,7 +77,9 @@ struct AttnCfg {
   static constexpr int ROWS = NT / (4 * NS);        // query rows that a softmax warp brings in
   static constexpr bool COMMON = NT >= 64;          // one scale for all rows (attn_rows)
   static constexpr int wV = 4, wS = 8;  // first warps of the roles
-  static constexpr int wI = wS + 4 * NS, FW = NT < 64 ? 2 : 1;  // warps that copy: a tile of few rows is short
+  // warps that copy: with few rows a tile is short (48 sequences: two 85 us, one 103 us),
+  // with many the registers of a warp less count more (the prompt: one 407 us, two 417 us)
+  static constexpr int wI = wS + 4 * NS, FW = NT < 64 ? 2 : 1;
   static constexpr int THREADS = 32 * (wI + 2 + FW);
   // TMEM columns: two K units (KW columns of 2 channels each), two S^T, O^T, two V units
   // (VW records each).  Large units cost fewer hand-overs; the widest case has no

@@ -267,8 +267,8 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
 // Grid (pieces of the (layer, head) pairs, B).  A block of up to 64 nodes lies in at
 // most three records.  The path is found once a block of threads, in shared memory;
 // then each warp moves K and the scales, or 128 channels of V, of one (layer, head)
-// pair at a time.  K codes and scales are moved by word, each word position by one lane, eight path nodes read
-// before they are written (a node's source is never an earlier node's destination,
+// pair at a time.  K codes and scales are moved by word, each word position by one
+// lane, eight path nodes read before they are written (a node's source is never an earlier node's destination,
 // since the i-th node of a path has index >= i).  A V channel's codes are gathered
 // nibble by nibble by the lane that owns the channel, from its rows in shared
 // memory; the places are the same for all channels, so a warp's lanes read one

@@ -43,9 +43,11 @@
  *    completed and its memory is visible, then lets the next kernel begin
  *    launching.  Stream order is kept for every read and write.  Before that
  *    wait a kernel only issues L2 prefetch hints for lines it will read
- *    (which never change memory).  A kernel of the caller's that follows one
- *    of ours with the same launch attribute must itself wait before reading
- *    our outputs (griddepcontrol.wait), as programmatic launch requires.
+ *    (which never change memory), or reads arrays of lengths and parents that
+ *    it reads again after it and then goes by.  A kernel of the caller's that
+ *    follows one of ours with the same launch attribute must itself wait
+ *    before reading our outputs (griddepcontrol.wait), as programmatic launch
+ *    requires.
  *  - All pointers must be 16-byte aligned; element strides are in elements.
  *  - Host-detected errors return a negative gdn_status before anything is
  *    launched.  Errors that depend on device data (a malformed tree, an
@@ -484,7 +486,12 @@ int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype
  * device) need not be initialised and may be reused once the call's work has
  * finished on the stream; the size depends on the sizes given here only, not on
  * the lengths.  The probabilities are rounded to binary16 for the product with
- * v; sums and the running maximum are fp32.
+ * v; sums and the running maximum are fp32.  The order of the sums depends on the
+ * lengths and the device alone: repeated calls give the same bits.
+ * GDN_ERR_UNSUPPORTED when B * Hkv * N * (Hq / Hkv) / 96 times max_pages *
+ * page_tokens / 128 would not fit 31 bits (work is counted in tiles of 128
+ * positions).  A wait inside the kernel that runs out is reported as
+ * GDN_ERR_TIMEOUT; the outputs are then undefined.
  */
 size_t gdn_kv4_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
                                          int32_t D);
