@@ -43,7 +43,7 @@
 // 37.7 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
 // item's output and the join.  With 96 rows the softmax warps: 1.6 us a tile, of which 0.5
 // us is the exponentials' issue at 80 registers, the tensor pipe 0.8 us; a 2048-token piece
-// of a prompt at 8192 tokens runs at 985 TFLOP/s of 1,880 measured.
+// of a prompt at 8192 tokens takes 365 us, 990 TFLOP/s of 1,880 measured.
 // Measured and left out (us for 131072 tokens / the prompt, against the figure of the
 // time): the products issued by the K and V warps themselves, 55 / 500 against 50 / 464;
 // two streams of tiles, each with softmax warps, 58 / 693 against 50 / 464; steps of two
@@ -88,6 +88,10 @@ struct AttnCfg {
   static constexpr int KW = BIG && D >= 128 ? 64 : 32, VW = BIG ? 2 : 1;
   static constexpr int UNITS = D / 2 / KW, VUNITS = 4 / VW;  // of a tile
   static constexpr int KU = 2, VU = 2;
+  // of the K and V warps' units: with many rows all roles' loops together strain the
+  // instruction cache (a 2048-token piece of a prompt: unrolled 377 us, rolled 365), with
+  // few they do less (131072 tokens: unrolled 37.3 us, rolled 38.4)
+  static constexpr int UNROLL = NT < 64 ? 8 : 1;
   static constexpr int cS = KW * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
   static_assert(cV + VU * VW * 16 * MB <= 512, "TMEM");
   // shared memory
@@ -781,7 +785,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const uint8_t* scales = smem + C::oK + stage * C::RAW + warp * C::HALF + 16 * D +
                                 lane * (D / 16);
         uint4 q4 = *reinterpret_cast<const uint4*>(rec);
-#pragma unroll
+#pragma unroll C::UNROLL
         for (int u = 0; u < C::UNITS; ++u) {
 #pragma unroll
           for (int k = 0; k < C::KW / 16; ++k) {  // 32 channels: one 16-byte chunk
@@ -853,14 +857,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const uint8_t* codes = raw + (mine ? ch * 16 : 0);
         const uint8_t* scales = vs + (ch >> 4) * C::VSG;
         uint4 q4 = *reinterpret_cast<const uint4*>(codes);
+#pragma unroll C::UNROLL
+        for (int u = 0; u < C::VUNITS; ++u, codes += C::VW * C::HALF, scales += C::VW * 64) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-#pragma unroll
-          for (int mb = 0; mb < C::MB; ++mb) {
+          for (int k = 0; k < C::VW * C::MB; ++k) {  // 128 channels of a record
+            const int r = k / C::MB, mb = k % C::MB, next = k + 1;
             const uint32_t c4[4] = {q4.x, q4.y, q4.z, q4.w};
             // the next 16 bytes: the other channel block's, or the next record's
-            const int next = r * C::MB + mb + 1;
-            if (next < 4 * C::MB)
+            if (next < C::VW * C::MB || u + 1 < C::VUNITS)
               q4 = *reinterpret_cast<const uint4*>(codes + next / C::MB * C::HALF +
                                                    next % C::MB * 2048);
             uint32_t w[16];
@@ -874,19 +878,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
               w[4 * i + 2] = hmul2(e2m1x2<2>(c4[i]), s4.z);
               w[4 * i + 3] = hmul2(e2m1x2<3>(c4[i]), s4.w);
             }
-            if (mb == 0 && r % C::VW == 0) {
+            if (k == 0) {
               attn_wait(&sh.v_empty[unit], unit_ph, dead);
               tc::fence_after_sync();
             }
-            tmem_st16(dst + ((unit * C::VW + r % C::VW) * C::MB + mb) * 16, w);
+            tmem_st16(dst + ((unit * C::VW + r) * C::MB + mb) * 16, w);
           }
-          if (r % C::VW == C::VW - 1) {
-            tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_full[unit]);
-            if (++unit == C::VU) unit = 0, unit_ph ^= 1;
-          }
+          tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_full[unit]);
+          if (++unit == C::VU) unit = 0, unit_ph ^= 1;
         }
         if (lane == 0) mbar_arrive(&sh.vr_empty[stage]);
         if (++stage == C::VR) stage = 0, raw_ph ^= 1;
