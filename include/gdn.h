@@ -486,7 +486,9 @@ int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype
  * device) need not be initialised and may be reused once the call's work has
  * finished on the stream; the size depends on the sizes given here only, not on
  * the lengths.  The probabilities are rounded to binary16 for the product with
- * v; sums and the running maximum are fp32.  The order of the sums depends on the
+ * v; queries are held as binary16, scaled by powers of two (exact down to 2^-14
+ * of their row's largest element, within 2^-25 of it below); sums and the
+ * running maximum are fp32.  The order of the sums depends on the
  * lengths and the device alone: repeated calls give the same bits.
  * GDN_ERR_UNSUPPORTED when B * Hkv * N * (Hq / Hkv) / 96 times max_pages *
  * page_tokens / 128 would not fit 31 bits (work is counted in tiles of 128

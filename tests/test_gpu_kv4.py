@@ -739,3 +739,53 @@ def test_reserve_of_large_pools(gpu_lib, n_pages, F, offset, short):
         assert np.array_equal(got.cpu().numpy(), exp)
     assert bool(failed) == short
     assert int(status.item()) == (gpu_lib.GDN_ERR_POOL_EMPTY if short else 0)
+
+
+# ------------------------------------------------------------------ wide tiles' scale
+@pytest.mark.parametrize("dtype, spread, D", [
+    ("bf16", 8, 128), ("f16", 8, 64), ("bf16", 9, 256), ("bf16", 60, 128), ("f16", 20, 256)])
+def test_attention_rows_of_many_magnitudes_in_a_wide_tile(gpu_lib, dtype, spread, D):
+    """80 rows whose largest magnitudes span 2^spread (up to 2^8 they share a scale), with
+    elements over the type's whole precision and some rows of zeros."""
+    rng, t = np.random.default_rng(50 + spread + D), torch()
+    s = Setup(rng, [333, 150], 1, D, 64)
+    cache = s.fill(rng)
+    B, N, Hq = 2, 20, 4
+    q = rng.uniform(-1, 1, (B, N, Hq, D)) * 2.0 ** rng.integers(-14, 1, (B, N, Hq, D))
+    row = rng.integers(0, spread + 1, (B, N, Hq))
+    row[:, 0, 0], row[:, 1, 0] = 0, spread
+    top = np.abs(q).max(-1)
+    q = q / 2.0 ** np.floor(np.log2(top))[..., None] * 2.0 ** (4.0 - row)[..., None]
+    q[:, 5, 1] = 0
+    q = t.from_numpy(q).cuda().to(tdtype(dtype))
+    check_attention(gpu_lib, s, cache, q, dtype, 0.05)
+    check_attention(gpu_lib, s, cache, q, dtype, 0.05, rand_trees(rng, B, N))
+
+
+def test_attention_infinite_and_nan_queries_in_a_wide_tile(gpu_lib):
+    """They stay in their row: the others' bits are those beside rows of zeros."""
+    rng, t = np.random.default_rng(60), torch()
+    s = Setup(rng, [500], 1, 128, 32)
+    s.fill(rng)
+    kw = s.gpu()
+    q = t.from_numpy(rng.standard_normal((1, 24, 4, 128))).cuda().to(t.bfloat16)
+    ws = t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(1, 24, 4, 1, 128), dtype=t.uint8,
+                 device="cuda")
+
+    def run(value):
+        x, o = q.clone(), t.empty_like(q)
+        x[0, 3, 1, 7], x[0, 9, 0] = value, value
+        gpu_lib.gdn_kv4_attention(x, s.g_pages, s.g_table, s.g_len, o, ws, scale=0.1, **kw)
+        return o
+
+    x = q.clone()
+    x[0, 3, 1], x[0, 9, 0] = 0, 0
+    base = t.empty_like(q)
+    gpu_lib.gdn_kv4_attention(x, s.g_pages, s.g_table, s.g_len, base, ws, scale=0.1, **kw)
+    others = t.ones(1, 24, 4, dtype=t.bool, device="cuda")
+    others[0, 3, 1] = others[0, 9, 0] = False
+    for value in (float("nan"), float("inf"), -float("inf")):
+        o = run(value)
+        assert t.equal(o[others], base[others])
+        assert not t.isfinite(o[0, 9, 0]).any()
+    assert int(s.status.item()) == 0
