@@ -266,18 +266,21 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
 // ---------------------------------------------------------------- commit
 // Grid (pieces of the (layer, head) pairs, B).  A block of up to 64 nodes lies in at
 // most three records.  The path is found once a block of threads, in shared memory;
-// then each warp moves K and the scales, or 128 channels of V, of one (layer, head)
+// then each warp moves K and the scales, or 64 channels of V, of one (layer, head)
 // pair at a time.  K codes and scales are moved by word, each word position by one
-// lane, eight path nodes read before they are written (a node's source is never an earlier node's destination,
-// since the i-th node of a path has index >= i).  A V channel's codes are gathered
-// nibble by nibble by the lane that owns the channel, from its rows in shared
-// memory; the places are the same for all channels, so a warp's lanes read one
-// word each of one row.  Bound by latency: few bytes have to move, but the rows of V
-// that hold them are read and written whole.  64 trees of 22 nodes, 8 heads of 128
-// channels, 16 layers: 38 us with a block a (layer, head) pair that walks the path
-// in global memory, 31 us with four layers to a block and the path in shared memory,
-// 26 us with blocks that do not all fit at once, 23.7 us this way (one tree: 6.2, 9.0,
-// 4.9 and 4.6 us).  Four blocks an SM spill: 27 us.
+// lane, eight path nodes read before they are written (a node's source is never an
+// earlier node's destination, since the i-th node of a path has index >= i).  A V
+// channel's codes are gathered nibble by nibble by the lane that owns the channel,
+// from its words in shared memory, two channels a lane: a nibble's place and turn are
+// worked out once, and cost each channel a rotation and a select.  Bound by latency
+// and those instructions: few bytes have to move, but the rows of V that hold them
+// are read and written whole.  64 trees of 22 nodes, 8 heads of 128 channels, 16
+// layers: 38 us with a block a (layer, head) pair that walks the path in global
+// memory, 31 us with four layers to a block and the path in shared memory, 26 us with
+// blocks that do not all fit at once, 23.5 us with one wave and a channel's nibbles
+// moved one by one, 15.7 us this way (one tree: 6.2, 9.0, 4.9, 4.6 and 3.9 us).  Of
+// waves of 456, 608, 760 and 912 blocks 608 (four an SM) took least: 16.9, 15.7, 18.0
+// and 17.2 us.
 constexpr int kMaxNodes = 64;
 constexpr int kWindow = 3;
 constexpr int kCommitWarps = kThreads / 32;
@@ -289,7 +292,8 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
   __shared__ int up[kMaxNodes], back[kMaxNodes];  // parents; the path from its end
   __shared__ int count, bad_tree;
   __shared__ uint8_t* recs[kWindow];  // of head 0, layer 0
-  __shared__ uint32_t rows[kCommitWarps][kWindow * 4][32];
+  __shared__ int src[kMaxNodes];  // where the i-th node of the path is, from the first record
+  __shared__ uint2 rows[kCommitWarps][kWindow * 4][32];
   pdl_enter();
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool lead = blockIdx.x == 0;
@@ -334,16 +338,17 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
   __syncthreads();
   const int m = count;
   if (m == 0) return;
-  auto path = [&](int i) { return back[m - 1 - i]; };
   const int off = (len - N) % kRec;
+  for (int i = threadIdx.x; i < m; i += kThreads) src[i] = off + back[m - 1 - i];
+  __syncthreads();
   int first = 0;  // nodes before it stay
-  while (path(first) == first) ++first;
+  while (src[first] == off + first) ++first;
   constexpr int kw = D / 8, sw = D / 64;  // words of a token's K codes, K scales
   const int rec0 = (off + first) / kRec, rec1 = (off + m - 1) / kRec;  // written
-  const int last = (off + path(m - 1)) / kRec;                         // read
+  const int last = src[m - 1] / kRec;                                  // read
   const int64_t head_stride = (int64_t)(c.page_tokens / kRec) * rec_bytes(D);
-  // a warp's work: a (layer, head) pair's K and scales, or 128 channels of its V
-  constexpr int CH = D / 32 < 4 ? D / 32 : 4, PARTS = 1 + D / (32 * CH);
+  // a warp's work: a (layer, head) pair's K and scales, or 64 channels of its V
+  constexpr int PARTS = 1 + D / 64;
   for (int i = blockIdx.x * kCommitWarps + warp; i < n_layers * c.Hkv * PARTS;
        i += gridDim.x * kCommitWarps) {
     const int part = i % PARTS, pair = i / PARTS;
@@ -360,7 +365,7 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (e0 + k >= m) break;
-          const int from = off + path(e0 + k);
+          const int from = src[e0 + k];
           const uint8_t* s = recs[from / kRec] + at + from % kRec * step;
           x[k] = byte ? *s : *reinterpret_cast<const uint32_t*>(s);
         }
@@ -375,44 +380,45 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
       }
     }
     if (part > 0) {
-      const int c0 = (part - 1) * 32 * CH + lane;
-      uint4 v[CH][kWindow];
+      // two channels a lane, the words of 8 tokens of both beside each other
+      const int64_t at = at0 + off_v(D) + ((part - 1) * 64 + lane) * 16;
+      uint4 v[2][kWindow];
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int w = 0; w < kWindow; ++w)
           if (w >= rec0 && w <= last)
-            v[k][w] = *reinterpret_cast<const uint4*>(recs[w] + at0 + off_v(D) +
-                                                      (c0 + 32 * k) * 16);
+            v[k][w] = *reinterpret_cast<const uint4*>(recs[w] + at + k * 512);
+      uint2(&row)[kWindow * 4][32] = rows[warp];
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        uint32_t(&row)[kWindow * 4][32] = rows[warp];
-#pragma unroll
-        for (int w = 0; w < kWindow; ++w)
-          if (w >= rec0 && w <= last) {
-            row[w * 4][lane] = v[k][w].x, row[w * 4 + 1][lane] = v[k][w].y;
-            row[w * 4 + 2][lane] = v[k][w].z, row[w * 4 + 3][lane] = v[k][w].w;
-          }
-        // words of 8 tokens, in order: a word's sources are at or after it
-        for (int w = (off + first) >> 3; w <= (off + m - 1) >> 3; ++w) {
-          uint32_t x = row[w][lane];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const int e = 8 * w + t - off;
-            if (e < first || e >= m) continue;
-            const int from = off + path(e);
-            const uint32_t code = row[from >> 3][lane] >> (4 * (from & 7)) & 15u;
-            x = (x & ~(15u << (4 * t))) | code << (4 * t);
-          }
-          row[w][lane] = x;
+      for (int w = 0; w < kWindow; ++w)
+        if (w >= rec0 && w <= last) {
+          row[w * 4][lane] = make_uint2(v[0][w].x, v[1][w].x);
+          row[w * 4 + 1][lane] = make_uint2(v[0][w].y, v[1][w].y);
+          row[w * 4 + 2][lane] = make_uint2(v[0][w].z, v[1][w].z);
+          row[w * 4 + 3][lane] = make_uint2(v[0][w].w, v[1][w].w);
         }
-#pragma unroll
-        for (int w = 0; w < kWindow; ++w)
-          if (w >= rec0 && w <= rec1)
-            *reinterpret_cast<uint4*>(recs[w] + at0 + off_v(D) + (c0 + 32 * k) * 16) =
-                make_uint4(row[w * 4][lane], row[w * 4 + 1][lane], row[w * 4 + 2][lane],
-                           row[w * 4 + 3][lane]);
+      // words in order: a word's sources are at or after it
+      for (int w = (off + first) >> 3; w <= (off + m - 1) >> 3; ++w) {
+        uint2 x = row[w][lane];
+        const int e0 = 8 * w - off;
+        for (int e = max(e0, first); e < min(e0 + 8, m); ++e) {
+          const int from = src[e], to = 4 * (e - e0), turn = 4 * from - to;
+          const uint32_t here = 15u << to;
+          const uint2 y = row[from >> 3][lane];
+          x.x = (x.x & ~here) | (__funnelshift_r(y.x, y.x, turn) & here);
+          x.y = (x.y & ~here) | (__funnelshift_r(y.y, y.y, turn) & here);
+        }
+        row[w][lane] = x;
       }
+#pragma unroll
+      for (int w = 0; w < kWindow; ++w)
+        if (w >= rec0 && w <= rec1) {
+          const uint2 a0 = row[w * 4][lane], a1 = row[w * 4 + 1][lane];
+          const uint2 a2 = row[w * 4 + 2][lane], a3 = row[w * 4 + 3][lane];
+          *reinterpret_cast<uint4*>(recs[w] + at) = make_uint4(a0.x, a1.x, a2.x, a3.x);
+          *reinterpret_cast<uint4*>(recs[w] + at + 512) = make_uint4(a0.y, a1.y, a2.y, a3.y);
+        }
     }
   }
 }
@@ -466,8 +472,8 @@ int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers
   // A unit of work a warp while the blocks are one wave, else one wave of blocks with
   // more units each (their path is found once), up to eight; a chain moves nothing:
   // one block per sequence writes its length.
-  const int64_t units = (int64_t)n_layers * c.Hkv * (c.D == 256 ? 3 : 2);
-  const int64_t wave = 152 * 3, most = (units + kCommitWarps - 1) / kCommitWarps;
+  const int64_t units = (int64_t)n_layers * c.Hkv * (1 + c.D / 64);
+  const int64_t wave = 152 * 4, most = (units + kCommitWarps - 1) / kCommitWarps;
   const int64_t few = wave / c.B > (most + 7) / 8 ? wave / c.B : (most + 7) / 8;
   const dim3 grid(parent == nullptr ? 1 : (unsigned)(most < few ? most : few), c.B);
   switch (c.D) {
