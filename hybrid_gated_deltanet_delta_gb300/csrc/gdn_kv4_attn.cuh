@@ -1339,7 +1339,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
 // Grid (blocks of the main kernel, pieces of the rows): the item that block x
 // left unfinished, if any: the parts of blocks x .. last, in that order.  A thread
 // has four channels, of one row; with few rows (NT = 16) the block's threads share
-// one row and take every NP-th part each, else each D/4 of them take a row.
+// one row and take every NP-th part each, else each D/4 of them take a row.  Bound
+// by latency: it ends 3.3 us after the last block of the main kernel for eight chains
+// (32 items over 152 blocks, 15 MB of parts), 4.6 us for a tree (8 items, 19 parts
+// each), 5.2 us for one sequence (4 items, 38 parts each).
 constexpr int kJoinThreads = 256;
 
 template <int D, bool ONE_ROW>
