@@ -459,6 +459,8 @@ int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
   if (st != GDN_OK) return st;
   if (Hkv < 1 || n_layers < 1) return GDN_ERR_INVALID_ARG;
   if (!kv4_head_size(D) || n_layers > 65535 || Hkv > 65535) return GDN_ERR_UNSUPPORTED;
+  // the plan adds up in 32 bits what all rows ask for, max_pages each at most
+  if ((int64_t)F * p->max_pages > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
   const int64_t head = (int64_t)(p->page_tokens / 32) * 36 * D;
   if (page_stride < head * Hkv) return GDN_ERR_INVALID_ARG;
   if (n_layers > 1 && layer_stride < (int64_t)p->n_pages * page_stride)

@@ -557,7 +557,8 @@ int gdn_kv4_fork(const gdn_kv4_pool* p, const int32_t* src, const int32_t* dst, 
  * n_layers layers (copy-on-write), and the old page loses a holder.  A row that
  * does not fit, and every row after it that needs pages, is left as it is:
  * GDN_ERR_POOL_EMPTY.  Afterwards positions below new_len[i] from the old
- * length on may be appended to.
+ * length on may be appended to.  GDN_ERR_UNSUPPORTED when F * max_pages would
+ * not fit 31 bits (the pages that the rows ask for are added up).
  */
 size_t gdn_kv4_reserve_workspace_bytes(int32_t F);
 

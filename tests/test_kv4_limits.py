@@ -1,0 +1,35 @@
+"""Sizes of the gdn_kv4_* calls at which a count would pass 32 bits: refused on the host
+before anything is launched, and answered by the size functions without a fault."""
+import ctypes
+
+import pytest
+
+import hybrid_gated_deltanet_delta_gb300 as gdn
+from hybrid_gated_deltanet_delta_gb300 import build as gdn_build
+
+V = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    gdn_build.build()
+    return gdn.load()
+
+
+def reserve(lib, *, F=2, Hkv=4, D=256, page_tokens=64, page_stride=None, **kw):
+    p = gdn.Kv4Pool()
+    base = dict(table=0x10000, kv_len=0x20000, ref=0x30000, table_stride=8, n_rows=4, max_pages=8,
+                n_pages=100, page_tokens=page_tokens)
+    base.update(kw)
+    for key, val in base.items():
+        setattr(p, key, val)
+    stride = page_stride or Hkv * (page_tokens // 32) * 36 * D
+    return lib.gdn_kv4_reserve(ctypes.byref(p), V(0x1000), stride, 0, 1, Hkv, D, V(0x100),
+                               V(0x200), F, V(0x3000), 1 << 40, None)
+
+
+@pytest.mark.parametrize("F, max_pages", [(65535, 32769), (60000, 60_000_000), (50, 60_000_000)])
+def test_reserve_refuses_more_pages_than_it_can_count(lib, F, max_pages):
+    assert F * max_pages > 0x7fffffff
+    assert reserve(lib, F=F, n_rows=65535, max_pages=max_pages, table_stride=max_pages,
+                   page_tokens=32) == gdn.GDN_ERR_UNSUPPORTED
