@@ -465,7 +465,8 @@ int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
   if (page_stride < head * Hkv) return GDN_ERR_INVALID_ARG;
   if (n_layers > 1 && layer_stride < (int64_t)p->n_pages * page_stride)
     return GDN_ERR_INVALID_ARG;
-  if (head * Hkv / 16 > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+  // the copy's and the plan's indices go on in steps of 4096 past the last one, in 32 bits
+  if (head * Hkv / 16 > 0x7ffff000 || p->n_pages > 0x7ffff000) return GDN_ERR_UNSUPPORTED;
   if (page_stride % 16 != 0 || layer_stride % 16 != 0) return GDN_ERR_MISALIGNED;
   if (F == 0) return GDN_OK;
   if (pages == nullptr) return GDN_ERR_INVALID_ARG;

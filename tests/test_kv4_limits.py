@@ -33,3 +33,16 @@ def test_reserve_refuses_more_pages_than_it_can_count(lib, F, max_pages):
     assert F * max_pages > 0x7fffffff
     assert reserve(lib, F=F, n_rows=65535, max_pages=max_pages, table_stride=max_pages,
                    page_tokens=32) == gdn.GDN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("records", [3728264, 3728269])
+def test_reserve_refuses_pages_that_its_copy_cannot_index(lib, records):
+    """Pages of almost 2^31 units of 16 bytes: the copy's next index would pass 32 bits."""
+    assert 0x7fffffff - 4095 < records * 36 * 256 // 16 <= 0x7fffffff
+    assert reserve(lib, Hkv=1, page_tokens=32 * records, max_pages=1,
+                   table_stride=1) == gdn.GDN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("n_pages", [0x7fffffff, 0x7fffffff - 4094])
+def test_reserve_refuses_more_counts_than_its_plan_can_index(lib, n_pages):
+    assert reserve(lib, n_pages=n_pages) == gdn.GDN_ERR_UNSUPPORTED
