@@ -170,12 +170,16 @@ int prefill_checks(const void* q, const void* k, const void* v, int32_t in_dtype
 
 bool kv4_head_size(int32_t D) { return D == 64 || D == 128 || D == 256; }
 
+// Nodes of a block, and nodes times query heads, that the kernels count in 32 bits.
+constexpr int32_t kMostNodes = 1 << 24;
+bool kv4_rows(int32_t N, int32_t Hq) { return N <= kMostNodes && (int64_t)N * Hq <= (1 << 30); }
+
 int kv4_checks(const gdn_kv4_cache* c, int32_t N) {
   if (c == nullptr) return GDN_ERR_INVALID_ARG;
   if (c->B < 0 || N < 1 || c->Hkv < 1 || c->max_pages < 1 || c->n_pages < 1 || c->page_tokens < 1)
     return GDN_ERR_INVALID_ARG;
   if (!kv4_head_size(c->D) || c->page_tokens % 32 != 0) return GDN_ERR_UNSUPPORTED;
-  if (c->B > 65535 || c->Hkv > 65535 || N > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+  if (c->B > 65535 || c->Hkv > 65535 || N > kMostNodes) return GDN_ERR_UNSUPPORTED;
   if ((int64_t)c->max_pages * c->page_tokens > 0x7fffffffLL - (1 << 24))
     return GDN_ERR_UNSUPPORTED;
   if (c->table_stride < c->max_pages) return GDN_ERR_INVALID_ARG;
@@ -383,6 +387,7 @@ int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype
 size_t gdn_kv4_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
                                          int32_t D) {
   if (B < 1 || N < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || !kv4_head_size(D)) return 0;
+  if (B > 65535 || Hkv > 65535 || !kv4_rows(N, Hq)) return 0;
   return gdn::kv4_attention_workspace_bytes(B, N, Hq, Hkv, D);
 }
 
@@ -397,7 +402,7 @@ int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int6
   if (dtype == GDN_F32) return GDN_ERR_UNSUPPORTED;
   if (dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
   if (parent != nullptr && N > 64) return GDN_ERR_UNSUPPORTED;
-  if ((int64_t)N * Hq > (1 << 30)) return GDN_ERR_UNSUPPORTED;
+  if (!kv4_rows(N, Hq)) return GDN_ERR_UNSUPPORTED;
   if (c->B == 0) return GDN_OK;
   if (q == nullptr || o == nullptr) return GDN_ERR_INVALID_ARG;
   if (!gdn::aligned16(q) || !gdn::aligned16(o) || !gdn::aligned16(workspace))

@@ -46,3 +46,14 @@ def test_reserve_refuses_pages_that_its_copy_cannot_index(lib, records):
 @pytest.mark.parametrize("n_pages", [0x7fffffff, 0x7fffffff - 4094])
 def test_reserve_refuses_more_counts_than_its_plan_can_index(lib, n_pages):
     assert reserve(lib, n_pages=n_pages) == gdn.GDN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("N, Hq", [(1 << 29, 8), (1 << 24, 4096), (1 << 24, 256), (1 << 23, 256),
+                                   (400_000_000, 6), ((1 << 24) + 1, 1), (1 << 24, 65)])
+def test_attention_workspace_of_sizes_that_are_refused_is_0(lib, N, Hq):
+    """As for the other sizes that gdn_kv4_attention refuses; rows past 2^31 divided by 0."""
+    assert lib.gdn_kv4_attention_workspace_bytes(1, N, Hq, 1, 256) == 0
+
+
+def test_attention_workspace_of_the_largest_call(lib):
+    assert lib.gdn_kv4_attention_workspace_bytes(1, 1 << 24, 64, 1, 256) > 0
