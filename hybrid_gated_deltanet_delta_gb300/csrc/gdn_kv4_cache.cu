@@ -321,18 +321,16 @@ commit_kernel(gdn_kv4_cache c, int64_t layer_stride, int n_layers, int N, const 
     else if (bad_tree) err = GDN_ERR_BAD_TREE;
     if (err == GDN_OK && parent != nullptr)
       for (int n = a; n >= 0; n = up[n]) back[m++] = n;
+    // a chain's path is where it is, and so is one of the nodes 0 .. m - 1
+    const bool moves = err == GDN_OK && parent != nullptr && a != m - 1;
+    if (moves)  // all of the block's pages, before anything is written
+      for (int w = 0; w < kWindow; ++w)
+        if (((len - N) / kRec + w) * kRec < len && recs[w] == nullptr) err = GDN_ERR_PAGE_RANGE;
     if (lead) {
       if (err != GDN_OK) report(c.status, err);
       len_out[b] = err == GDN_OK ? len - N + m : c.kv_len[b];
     }
-    // a chain's path is where it is, and so is one of the nodes 0 .. m - 1
-    if (err != GDN_OK || parent == nullptr || a == m - 1) m = 0;
-    if (m > 0)
-      for (int w = 0; w < kWindow; ++w)
-        if (((len - N) / kRec + w) * kRec < len && recs[w] == nullptr) {
-          if (lead) report(c.status, GDN_ERR_PAGE_RANGE);
-          m = 0;
-        }
+    if (err != GDN_OK || !moves) m = 0;
     count = m;
   }
   __syncthreads();

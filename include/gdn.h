@@ -511,9 +511,13 @@ int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int6
  * and values are moved to position kv_len[b] - N + i, codes and scales
  * unchanged, and len_out[b] = kv_len[b] - N + (nodes on the path).  Positions
  * from len_out[b] on keep unspecified contents.  len_out must not be kv_len.
- * A block with kv_len[b] < N, a bad accept index or a malformed parent array
- * leaves the sequence as it is (len_out[b] = kv_len[b]) and is reported
- * (GDN_ERR_ROW_RANGE, GDN_ERR_ACCEPT_RANGE, GDN_ERR_BAD_TREE).
+ * A block with kv_len[b] < N, a bad accept index or a malformed parent array, or
+ * one that has nodes to move and lies, in whole or in part, on a page number
+ * outside the pool, leaves the sequence as it is in every layer (len_out[b] =
+ * kv_len[b]) and is reported (GDN_ERR_ROW_RANGE, GDN_ERR_ACCEPT_RANGE,
+ * GDN_ERR_BAD_TREE, GDN_ERR_PAGE_RANGE).  Pages that nodes are moved in must not
+ * be held by another sequence as well: gdn_kv4_reserve gives a row its own before
+ * the block is appended; branch it (gdn_kv4_fork) after the commit, not between.
  */
 int gdn_kv4_commit(const gdn_kv4_cache* c, int64_t layer_stride, int32_t n_layers, int32_t N,
                    const int32_t* parent, const int32_t* accept_idx, int32_t* len_out,

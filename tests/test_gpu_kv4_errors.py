@@ -1,0 +1,62 @@
+"""Sequences of the 4-bit cache that cannot be served are left as they are: bad page
+numbers, beside sequences that are served."""
+import numpy as np
+import pytest
+
+import kv4_reference as ref
+from gpu_helpers import torch
+from test_gpu_kv4 import Setup, i32
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ commit
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("page", [-1, 1 << 20])
+def test_commit_on_a_bad_page_leaves_the_sequence(gpu_lib, which, page):
+    """One of the block's pages is not there: no layer moves, the length stays, and the
+    sequences beside it are committed."""
+    rng, t = np.random.default_rng(70 + which), torch()
+    N, P, layers = 40, 32, 2
+    s = Setup(rng, [90, 90, 131], 2, 64, P, layers=layers)
+    s.gpu()
+    parent = np.tile([-1, 0, 0] + [2] + list(range(3, N - 1)), (3, 1))   # node 1 is a leaf
+    accept = np.array([N - 1, N - 1, 7])
+    # sequence 1's block is at 50 .. 89: pages 1 and 2 of its row; which = 0: a page before
+    # the block, which the call has no business with
+    s.g_table[1, which] = page
+    out = i32([-7, -7, -7])
+    before = s.g_pages.clone()
+    gpu_lib.gdn_kv4_commit(s.g_pages, s.g_table, s.g_len, i32(accept), out, N=N,
+                           parent=i32(parent), status=s.status)
+    want = ref.commit([ref.Cache(s.pages[l], 64) for l in range(layers)], s.table, s.lens, P, N,
+                      accept, parent)
+    assert int(s.status.item()) == (gpu_lib.GDN_ERR_PAGE_RANGE if which else 0)
+    if which:
+        want[1] = 90
+    assert out.tolist() == want.tolist()
+    own = s.table[1][s.table[1] >= 0]
+    if which:
+        assert t.equal(s.g_pages[:, own], before[:, own])
+    got = s.g_pages.cpu().numpy()
+    for l in range(layers):
+        a, b_ = ref.Cache(got[l], 64), ref.Cache(s.pages[l], 64)
+        for b in (0, 2) if which else (0, 1, 2):
+            for p in range(int(want[b])):
+                for h in range(2):
+                    for x, y in zip(a.get(s.table[b, p // P], h, p % P),
+                                    b_.get(s.table[b, p // P], h, p % P)):
+                        assert np.array_equal(x, y)
+
+
+def test_commit_with_nothing_to_move_does_not_look_at_the_pages(gpu_lib):
+    """A chain, and a tree's path that is in place, are committed by their length alone."""
+    rng = np.random.default_rng(75)
+    s = Setup(rng, [40], 1, 64, 32)
+    s.gpu()
+    s.g_table[0] = -1
+    for parent in (None, i32([[-1, 0, 1, 2]])):
+        out = i32([0])
+        gpu_lib.gdn_kv4_commit(s.g_pages, s.g_table, s.g_len, i32([2]), out, N=4, parent=parent,
+                               status=s.status)
+        assert out.tolist() == [39] and int(s.status.item()) == 0
