@@ -64,12 +64,17 @@ fork_kernel(gdn_kv4_pool p, const int32_t* src, const int32_t* dst) {
   const int32_t* s = p.table + (int64_t)from * p.table_stride;
   int32_t* d = p.table + (int64_t)to * p.table_stride;
   const int len = p.kv_len[from], held = pages_of(p, len);
+  // a row is branched whole or not at all: its pages are looked at before any is counted
+  bool bad = false;
+  for (int j = threadIdx.x; j < held; j += kThreads)
+    bad |= !page_ok(p, j < kThreads ? ahead : s[j]);
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) report(p.status, GDN_ERR_PAGE_RANGE);
+    return;
+  }
   for (int j = threadIdx.x; j < p.max_pages; j += kThreads) {
     const int page = j >= held ? -1 : j < kThreads ? ahead : s[j];
-    if (j < held) {
-      if (page_ok(p, page)) atomicAdd(p.ref + page, 1);
-      else report(p.status, GDN_ERR_PAGE_RANGE);
-    }
+    if (j < held) atomicAdd(p.ref + page, 1);
     d[j] = page;
   }
   __syncthreads();

@@ -5,7 +5,7 @@ import pytest
 
 import kv4_reference as ref
 from gpu_helpers import torch
-from test_gpu_kv4 import Setup, i32
+from test_gpu_kv4 import Setup, i32, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,37 @@ def test_commit_with_nothing_to_move_does_not_look_at_the_pages(gpu_lib):
         gpu_lib.gdn_kv4_commit(s.g_pages, s.g_table, s.g_len, i32([2]), out, N=4, parent=parent,
                                status=s.status)
         assert out.tolist() == [39] and int(s.status.item()) == 0
+
+
+# ------------------------------------------------------------------ pool
+def pool_of(widths, P=32, width=200, rows=8):
+    """Rows of `widths` pages each, their last page partly filled, then empty rows."""
+    table, kv_len = np.full((rows, width), -1, np.int64), np.zeros(rows, np.int64)
+    at = 0
+    for r, w in enumerate(widths):
+        table[r, :w] = np.arange(at, at + w)
+        kv_len[r] = w * P - 5
+        at += w
+    count = np.zeros(at + 40, np.int64)
+    count[:at] = 1
+    return ref.Pool(table, kv_len, count, P)
+
+
+BAD = [(3, -1), (3, 1 << 20), (0, -5), (150, -1), (180, 1 << 20)]   # entry, page number
+
+
+@pytest.mark.parametrize("entry, page", BAD)
+def test_fork_of_a_row_with_a_bad_page_leaves_everything(gpu_lib, entry, page):
+    t = torch()
+    pool = pool_of([190, 5])
+    g = [i32(pool.table), i32(pool.kv_len), i32(pool.ref)]
+    g[0][0, entry] = page
+    row0 = g[0][0].clone()
+    pool.fork([1], [5])
+    status = status_word()
+    gpu_lib.gdn_kv4_fork(*g, i32([0, 1]), i32([4, 5]), page_tokens=32, status=status)
+    assert int(status.item()) == gpu_lib.GDN_ERR_PAGE_RANGE
+    assert t.equal(g[0][0], row0)
+    assert np.array_equal(g[0][1:].cpu().numpy(), pool.table[1:])
+    assert np.array_equal(g[1].cpu().numpy(), pool.kv_len)
+    assert np.array_equal(g[2].cpu().numpy(), pool.ref)
