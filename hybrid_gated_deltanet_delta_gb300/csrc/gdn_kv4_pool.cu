@@ -38,10 +38,16 @@ release_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* keep_len) {
   const int len = p.kv_len[row];
   if (keep >= len) return;
   int32_t* t = p.table + (int64_t)row * p.table_stride;
+  // all of the pages that are given up are looked at before any is
+  bool bad = false;
+  for (int j = pages_of(p, keep) + threadIdx.x; j < pages_of(p, len); j += kThreads)
+    bad |= !page_ok(p, t[j]);
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) report(p.status, GDN_ERR_PAGE_RANGE);
+    return;
+  }
   for (int j = pages_of(p, keep) + threadIdx.x; j < pages_of(p, len); j += kThreads) {
-    const int page = t[j];
-    if (page_ok(p, page)) atomicSub(p.ref + page, 1);
-    else report(p.status, GDN_ERR_PAGE_RANGE);
+    atomicSub(p.ref + t[j], 1);
     t[j] = -1;
   }
   __syncthreads();

@@ -94,3 +94,34 @@ def test_fork_of_a_row_with_a_bad_page_leaves_everything(gpu_lib, entry, page):
     assert np.array_equal(g[0][1:].cpu().numpy(), pool.table[1:])
     assert np.array_equal(g[1].cpu().numpy(), pool.kv_len)
     assert np.array_equal(g[2].cpu().numpy(), pool.ref)
+
+
+@pytest.mark.parametrize("entry, page", BAD)
+def test_release_of_a_row_with_a_bad_page_leaves_everything(gpu_lib, entry, page):
+    t = torch()
+    pool = pool_of([190, 5])
+    g = [i32(pool.table), i32(pool.kv_len), i32(pool.ref)]
+    g[0][0, entry] = page
+    row0 = g[0][0].clone()
+    pool.release([1], [40])
+    status = status_word()
+    gpu_lib.gdn_kv4_release(*g, i32([0, 1]), i32([0, 40]), page_tokens=32, status=status)
+    assert int(status.item()) == gpu_lib.GDN_ERR_PAGE_RANGE
+    assert t.equal(g[0][0], row0)
+    assert np.array_equal(g[0][1:].cpu().numpy(), pool.table[1:])
+    assert np.array_equal(g[1].cpu().numpy(), pool.kv_len)
+    assert np.array_equal(g[2].cpu().numpy(), pool.ref)
+
+
+def test_release_past_a_bad_page_is_served(gpu_lib):
+    """Only the pages that are given up have to be there."""
+    pool = pool_of([190])
+    g = [i32(pool.table), i32(pool.kv_len), i32(pool.ref)]
+    g[0][0, 3] = -1
+    pool.table[0, 3] = -1
+    pool.release([0], [200])
+    status = status_word()
+    gpu_lib.gdn_kv4_release(*g, i32([0]), i32([200]), page_tokens=32, status=status)
+    assert int(status.item()) == 0
+    for got, want in zip(g, (pool.table, pool.kv_len, pool.ref)):
+        assert np.array_equal(got.cpu().numpy(), want)
