@@ -121,6 +121,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
 
 struct Need {
   bool ok, copy;
+  int err;                                  // why not ok
   int row, old_len, new_len, lowest, want;  // entries lowest .. want-1 are new
   int from;                                 // the shared last page, to be copied
 };
@@ -128,6 +129,7 @@ struct Need {
 __device__ __forceinline__ Need need_of(const gdn_kv4_pool& p, const int32_t* rows,
                                         const int32_t* new_len, int f) {
   Need n = {};
+  n.err = GDN_ERR_ROW_RANGE;
   n.row = rows[f];
   n.new_len = new_len[f];
   n.ok = row_ok(p, n.row) && (int64_t)n.new_len <= (int64_t)p.max_pages * p.page_tokens;
@@ -141,6 +143,7 @@ __device__ __forceinline__ Need need_of(const gdn_kv4_pool& p, const int32_t* ro
     const int tail = p.table[(int64_t)n.row * p.table_stride + n.lowest - 1];
     if (!page_ok(p, tail)) {
       n.ok = false;
+      n.err = GDN_ERR_PAGE_RANGE;
     } else if (p.ref[tail] > 1) {
       n.copy = true;
       n.from = tail;
@@ -210,7 +213,7 @@ plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, 
   // shared memory (row tid: `own`), the others in the plan
   auto look = [&](int f) {
     const Need n = need_of(p, rows, new_len, f);
-    if (!n.ok) report(p.status, GDN_ERR_ROW_RANGE);
+    if (!n.ok) report(p.status, n.err);
     return n;
   };
   auto records = [&](const Need& n) {

@@ -530,7 +530,11 @@ int gdn_kv4_commit(const gdn_kv4_cache* c, int64_t layer_stride, int32_t n_layer
  * is device memory that the three calls below read and update on the stream, so
  * a captured step can branch and free sequences without the host.  The rows
  * named by one call must be distinct (fork: the dst rows; a dst row is not a
- * src row).  A row that cannot be served is left as it is and reported.
+ * src row).  A row that cannot be served is left as it is and reported:
+ * GDN_ERR_ROW_RANGE for a row, length or branch that is out of range, and
+ * GDN_ERR_PAGE_RANGE for a page number outside [0, n_pages) among the pages that
+ * the call has to look at (fork: all of the source's; release: those given up;
+ * reserve: a partly filled last one).
  */
 typedef struct gdn_kv4_pool {
   int32_t* table;  /* [n_rows] rows of max_pages entries, table_stride entries apart */

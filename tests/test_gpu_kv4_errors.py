@@ -125,3 +125,22 @@ def test_release_past_a_bad_page_is_served(gpu_lib):
     assert int(status.item()) == 0
     for got, want in zip(g, (pool.table, pool.kv_len, pool.ref)):
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("page", [-1, 1 << 20])
+def test_reserve_on_a_bad_last_page_leaves_the_row(gpu_lib, page):
+    t = torch()
+    pool = pool_of([4, 5])
+    g = [i32(pool.table), i32(pool.kv_len), i32(pool.ref)]
+    g[0][0, 3] = page
+    row0 = g[0][0].clone()
+    assert pool.reserve([1], [170]) == []
+    pages = t.zeros(len(pool.ref), 1, 1, 36 * 64, dtype=t.uint8, device="cuda")
+    ws = t.empty(gpu_lib.gdn_kv4_reserve_workspace_bytes(2), dtype=t.uint8, device="cuda")
+    status = status_word()
+    gpu_lib.gdn_kv4_reserve(pages, *g, i32([0, 1]), i32([130, 170]), ws, status=status)
+    assert int(status.item()) == gpu_lib.GDN_ERR_PAGE_RANGE
+    assert t.equal(g[0][0], row0)
+    assert np.array_equal(g[0][1:].cpu().numpy(), pool.table[1:])
+    assert np.array_equal(g[1].cpu().numpy(), pool.kv_len)
+    assert np.array_equal(g[2].cpu().numpy(), pool.ref)
