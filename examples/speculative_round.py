@@ -5,14 +5,17 @@ commit its accepted path:
 
   recurrent layer   gdn_verify_tree over the block, every node's state persisted;
                     gdn_commit_accepted puts the accepted node's state in the cache
-  attention layer   gdn_kv4_reserve makes room, gdn_kv4_append quantises the
-                    block's keys and values into the 4-bit cache,
+  attention layer   gdn_kv4_reserve makes room and says for which sequences it
+                    could, gdn_kv4_append quantises the block's keys and values
+                    into the 4-bit cache,
                     gdn_kv4_attention attends under the ancestor mask;
                     gdn_kv4_commit moves the accepted path together and
                     gdn_kv4_release gives the pages past it back
 
 The projections around the mixers are random tensors here.  Nothing in a round
-waits for the host: lengths, tables and page counts are device memory.
+waits for the host: lengths, tables and page counts are device memory.  A sequence
+that finds no page sits the round out: its granted length is -1, so no call touches
+its tokens, and no node of it is accepted in any layer.
 
     python examples/speculative_round.py
 """
@@ -51,6 +54,7 @@ class Mixers:
         self.rows = torch.arange(B, **i32)
         self.status = torch.zeros(1, **i32)
         self.committed = torch.zeros(B, **i32)
+        self.block = torch.zeros(B, **i32)         # tokens with the block; -1: no page for it
         self.reserve_ws = torch.empty(gdn.gdn_kv4_reserve_workspace_bytes(B), dtype=torch.uint8,
                                       **new)
 
@@ -60,8 +64,8 @@ class Mixers:
     def _append(self, k, v, grown):
         """Room for the block, then its keys and values at its end."""
         gdn.gdn_kv4_reserve(self.pages, self.table, self.length, self.ref, self.rows, grown,
-                            self.reserve_ws, status=self.status)
-        gdn.gdn_kv4_append(k, v, self.pages, self.table, self.length, status=self.status)
+                            self.reserve_ws, granted=self.block, status=self.status)
+        gdn.gdn_kv4_append(k, v, self.pages, self.table, self.block, status=self.status)
 
     def prompt(self, tokens):
         """A prompt of the same number of tokens for every sequence (attention layer)."""
@@ -77,7 +81,7 @@ class Mixers:
         ws = torch.empty(gdn.gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D),
                          dtype=torch.uint8, device="cuda")
         o = torch.empty(q.shape, dtype=q.dtype, device="cuda")
-        gdn.gdn_kv4_attention(q, self.pages, self.table, self.length, o, ws, scale=D ** -0.5,
+        gdn.gdn_kv4_attention(q, self.pages, self.table, self.block, o, ws, scale=D ** -0.5,
                               parent=parent, status=self.status)
         return o
 
@@ -98,10 +102,11 @@ class Mixers:
     def commit(self, parent, accept):
         """Commit the path to accept[b] of every sequence's tree, in every layer."""
         _, Hv, d = self.shape[:3]
+        accept = torch.where(self.block < 0, -1, accept)
         for state, (snap, _) in zip(self.state, self.blocks):
             gdn.gdn_commit_accepted(snap, accept, state, B=self.B, N=self.N, Hv=Hv, dk=d, dv=d,
                                     status=self.status)
-        gdn.gdn_kv4_commit(self.pages, self.table, self.length, accept, self.committed, N=self.N,
+        gdn.gdn_kv4_commit(self.pages, self.table, self.block, accept, self.committed, N=self.N,
                            parent=parent, status=self.status)
         gdn.gdn_kv4_release(self.table, self.length, self.ref, self.rows, self.committed,
                             page_tokens=self.page_tokens, status=self.status)

@@ -14,7 +14,7 @@ Entry points (same names as the C ABI):
   gdn_prefill_chunked, gdn_prefill_workspace_bytes, gdn_prefill_chunked_noalloc
   the 4-bit key/value cache of the full-attention layers: gdn_kv4_append,
   gdn_kv4_read, gdn_kv4_attention, gdn_kv4_commit, and its page pool:
-  gdn_kv4_release, gdn_kv4_fork, gdn_kv4_reserve
+  gdn_kv4_release, gdn_kv4_fork, gdn_kv4_reserve (gdn_kv4_reserve_granted)
 and, for serving loops that issue the same call every step, bound calls
 (bind_verify_chain, bind_verify_tree, bind_commit_accepted,
 bind_replay_accepted, bind_prefill_chunked, bind_kv4_*): the arguments are marshalled once
@@ -160,6 +160,8 @@ def load(path: str | None = None):
     lib.gdn_kv4_reserve_workspace_bytes.restype = sz
     lib.gdn_kv4_reserve.argtypes = [L, P, i64, i64, i32, i32, i32, P, P, i32, P, sz, P]
     lib.gdn_kv4_reserve.restype = ctypes.c_int
+    lib.gdn_kv4_reserve_granted.argtypes = [L, P, i64, i64, i32, i32, i32, P, P, i32, P, P, sz, P]
+    lib.gdn_kv4_reserve_granted.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.argtypes = []
@@ -734,23 +736,32 @@ def gdn_kv4_reserve_workspace_bytes(F) -> int:
     return int(load().gdn_kv4_reserve_workspace_bytes(F))
 
 
-def bind_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, *, status=None,
-                     stream=None):
-    """gdn_kv4_reserve bound to these buffers."""
+def bind_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, *, granted=None,
+                     status=None, stream=None):
+    """gdn_kv4_reserve (or, with granted, gdn_kv4_reserve_granted) bound to these buffers."""
     layers, n_pages, Hkv, page_tokens, D, page_stride, layer_stride = _kv4_pages(pages)
     p = _kv4_pool(table, kv_len, ref, page_tokens, status)
     _need(p.n_pages == n_pages, "ref must have one entry per page")
     _i32(rows, (rows.numel(),), "rows")
     _i32(new_len, (rows.numel(),), "new_len")
-    return BoundCall(load().gdn_kv4_reserve, "gdn_kv4_reserve",
+    _i32(granted, (rows.numel(),), "granted")
+    fn, name, more = load().gdn_kv4_reserve, "gdn_kv4_reserve", ()
+    if granted is not None:
+        fn, name, more = load().gdn_kv4_reserve_granted, "gdn_kv4_reserve_granted", (_ptr(granted),)
+    return BoundCall(fn, name,
                      (ctypes.byref(p), _ptr(pages), page_stride, layer_stride, layers, Hkv, D,
-                      _ptr(rows), _ptr(new_len), rows.numel(), _ptr(workspace),
+                      _ptr(rows), _ptr(new_len), rows.numel(), *more, _ptr(workspace),
                       workspace.numel() * workspace.element_size(), _stream(stream)),
-                     (p, pages, table, kv_len, ref, rows, new_len, workspace, status))
+                     (p, pages, table, kv_len, ref, rows, new_len, workspace, granted, status))
 
 
 def gdn_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, **kw):
     """Grow rows[i] to new_len[i] tokens with the lowest-numbered free pages; a
     partly filled last page that has other holders is copied first, in every
-    layer of pages.  workspace: gdn_kv4_reserve_workspace_bytes(len(rows))."""
+    layer of pages.  workspace: gdn_kv4_reserve_workspace_bytes(len(rows)).
+
+    granted, an optional int32 [len(rows)], gets new_len[i] for a row that was
+    served and -1 for one that was not.  Given as kv_len of append, attention and
+    commit it keeps a row that found no page, and those that share its pages, as
+    they are (see include/gdn.h)."""
     bind_kv4_reserve(pages, table, kv_len, ref, rows, new_len, workspace, **kw)()

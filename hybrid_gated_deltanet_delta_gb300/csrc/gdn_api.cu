@@ -214,6 +214,33 @@ int kv4_pool_checks(const gdn_kv4_pool* p, const int32_t* a, const int32_t* b, i
   return GDN_OK;
 }
 
+int kv4_reserve_common(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
+                       int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
+                       const int32_t* rows, const int32_t* new_len, int32_t F, int32_t* granted,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = kv4_pool_checks(p, rows, new_len, F);
+  if (st != GDN_OK) return st;
+  if (Hkv < 1 || n_layers < 1) return GDN_ERR_INVALID_ARG;
+  if (!kv4_head_size(D) || n_layers > 65535 || Hkv > 65535) return GDN_ERR_UNSUPPORTED;
+  // the plan adds up in 32 bits what all rows ask for, max_pages each at most
+  if ((int64_t)F * p->max_pages > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+  const int64_t head = (int64_t)(p->page_tokens / 32) * 36 * D;
+  if (page_stride < head * Hkv) return GDN_ERR_INVALID_ARG;
+  if (n_layers > 1 && layer_stride < (int64_t)p->n_pages * page_stride)
+    return GDN_ERR_INVALID_ARG;
+  // the copy's and the plan's indices go on in steps of 4096 past the last one, in 32 bits
+  if (head * Hkv / 16 > 0x7ffff000 || p->n_pages > 0x7ffff000) return GDN_ERR_UNSUPPORTED;
+  if (page_stride % 16 != 0 || layer_stride % 16 != 0) return GDN_ERR_MISALIGNED;
+  if (F == 0) return GDN_OK;
+  if (pages == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(pages) || !gdn::aligned16(workspace) || !ok_ptr4(granted))
+    return GDN_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < gdn::kv4_reserve_workspace_bytes(F))
+    return GDN_ERR_WORKSPACE;
+  return gdn::launch_kv4_reserve(*p, pages, page_stride, layer_stride, n_layers, Hkv, D, rows,
+                                 new_len, F, granted, workspace, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -460,26 +487,19 @@ int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
                     const int32_t* rows, const int32_t* new_len, int32_t F, void* workspace,
                     size_t workspace_bytes, void* stream) {
   GDN_RANGE();
-  const int st = kv4_pool_checks(p, rows, new_len, F);
-  if (st != GDN_OK) return st;
-  if (Hkv < 1 || n_layers < 1) return GDN_ERR_INVALID_ARG;
-  if (!kv4_head_size(D) || n_layers > 65535 || Hkv > 65535) return GDN_ERR_UNSUPPORTED;
-  // the plan adds up in 32 bits what all rows ask for, max_pages each at most
-  if ((int64_t)F * p->max_pages > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
-  const int64_t head = (int64_t)(p->page_tokens / 32) * 36 * D;
-  if (page_stride < head * Hkv) return GDN_ERR_INVALID_ARG;
-  if (n_layers > 1 && layer_stride < (int64_t)p->n_pages * page_stride)
-    return GDN_ERR_INVALID_ARG;
-  // the copy's and the plan's indices go on in steps of 4096 past the last one, in 32 bits
-  if (head * Hkv / 16 > 0x7ffff000 || p->n_pages > 0x7ffff000) return GDN_ERR_UNSUPPORTED;
-  if (page_stride % 16 != 0 || layer_stride % 16 != 0) return GDN_ERR_MISALIGNED;
-  if (F == 0) return GDN_OK;
-  if (pages == nullptr) return GDN_ERR_INVALID_ARG;
-  if (!gdn::aligned16(pages) || !gdn::aligned16(workspace)) return GDN_ERR_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < gdn::kv4_reserve_workspace_bytes(F))
-    return GDN_ERR_WORKSPACE;
-  return gdn::launch_kv4_reserve(*p, pages, page_stride, layer_stride, n_layers, Hkv, D, rows,
-                                 new_len, F, workspace, static_cast<cudaStream_t>(stream));
+  return kv4_reserve_common(p, pages, page_stride, layer_stride, n_layers, Hkv, D, rows, new_len,
+                            F, nullptr, workspace, workspace_bytes, stream);
+}
+
+int gdn_kv4_reserve_granted(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
+                            int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
+                            const int32_t* rows, const int32_t* new_len, int32_t F,
+                            int32_t* granted, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  GDN_RANGE();
+  if (F > 0 && granted == nullptr) return GDN_ERR_INVALID_ARG;
+  return kv4_reserve_common(p, pages, page_stride, layer_stride, n_layers, Hkv, D, rows, new_len,
+                            F, granted, workspace, workspace_bytes, stream);
 }
 
 const char* gdn_status_string(int status) {

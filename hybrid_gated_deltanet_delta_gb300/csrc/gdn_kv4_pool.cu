@@ -201,7 +201,8 @@ struct PlanRow {
 // page a thread and the rows' plan in global memory, 13.6 us with each thread handing
 // out its own eight pages, 10.9 us this way; 32 sequences 37.2, 41.0 and 36.0 us.
 __global__ void __launch_bounds__(kPlan, 1)
-plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, Copy* plan) {
+plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, Copy* plan,
+            int32_t* granted) {
   __shared__ int warp_sum[32];
   __shared__ PlanRow kept[kPlan];              // of the first kPlan rows
   __shared__ uint16_t by_rank[kPlan * kScan];  // free pages of a chunk
@@ -290,6 +291,10 @@ plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, 
     rank0 += total;
     __syncthreads();
   }
+  // (a row that was not served gets a length that every later call skips)
+  auto grant = [&](int f, int n) {
+    if (granted != nullptr) granted[f] = n;
+  };
   for (int f = tid; f < F; f += kPlan) {
     if (f < kPlan) {
       const int recs = records(own);
@@ -297,14 +302,17 @@ plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, 
       plan[f].records = recs < 0 ? 0 : recs;
       if (recs > 0) atomicSub(p.ref + own.from, 1);
       if (recs >= 0) p.kv_len[own.row] = own.new_len;
+      grant(f, recs >= 0 ? own.new_len : -1);
       continue;
     }
     if (plan[f].records < 0) {
       plan[f].records = 0;
+      grant(f, -1);
       continue;
     }
     if (plan[f].records > 0) atomicSub(p.ref + plan[f].from, 1);
     p.kv_len[rows[f]] = new_len[f];
+    grant(f, new_len[f]);
   }
 }
 
@@ -355,9 +363,11 @@ size_t kv4_reserve_workspace_bytes(int F) { return (size_t)F * sizeof(Copy); }
 
 int launch_kv4_reserve(const gdn_kv4_pool& p, void* pages, int64_t page_stride,
                        int64_t layer_stride, int n_layers, int Hkv, int D, const int32_t* rows,
-                       const int32_t* new_len, int F, void* workspace, cudaStream_t s) {
+                       const int32_t* new_len, int F, int32_t* granted, void* workspace,
+                       cudaStream_t s) {
   Copy* plan = static_cast<Copy*>(workspace);
-  const int rc = launch_pdl(plan_kernel, dim3(1), dim3(kPlan), 0, s, p, rows, new_len, F, plan);
+  const int rc =
+      launch_pdl(plan_kernel, dim3(1), dim3(kPlan), 0, s, p, rows, new_len, F, plan, granted);
   if (rc != GDN_OK || n_layers == 0) return rc;
   return launch_pdl(copy_kernel, dim3(8, F, n_layers), dim3(kThreads), 0, s, (const Copy*)plan,
                     static_cast<uint8_t*>(pages), page_stride, layer_stride, Hkv,

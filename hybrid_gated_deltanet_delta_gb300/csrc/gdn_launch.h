@@ -72,6 +72,7 @@ int launch_kv4_fork(const gdn_kv4_pool& p, const int32_t* src, const int32_t* ds
 size_t kv4_reserve_workspace_bytes(int F);
 int launch_kv4_reserve(const gdn_kv4_pool& p, void* pages, int64_t page_stride,
                        int64_t layer_stride, int n_layers, int Hkv, int D, const int32_t* rows,
-                       const int32_t* new_len, int F, void* workspace, cudaStream_t s);
+                       const int32_t* new_len, int F, int32_t* granted, void* workspace,
+                       cudaStream_t s);
 
 }  // namespace gdn

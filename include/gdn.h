@@ -565,7 +565,8 @@ int gdn_kv4_fork(const gdn_kv4_pool* p, const int32_t* src, const int32_t* dst, 
  * n_layers layers (copy-on-write), and the old page loses a holder.  A row that
  * does not fit, and every row after it that needs pages, is left as it is:
  * GDN_ERR_POOL_EMPTY.  Afterwards positions below new_len[i] from the old
- * length on may be appended to.  GDN_ERR_UNSUPPORTED when F * max_pages would
+ * length on may be appended to, in the rows that were served (where some may not
+ * be, gdn_kv4_reserve_granted says which).  GDN_ERR_UNSUPPORTED when F * max_pages would
  * not fit 31 bits (the pages that the rows ask for are added up).
  */
 size_t gdn_kv4_reserve_workspace_bytes(int32_t F);
@@ -574,6 +575,25 @@ int gdn_kv4_reserve(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
                     int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
                     const int32_t* rows, const int32_t* new_len, int32_t F, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_kv4_reserve that also says which rows were served: granted[i] = new_len[i]
+ * for those, -1 for the others.
+ *
+ * A row that was refused keeps its length, and its last page may have other
+ * holders; a block appended at that length would overwrite the row's last N
+ * tokens, theirs too.  A step that goes on without the host therefore takes the
+ * block's lengths from `granted`: given as kv_len of gdn_kv4_append, _attention and
+ * _commit (with the table's rows in the order of rows[]), a -1 is skipped and
+ * reported by each (GDN_ERR_ROW_RANGE, after GDN_ERR_POOL_EMPTY in a status word that
+ * they share): nothing is written, the output is 0, len_out is -1.  That -1 as
+ * keep_len of gdn_kv4_release leaves the row as it is.
+ */
+int gdn_kv4_reserve_granted(const gdn_kv4_pool* p, void* pages, int64_t page_stride,
+                            int64_t layer_stride, int32_t n_layers, int32_t Hkv, int32_t D,
+                            const int32_t* rows, const int32_t* new_len, int32_t F,
+                            int32_t* granted, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* Human-readable name of a gdn_status value (static string, never NULL). */
 const char* gdn_status_string(int status);

@@ -3,6 +3,7 @@ before anything is launched, and answered by the size functions without a fault.
 import ctypes
 
 import pytest
+import torch
 
 import hybrid_gated_deltanet_delta_gb300 as gdn
 from hybrid_gated_deltanet_delta_gb300 import build as gdn_build
@@ -57,3 +58,26 @@ def test_attention_workspace_of_sizes_that_are_refused_is_0(lib, N, Hq):
 
 def test_attention_workspace_of_the_largest_call(lib):
     assert lib.gdn_kv4_attention_workspace_bytes(1, 1 << 24, 64, 1, 256) > 0
+
+
+def test_reserve_granted_checks(lib):
+    p = gdn.Kv4Pool()
+    for key, val in dict(table=0x10000, kv_len=0x20000, ref=0x30000, table_stride=8, n_rows=4,
+                         max_pages=8, n_pages=100, page_tokens=64).items():
+        setattr(p, key, val)
+    for granted, F, want in ((0, 2, gdn.GDN_ERR_INVALID_ARG), (0x502, 2, gdn.GDN_ERR_MISALIGNED),
+                             (0, 0, gdn.GDN_OK), (0x500, -1, gdn.GDN_ERR_INVALID_ARG),
+                             (0x500, 1 << 17, gdn.GDN_ERR_UNSUPPORTED)):
+        assert lib.gdn_kv4_reserve_granted(ctypes.byref(p), V(0x1000), 4 * 2 * 36 * 256, 0, 1, 4,
+                                           256, V(0x100), V(0x200), F, V(granted), V(0x3000),
+                                           1 << 20, None) == want
+
+
+def test_binding_refuses_a_bad_granted(lib):
+    i32 = torch.int32
+    pages = torch.zeros(4, 2, 2, 36 * 64, dtype=torch.uint8)
+    table, one = torch.zeros(1, 2, dtype=i32), torch.zeros(1, dtype=i32)
+    for bad in (torch.zeros(2, dtype=i32), torch.zeros(1), torch.zeros(1, dtype=torch.int64)):
+        with pytest.raises(ValueError):
+            gdn.gdn_kv4_reserve(pages, table, one, torch.zeros(4, dtype=i32), one, one, pages,
+                                granted=bad)
