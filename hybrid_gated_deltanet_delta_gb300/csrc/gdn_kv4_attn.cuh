@@ -31,12 +31,15 @@
 //               come from one thread: across threads they have no order)
 //   1 or 2 that cut the run into segments and copy the records
 //
-// The reference m is moved only when some p would pass 2^8 (p is at most 65504
-// in binary16): the sums and O^T are then multiplied by 2^(old - new), which
-// happens on an item's first tile and seldom later, so the usual tile takes
-// one FMA, one maximum, one exp2 and one addition per logit and no reduction
-// across lanes.  p is rounded to binary16 for the product (2^-11; bf16 would
-// give 2^-8); code * scale needs 6 significand bits, so K and V are exact.
+// The reference m is set 7 under a row's largest logit (so that p = 2^7 there) and
+// moved only when some p would pass 2^15 (binary16 ends at 65504): the sums and O^T are
+// then multiplied by 2^(old - new), which happens on an item's first tile and seldom
+// later, so the usual tile takes one FMA, one maximum, one exp2 and one addition per
+// logit and no reduction across lanes.  p is rounded to binary16 for the product: 2^-11
+// relative (bf16 would give 2^-8) from 2^-21 of the row's largest p on, and to multiples of
+// 2^-31 of it below (their sum l is taken before, in fp32); with m at the largest logit
+// itself these were 2^-14 and 2^-24, and a flat tail 17 nats under one large logit was lost.
+// code * scale needs 6 significand bits, so K and V are exact.
 //
 // What bounds it.  With few rows the bytes: a tile of 36.8 KB (D = 256) takes 0.93 us a
 // block, 39.6 GB/s an SM of 43.8 measured for a copy; 131072 tokens of 4 heads take
@@ -64,7 +67,10 @@ namespace kv4 {
 
 constexpr int kTile = 128;  // positions of a tile: four records
 constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen nothing
-constexpr unsigned kMostP = 0x5c00;  // 2^8 in binary16: the largest p before m moves
+// m is set kBelow under the largest logit (log2 units), so that p starts at 2^7, and moves
+// when some p passes 2^15 in binary16.
+constexpr float kBelow = 7.f;
+constexpr unsigned kMostP = 0x7800;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaitPolls = 1 << 20;  // bound of every wait
 
@@ -971,13 +977,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
           if constexpr (C::NH == 32) tc::tmem_ready(y[1]);
         };
         // The first tile sets the references; a later one is tried with those there
-        // are, and done again in the case that some p passed 2^8.
+        // are, and done again in the case that some p passed 2^15.
         bool raise = t == e.t0;
 #pragma unroll 1
         for (;;) {
           load(sa);
           if (raise) {
-            // ---- new references: the largest logits so far
+            // ---- new references: kBelow under the largest logits so far
             float x[C::NH];
 #pragma unroll
             for (int i = 0; i < C::NH; i += 4) {
@@ -999,7 +1005,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
               float m = old;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float w = sh.part[q][r];
+                const float w = sh.part[q][r] - kBelow;
                 m = w > m || w != w ? w : m;
               }
               sh.neg_m[r] = -m;
