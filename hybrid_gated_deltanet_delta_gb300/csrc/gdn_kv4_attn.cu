@@ -18,17 +18,6 @@ constexpr int kMaxRows = 96;
 
 int round_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kMaxRows; }
 
-// One block per SM: a block takes the whole of tensor memory.
-int blocks() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return sms;
-}
-
 void row_tiles(int rows, int* tiles, int* per_tile) {
   *tiles = (rows + kMaxRows - 1) / kMaxRows;
   *per_tile = (rows + *tiles - 1) / *tiles;
@@ -39,8 +28,8 @@ void row_tiles(int rows, int* tiles, int* per_tile) {
 size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   int tiles, per_tile;
   row_tiles(N * (Hq / Hkv), &tiles, &per_tile);
-  // without a device (a size asked for on the host alone) as for 256 SMs
-  const int sms = blocks();
+  // one block per SM; without a device (a size asked for on the host alone) as for 256
+  const int sms = sm_count();
   return (size_t)(sms > 0 ? sms : 256) *
          (2 * round_rows(per_tile) * (D * 4 + 8) + sizeof(kv4::AttnJoin));
 }
@@ -48,7 +37,7 @@ size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
 int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb, int64_t qsn,
                          int N, int Hq, float scale, const int32_t* parent, void* o, float* lse,
                          void* workspace, cudaStream_t s) {
-  const int parts = blocks();
+  const int parts = sm_count();  // one block per SM: a block takes the whole of tensor memory
   if (parts == 0) return GDN_ERR_CUDA;
   AttnArgs a = {};
   a.c = c;

@@ -279,8 +279,8 @@ read_kernel(gdn_kv4_cache c, void* __restrict__ kout, void* __restrict__ vout, i
 // memory, 31 us with four layers to a block and the path in shared memory, 26 us with
 // blocks that do not all fit at once, 23.5 us with one wave and a channel's nibbles
 // moved one by one, 15.7 us this way (one tree: 6.2, 9.0, 4.9, 4.6 and 3.9 us).  Of
-// waves of 456, 608, 760 and 912 blocks 608 (four an SM) took least: 16.9, 15.7, 18.0
-// and 17.2 us.
+// waves of 456, 608, 760 and 912 blocks 608 (four on each of 152 SMs) took least: 16.9,
+// 15.7, 18.0 and 17.2 us.
 constexpr int kMaxNodes = 64;
 constexpr int kWindow = 3;
 constexpr int kCommitWarps = kThreads / 32;
@@ -471,7 +471,8 @@ int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers
   // more units each (their path is found once), up to eight; a chain moves nothing:
   // one block per sequence writes its length.
   const int64_t units = (int64_t)n_layers * c.Hkv * (1 + c.D / 64);
-  const int64_t wave = 152 * 4, most = (units + kCommitWarps - 1) / kCommitWarps;
+  const int64_t wave = (int64_t)sm_count() * 4, most = (units + kCommitWarps - 1) / kCommitWarps;
+  if (wave == 0) return GDN_ERR_CUDA;
   const int64_t few = wave / c.B > (most + 7) / 8 ? wave / c.B : (most + 7) / 8;
   const dim3 grid(parent == nullptr ? 1 : (unsigned)(most < few ? most : few), c.B);
   switch (c.D) {
