@@ -368,7 +368,7 @@ int launch_kv4_reserve(const gdn_kv4_pool& p, void* pages, int64_t page_stride,
   Copy* plan = static_cast<Copy*>(workspace);
   const int rc =
       launch_pdl(plan_kernel, dim3(1), dim3(kPlan), 0, s, p, rows, new_len, F, plan, granted);
-  if (rc != GDN_OK || n_layers == 0) return rc;
+  if (rc != GDN_OK) return rc;
   return launch_pdl(copy_kernel, dim3(8, F, n_layers), dim3(kThreads), 0, s, (const Copy*)plan,
                     static_cast<uint8_t*>(pages), page_stride, layer_stride, Hkv,
                     p.page_tokens / kv4::kRec, kv4::rec_bytes(D));
