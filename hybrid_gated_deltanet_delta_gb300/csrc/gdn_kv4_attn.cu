@@ -12,8 +12,8 @@ using kv4::AttnArgs;
 // Query rows of a tile.  K and V are brought in and dequantised once per row tile, so
 // wide ones pay: with tiles of at most 64 rows a 2048-token piece of a prompt takes 431 us,
 // eight chains of 16 (96 rows) 79.8 us and a tree of 22 (132 rows, three tiles of 44)
-// 42.8 us, with 96 367, 64.0 and 40.7 us.  Rows are spread evenly over the tiles.  More
-// than 96 do not fit tensor memory beside two units of K and V (D = 256).
+// 42.8 us, with 96 367, 64.0 and 40.7 us (in turn on one box).  Rows are spread evenly over
+// the tiles.  More than 96 do not fit tensor memory beside two units of K and V (D = 256).
 constexpr int kMaxRows = 96;
 
 int round_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kMaxRows; }

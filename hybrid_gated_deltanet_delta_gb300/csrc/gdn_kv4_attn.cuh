@@ -43,10 +43,11 @@
 //
 // What bounds it.  With few rows the bytes: a tile of 36.8 KB (D = 256) takes 0.93 us a
 // block, 39.6 GB/s an SM of 43.8 measured for a copy; 131072 tokens of 4 heads take
-// 37.7 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
+// 37.9 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
 // item's output and the join.  With 96 rows the softmax warps: 1.6 us a tile, of which 0.5
 // us is the exponentials' issue at 80 registers, the tensor pipe 0.8 us; a 2048-token piece
-// of a prompt at 8192 tokens takes 365 us, 990 TFLOP/s of 1,880 measured.
+// of a prompt at 8192 tokens takes 362 to 371 us over runs, 975 to 997 TFLOP/s of 1,880
+// measured.
 // Measured and left out (us for 131072 tokens / the prompt, against the figure of the
 // time): the products issued by the K and V warps themselves, 55 / 500 against 50 / 464;
 // two streams of tiles, each with softmax warps, 58 / 693 against 50 / 464; steps of two

@@ -197,9 +197,10 @@ struct PlanRow {
 // counts, 8 consecutive pages a thread, so that a pool of 4096 pages takes one read
 // and one scan; the free pages then go to shared memory by rank and a thread serves
 // one rank, with what it needs of the row in shared memory as well.  One sequence
-// branched four ways (with the counts before it and the copy after it): 12.3 us with a
+// branched four ways (four kernels: release, fork, this one and the copy): 12.3 us with a
 // page a thread and the rows' plan in global memory, 13.6 us with each thread handing
-// out its own eight pages, 10.9 us this way; 32 sequences 37.2, 41.0 and 36.0 us.
+// out its own eight pages, 10.9 us this way; 32 sequences 37.2, 41.0 and 36.0 us.  (Now
+// 11.3 to 12.1 us over boxes and 36.6 us: release and fork look at all pages first, 0.2 us.)
 __global__ void __launch_bounds__(kPlan, 1)
 plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, Copy* plan,
             int32_t* granted) {
@@ -318,7 +319,7 @@ plan_kernel(gdn_kv4_pool p, const int32_t* rows, const int32_t* new_len, int F, 
 
 // Grid (pieces, F, layers): the records of a page that hold tokens, head by head.
 // Bound by HBM: each thread has four 16-byte loads in flight (32 sequences branched
-// four ways copy 73 MB to 73 MB, of 36 us with the kernels before it).
+// four ways copy 73 MB to 73 MB, most of 36.6 us with the three kernels before it).
 __global__ void __launch_bounds__(kThreads)
 copy_kernel(const Copy* plan, uint8_t* pages, int64_t page_stride, int64_t layer_stride, int Hkv,
             int recs, int rec_bytes) {
