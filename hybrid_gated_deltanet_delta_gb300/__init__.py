@@ -13,7 +13,8 @@ Entry points (same names as the C ABI):
   gdn_replay_accepted,
   gdn_prefill_chunked, gdn_prefill_workspace_bytes, gdn_prefill_chunked_noalloc
   the 4-bit key/value cache of the full-attention layers: gdn_kv4_append,
-  gdn_kv4_read, gdn_kv4_attention, gdn_kv4_commit, and its page pool:
+  gdn_kv4_append_rotary, gdn_kv4_read, gdn_kv4_attention, gdn_kv4_attention_window,
+  gdn_kv4_attention_shared, gdn_kv4_commit, and its page pool:
   gdn_kv4_release, gdn_kv4_fork, gdn_kv4_reserve (gdn_kv4_reserve_granted)
 and, for serving loops that issue the same call every step, bound calls
 (bind_verify_chain, bind_verify_tree, bind_commit_accepted,
@@ -43,6 +44,7 @@ GDN_ERR_PAGE_RANGE = -11
 GDN_ERR_POOL_EMPTY = -12
 GDN_ERR_ROW_RANGE = -13
 GDN_ERR_NONFINITE = -14
+GDN_ERR_POSITION_RANGE = -15
 PREFILL_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 GDN_F32 = 0
@@ -82,6 +84,16 @@ class Kv4Cache(ctypes.Structure):
         ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
         ("max_pages", ctypes.c_int32), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32),
         ("D", ctypes.c_int32),
+    ]
+
+
+class Rotary(ctypes.Structure):
+    """Mirror of gdn_rotary."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+        ("pos_stride_axis", ctypes.c_int64), ("pos_stride_b", ctypes.c_int64),
+        ("n_positions", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("pairs", ctypes.c_int32),
+        ("adjacent", ctypes.c_int32),
     ]
 
 
@@ -150,6 +162,17 @@ def load(path: str | None = None):
     lib.gdn_kv4_attention.argtypes = [C, P, i32, i64, i64, i32, i32, ctypes.c_float, P, P, P, P,
                                       sz, P]
     lib.gdn_kv4_attention.restype = ctypes.c_int
+    lib.gdn_kv4_append_rotary.argtypes = [C, ctypes.POINTER(Rotary), P, i64, i64, i32, P, i64, i64,
+                                          P, P, i32, i64, i64, i64, i64, i32, P]
+    lib.gdn_kv4_append_rotary.restype = ctypes.c_int
+    lib.gdn_kv4_attention_window.argtypes = [C, P, i32, i64, i64, i32, i32, ctypes.c_float, i32,
+                                             i32, P, P, P, P, sz, P]
+    lib.gdn_kv4_attention_window.restype = ctypes.c_int
+    lib.gdn_kv4_attention_shared_workspace_bytes.argtypes = [i32] * 6
+    lib.gdn_kv4_attention_shared_workspace_bytes.restype = sz
+    lib.gdn_kv4_attention_shared.argtypes = [C, P, i32, i64, i64, i32, i32, ctypes.c_float, P, P,
+                                             i32, P, P, P, sz, P]
+    lib.gdn_kv4_attention_shared.restype = ctypes.c_int
     lib.gdn_kv4_commit.argtypes = [C, i64, i32, i32, P, P, P, P]
     lib.gdn_kv4_commit.restype = ctypes.c_int
     lib.gdn_kv4_release.argtypes = [L, P, P, i32, P]
@@ -607,6 +630,65 @@ def gdn_kv4_append(k, v, pages, table, kv_len, **kw):
     bind_kv4_append(k, v, pages, table, kv_len, **kw)()
 
 
+def _on_device(*tensors):
+    """All of them on the current CUDA device (a pointer to another one's, or to the host's, would
+    fault in the kernel)."""
+    import torch
+
+    for t in tensors:
+        _need(t is None or (t.is_cuda and t.device.index == torch.cuda.current_device()),
+              "every tensor must be on the current CUDA device")
+
+
+def bind_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, *, axis=None,
+                           adjacent=False, k_scale=None, v_scale=None, status=None, stream=None):
+    """gdn_kv4_append_rotary bound to these buffers."""
+    import torch
+
+    _need(pages.dim() == 4, "append takes one layer's pages")
+    c = _kv4_cache(pages, table, kv_len, k_scale, v_scale, status)
+    qs, ks, vs, out = (_rows(t, c, n) for t, n in ((q, "q"), (k, "k"), (v, "v"),
+                                                   (q_out, "q_out")))
+    B, N, Hq, _ = q.shape
+    _need(tuple(k.shape) == tuple(v.shape) == (B, N, c.Hkv, c.D) and q_out.shape == q.shape,
+          "q and q_out must share a shape [B,N,Hq,D], k and v a shape [B,N,Hkv,D]")
+    _need(q.dtype == k.dtype == v.dtype == q_out.dtype, "q, k, v and q_out must share a dtype")
+    _need(cos_sin.dtype == torch.float32 and cos_sin.dim() == 3 and cos_sin.shape[1] == 2 and
+          cos_sin.is_contiguous(), "cos_sin must be contiguous float32 [n_positions,2,pairs]")
+    _need(positions.dtype == torch.int32 and positions.dim() == 3 and
+          tuple(positions.shape[1:]) == (B, N) and (N == 1 or positions.stride(2) == 1),
+          "positions must be int32 [axes,B,N] with contiguous nodes")
+    pairs = cos_sin.shape[2]
+    _need(axis is None or (axis.dtype == torch.uint8 and axis.is_contiguous() and
+                           tuple(axis.shape) == (pairs,)), "axis must be contiguous uint8 [pairs]")
+    _need(q_out.data_ptr() != q.data_ptr() or q_out.stride() == q.stride() or q.numel() == 0,
+          "q_out in q's place must have q's strides")
+    _on_device(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, axis, k_scale, v_scale,
+               status)
+    r = Rotary(cos_sin=cos_sin.data_ptr(), positions=positions.data_ptr(),
+               axis=None if axis is None else axis.data_ptr(),
+               pos_stride_axis=positions.stride(0), pos_stride_b=positions.stride(1),
+               n_positions=cos_sin.shape[0], n_axes=positions.shape[0], pairs=pairs,
+               adjacent=int(bool(adjacent)))
+    return BoundCall(load().gdn_kv4_append_rotary, "gdn_kv4_append_rotary",
+                     (ctypes.byref(c), ctypes.byref(r), _ptr(q), *qs, Hq, _ptr(q_out), *out,
+                      _ptr(k), _ptr(v), _dtype16(q), *ks, *vs, N, _stream(stream)),
+                     (c, r, q, k, v, positions, cos_sin, pages, table, kv_len, q_out, axis,
+                      k_scale, v_scale, status))
+
+
+def gdn_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, **kw):
+    """Turn q [B,N,Hq,D] and k [B,N,Hkv,D] by their rotary positions, write the queries to q_out
+    (q itself, or a tensor apart) and append k and v to the 4-bit cache as gdn_kv4_append does.
+
+    positions int32 [axes,B,N]; cos_sin float32 [n_positions,2,pairs], the cosines and sines of
+    every position; axis an optional uint8 [pairs], the axis that each pair goes by (None: all by
+    axis 0); adjacent=False pairs channels i and pairs + i, True 2i and 2i + 1; channels from
+    2*pairs on pass.  float32, bfloat16 or float16, any batch and node strides; the others as for
+    gdn_kv4_append (see include/gdn.h)."""
+    bind_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, **kw)()
+
+
 def bind_kv4_read(pages, table, kv_len, k_out, v_out, *, k_scale=None, v_scale=None, status=None,
                   stream=None):
     """gdn_kv4_read bound to these buffers."""
@@ -632,9 +714,10 @@ def gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D) -> int:
     return int(load().gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D))
 
 
-def bind_kv4_attention(q, pages, table, kv_len, o, workspace, *, scale, parent=None, lse=None,
-                       k_scale=None, v_scale=None, status=None, stream=None):
-    """gdn_kv4_attention bound to these buffers."""
+def _kv4_attention(q, pages, table, kv_len, o, workspace, scale, parent, lse, k_scale, v_scale,
+                   status):
+    """What every form of the attention is given: the cache, the leading and the trailing
+    arguments of the call, and what they point to."""
     import torch
 
     _need(pages.dim() == 4, "attention takes one layer's pages")
@@ -646,12 +729,18 @@ def bind_kv4_attention(q, pages, table, kv_len, o, workspace, *, scale, parent=N
     _i32(parent, (B, N), "parent")
     _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and
                           tuple(lse.shape) == (B, N, Hq)), "lse must be float32 [B,N,Hq]")
+    return ((ctypes.byref(c), _ptr(q), _dtype16(q), *qs, N, Hq, scale),
+            (_ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size()),
+            (c, q, pages, table, kv_len, o, workspace, parent, lse, k_scale, v_scale, status))
+
+
+def bind_kv4_attention(q, pages, table, kv_len, o, workspace, *, scale, parent=None, lse=None,
+                       k_scale=None, v_scale=None, status=None, stream=None):
+    """gdn_kv4_attention bound to these buffers."""
+    lead, trail, keep = _kv4_attention(q, pages, table, kv_len, o, workspace, scale, parent, lse,
+                                       k_scale, v_scale, status)
     return BoundCall(load().gdn_kv4_attention, "gdn_kv4_attention",
-                     (ctypes.byref(c), _ptr(q), _dtype16(q), *qs, N, Hq, scale, _ptr(parent),
-                      _ptr(o), _ptr(lse), _ptr(workspace),
-                      workspace.numel() * workspace.element_size(), _stream(stream)),
-                     (c, q, pages, table, kv_len, o, workspace, parent, lse, k_scale, v_scale,
-                      status))
+                     (*lead, _ptr(parent), *trail, _stream(stream)), keep)
 
 
 def gdn_kv4_attention(q, pages, table, kv_len, o, workspace, **kw):
@@ -664,6 +753,52 @@ def gdn_kv4_attention(q, pages, table, kv_len, o, workspace, **kw):
     scale a float; lse an optional float32 [B,N,Hq]; the others as for
     gdn_kv4_append."""
     bind_kv4_attention(q, pages, table, kv_len, o, workspace, **kw)()
+
+
+def bind_kv4_attention_window(q, pages, table, kv_len, o, workspace, *, scale, window, sinks=0,
+                              parent=None, lse=None, k_scale=None, v_scale=None, status=None,
+                              stream=None):
+    """gdn_kv4_attention_window bound to these buffers."""
+    lead, trail, keep = _kv4_attention(q, pages, table, kv_len, o, workspace, scale, parent, lse,
+                                       k_scale, v_scale, status)
+    _on_device(*keep[1:])
+    most = 2 ** 31 - 1  # longer than any sequence
+    return BoundCall(load().gdn_kv4_attention_window, "gdn_kv4_attention_window",
+                     (*lead, min(sinks, most), min(window, most), _ptr(parent), *trail,
+                      _stream(stream)), keep)
+
+
+def gdn_kv4_attention_window(q, pages, table, kv_len, o, workspace, **kw):
+    """gdn_kv4_attention over the last `window` entries of each node's path, the node itself
+    among them, and the first `sinks` (default 0); both integers.  The other arguments, the
+    workspace among them, as for gdn_kv4_attention."""
+    bind_kv4_attention_window(q, pages, table, kv_len, o, workspace, **kw)()
+
+
+def gdn_kv4_attention_shared_workspace_bytes(B, N, Hq, Hkv, D, n_groups) -> int:
+    return int(load().gdn_kv4_attention_shared_workspace_bytes(B, N, Hq, Hkv, D, n_groups))
+
+
+def bind_kv4_attention_shared(q, pages, table, kv_len, group, o, workspace, *, scale, parent=None,
+                              lse=None, k_scale=None, v_scale=None, status=None, stream=None):
+    """gdn_kv4_attention_shared bound to these buffers."""
+    lead, trail, keep = _kv4_attention(q, pages, table, kv_len, o, workspace, scale, parent, lse,
+                                       k_scale, v_scale, status)
+    _i32(group, (group.numel(),), "group")
+    _on_device(*keep[1:], group)
+    return BoundCall(load().gdn_kv4_attention_shared, "gdn_kv4_attention_shared",
+                     (*lead, _ptr(parent), _ptr(group), group.numel() - 1, *trail,
+                      _stream(stream)), (*keep, group))
+
+
+def gdn_kv4_attention_shared(q, pages, table, kv_len, group, o, workspace, **kw):
+    """gdn_kv4_attention of a batch whose sequences share pages (branches made by gdn_kv4_fork):
+    the part that the sequences of a group have in common is read once for all of them.
+
+    group int32 [n_groups + 1]: group g is sequences group[g] .. group[g+1] - 1 of the batch; how
+    much they share follows from the table.  workspace a uint8 tensor of
+    gdn_kv4_attention_shared_workspace_bytes(...) bytes; the others as for gdn_kv4_attention."""
+    bind_kv4_attention_shared(q, pages, table, kv_len, group, o, workspace, **kw)()
 
 
 def bind_kv4_commit(pages, table, kv_len, accept_idx, len_out, *, N, parent=None, status=None,

@@ -196,6 +196,31 @@ int kv4_checks(const gdn_kv4_cache* c, int32_t N) {
   return GDN_OK;
 }
 
+// Query rows of a batch, that the join of shared and own parts counts in 31 bits.
+bool kv4_shared_rows(int32_t B, int32_t N, int32_t Hq) {
+  return (int64_t)N * Hq <= 0x7fffffff / B;
+}
+
+// What every form of the attention checks, but for the size of its workspace.
+int kv4_attention_checks(const gdn_kv4_cache* c, const void* q, int32_t dtype, int64_t q_stride_b,
+                         int64_t q_stride_n, int32_t N, int32_t Hq, const int32_t* parent,
+                         const void* o, const float* lse, const void* workspace) {
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (Hq < 1 || Hq % c->Hkv != 0) return GDN_ERR_INVALID_ARG;
+  if (dtype == GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
+  if (parent != nullptr && N > 64) return GDN_ERR_UNSUPPORTED;
+  if (!kv4_rows(N, Hq)) return GDN_ERR_UNSUPPORTED;
+  if (c->B == 0) return GDN_OK;
+  if (q == nullptr || o == nullptr) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(q) || !gdn::aligned16(o) || !gdn::aligned16(workspace))
+    return GDN_ERR_MISALIGNED;
+  if (q_stride_b % 8 != 0 || q_stride_n % 8 != 0) return GDN_ERR_MISALIGNED;
+  if (!ok_ptr4(parent) || !ok_ptr4(lse)) return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
 int kv4_pool_checks(const gdn_kv4_pool* p, const int32_t* a, const int32_t* b, int32_t F) {
   if (p == nullptr || F < 0) return GDN_ERR_INVALID_ARG;
   if (p->n_rows < 1 || p->max_pages < 1 || p->n_pages < 1 || p->page_tokens < 1)
@@ -399,6 +424,38 @@ int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t
                                 N, static_cast<cudaStream_t>(stream));
 }
 
+int gdn_kv4_append_rotary(const gdn_kv4_cache* c, const gdn_rotary* r, const void* q,
+                          int64_t q_stride_b, int64_t q_stride_n, int32_t Hq, void* q_out,
+                          int64_t out_stride_b, int64_t out_stride_n, const void* k, const void* v,
+                          int32_t dtype, int64_t k_stride_b, int64_t k_stride_n,
+                          int64_t v_stride_b, int64_t v_stride_n, int32_t N, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_checks(c, N);
+  if (st != GDN_OK) return st;
+  if (dtype != GDN_F32 && dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
+  if (r == nullptr || Hq < 1 || Hq % c->Hkv != 0) return GDN_ERR_INVALID_ARG;
+  if (r->pairs < 1 || r->n_positions < 1 || r->n_axes < 1) return GDN_ERR_INVALID_ARG;
+  if (r->adjacent != 0 && r->adjacent != 1) return GDN_ERR_INVALID_ARG;
+  if (r->pairs % 8 != 0 || r->pairs > c->D / 2 || Hq > 65535) return GDN_ERR_UNSUPPORTED;
+  if (c->B == 0) return GDN_OK;
+  if (q == nullptr || q_out == nullptr || k == nullptr || v == nullptr || r->cos_sin == nullptr ||
+      r->positions == nullptr)
+    return GDN_ERR_INVALID_ARG;
+  if (q == q_out && (q_stride_b != out_stride_b || q_stride_n != out_stride_n))
+    return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16(q) || !gdn::aligned16(q_out) || !gdn::aligned16(k) || !gdn::aligned16(v) ||
+      !gdn::aligned16(r->cos_sin) || !ok_ptr4(r->positions))
+    return GDN_ERR_MISALIGNED;
+  const int64_t unit = dtype == GDN_F32 ? 4 : 8;
+  for (int64_t stride : {q_stride_b, q_stride_n, out_stride_b, out_stride_n, k_stride_b, k_stride_n,
+                         v_stride_b, v_stride_n})
+    if (stride % unit != 0) return GDN_ERR_MISALIGNED;
+  return gdn::launch_kv4_append_rotary(*c, *r, q, q_stride_b, q_stride_n, Hq, q_out, out_stride_b,
+                                       out_stride_n, k, v, dtype, k_stride_b, k_stride_n,
+                                       v_stride_b, v_stride_n, N,
+                                       static_cast<cudaStream_t>(stream));
+}
+
 int gdn_kv4_read(const gdn_kv4_cache* c, void* k_out, void* v_out, int32_t dtype, int32_t N,
                  void* stream) {
   GDN_RANGE();
@@ -423,24 +480,60 @@ int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int6
                       const int32_t* parent, void* o, float* lse, void* workspace,
                       size_t workspace_bytes, void* stream) {
   GDN_RANGE();
-  const int st = kv4_checks(c, N);
-  if (st != GDN_OK) return st;
-  if (Hq < 1 || Hq % c->Hkv != 0) return GDN_ERR_INVALID_ARG;
-  if (dtype == GDN_F32) return GDN_ERR_UNSUPPORTED;
-  if (dtype != GDN_BF16 && dtype != GDN_F16) return GDN_ERR_INVALID_ARG;
-  if (parent != nullptr && N > 64) return GDN_ERR_UNSUPPORTED;
-  if (!kv4_rows(N, Hq)) return GDN_ERR_UNSUPPORTED;
-  if (c->B == 0) return GDN_OK;
-  if (q == nullptr || o == nullptr) return GDN_ERR_INVALID_ARG;
-  if (!gdn::aligned16(q) || !gdn::aligned16(o) || !gdn::aligned16(workspace))
-    return GDN_ERR_MISALIGNED;
-  if (q_stride_b % 8 != 0 || q_stride_n % 8 != 0) return GDN_ERR_MISALIGNED;
-  if (!ok_ptr4(parent) || !ok_ptr4(lse)) return GDN_ERR_MISALIGNED;
+  const int st = kv4_attention_checks(c, q, dtype, q_stride_b, q_stride_n, N, Hq, parent, o, lse,
+                                      workspace);
+  if (st != GDN_OK || c->B == 0) return st;
   if (workspace == nullptr ||
       workspace_bytes < gdn_kv4_attention_workspace_bytes(c->B, N, Hq, c->Hkv, c->D))
     return GDN_ERR_WORKSPACE;
   return gdn::launch_kv4_attention(*c, q, dtype, q_stride_b, q_stride_n, N, Hq, scale, parent, o,
                                    lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int gdn_kv4_attention_window(const gdn_kv4_cache* c, const void* q, int32_t dtype,
+                             int64_t q_stride_b, int64_t q_stride_n, int32_t N, int32_t Hq,
+                             float scale, int32_t sinks, int32_t window, const int32_t* parent,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  GDN_RANGE();
+  if (window < 1 || sinks < 0) return GDN_ERR_INVALID_ARG;
+  const int st = kv4_attention_checks(c, q, dtype, q_stride_b, q_stride_n, N, Hq, parent, o, lse,
+                                      workspace);
+  if (st != GDN_OK || c->B == 0) return st;
+  if (workspace == nullptr ||
+      workspace_bytes < gdn_kv4_attention_workspace_bytes(c->B, N, Hq, c->Hkv, c->D))
+    return GDN_ERR_WORKSPACE;
+  return gdn::launch_kv4_attention_window(*c, q, dtype, q_stride_b, q_stride_n, N, Hq, scale, sinks,
+                                          window, parent, o, lse, workspace,
+                                          static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_kv4_attention_shared_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                                                int32_t D, int32_t n_groups) {
+  if (gdn_kv4_attention_workspace_bytes(B, N, Hq, Hkv, D) == 0) return 0;
+  if (n_groups < 1 || n_groups > B || !kv4_shared_rows(B, N, Hq)) return 0;
+  return gdn::kv4_attention_shared_workspace_bytes(B, N, Hq, Hkv, D, n_groups);
+}
+
+int gdn_kv4_attention_shared(const gdn_kv4_cache* c, const void* q, int32_t dtype,
+                             int64_t q_stride_b, int64_t q_stride_n, int32_t N, int32_t Hq,
+                             float scale, const int32_t* parent, const int32_t* group,
+                             int32_t n_groups, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  GDN_RANGE();
+  const int st = kv4_attention_checks(c, q, dtype, q_stride_b, q_stride_n, N, Hq, parent, o, lse,
+                                      workspace);
+  if (st != GDN_OK || c->B == 0) return st;
+  if (group == nullptr || n_groups < 1 || n_groups > c->B) return GDN_ERR_INVALID_ARG;
+  if (!kv4_shared_rows(c->B, N, Hq)) return GDN_ERR_UNSUPPORTED;
+  if (!ok_ptr4(group)) return GDN_ERR_MISALIGNED;
+  if (workspace == nullptr ||
+      workspace_bytes <
+          gdn_kv4_attention_shared_workspace_bytes(c->B, N, Hq, c->Hkv, c->D, n_groups))
+    return GDN_ERR_WORKSPACE;
+  return gdn::launch_kv4_attention_shared(*c, q, dtype, q_stride_b, q_stride_n, N, Hq, scale,
+                                          parent, group, n_groups, o, lse, workspace,
+                                          static_cast<cudaStream_t>(stream));
 }
 
 int gdn_kv4_commit(const gdn_kv4_cache* c, int64_t layer_stride, int32_t n_layers, int32_t N,
@@ -519,6 +612,7 @@ const char* gdn_status_string(int status) {
     case GDN_ERR_POOL_EMPTY: return "GDN_ERR_POOL_EMPTY";
     case GDN_ERR_ROW_RANGE: return "GDN_ERR_ROW_RANGE";
     case GDN_ERR_NONFINITE: return "GDN_ERR_NONFINITE";
+    case GDN_ERR_POSITION_RANGE: return "GDN_ERR_POSITION_RANGE";
     default: return "GDN_ERR_UNKNOWN";
   }
 }

@@ -8,19 +8,41 @@ namespace gdn {
 namespace {
 
 using kv4::AttnArgs;
+using kv4::round_rows;
+using kv4::row_tiles;
 
-// Query rows of a tile.  K and V are brought in and dequantised once per row tile, so
-// wide ones pay: with tiles of at most 64 rows a 2048-token piece of a prompt takes 431 us,
-// eight chains of 16 (96 rows) 79.8 us and a tree of 22 (132 rows, three tiles of 44)
-// 42.8 us, with 96 367, 64.0 and 40.7 us (in turn on one box).  Rows are spread evenly over
-// the tiles.  More than 96 do not fit tensor memory beside two units of K and V (D = 256).
-constexpr int kMaxRows = 96;
+// What all forms of the attention are given.
+AttnArgs attn_args(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb, int64_t qsn,
+                   int N, int Hq, float scale, const int32_t* parent, void* o, float* lse) {
+  AttnArgs a = {};
+  a.c = c;
+  a.q = q;
+  a.q_stride_b = qsb;
+  a.q_stride_n = qsn;
+  a.parent = parent;
+  a.o = o;
+  a.lse = lse;
+  a.scale = scale;
+  a.N = N;
+  a.Hq = Hq;
+  a.G = Hq / c.Hkv;
+  a.rows_total = N * a.G;
+  row_tiles(a.rows_total, &a.row_tiles, &a.rows_per_tile);
+  a.bf16 = dtype == GDN_BF16;
+  return a;
+}
 
-int round_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kMaxRows; }
+// The kernels count tiles in 32 bits.
+bool countable(const gdn_kv4_cache& c, int64_t row_tiles) {
+  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128 + 8;
+  return row_tiles <= INT32_MAX / c.Hkv && row_tiles * c.Hkv <= INT32_MAX / tiles;
+}
 
-void row_tiles(int rows, int* tiles, int* per_tile) {
-  *tiles = (rows + kMaxRows - 1) / kMaxRows;
-  *per_tile = (rows + *tiles - 1) / *tiles;
+// Workspace of the parts that a pass with one output leaves to its join.
+void place_parts(AttnArgs& a, void* workspace, int NT, int parts) {
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * parts * NT * a.c.D);
+  a.join = reinterpret_cast<kv4::AttnJoin*>(a.part_ml + (size_t)2 * parts * NT);
 }
 
 }  // namespace
@@ -39,35 +61,146 @@ int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64
                          void* workspace, cudaStream_t s) {
   const int parts = sm_count();  // one block per SM: a block takes the whole of tensor memory
   if (parts == 0) return GDN_ERR_CUDA;
-  AttnArgs a = {};
-  a.c = c;
-  a.q = q;
-  a.q_stride_b = qsb;
-  a.q_stride_n = qsn;
-  a.parent = parent;
-  a.o = o;
-  a.lse = lse;
-  a.scale = scale;
-  a.N = N;
-  a.Hq = Hq;
-  a.G = Hq / c.Hkv;
-  a.rows_total = N * a.G;
-  row_tiles(a.rows_total, &a.row_tiles, &a.rows_per_tile);
-  a.bf16 = dtype == GDN_BF16;
-  // the kernels count tiles in 32 bits
-  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128 + 8;
-  if ((int64_t)a.row_tiles * c.B > INT32_MAX / c.Hkv ||
-      (int64_t)a.row_tiles * c.B * c.Hkv > INT32_MAX / tiles)
-    return GDN_ERR_UNSUPPORTED;
+  AttnArgs a = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
+  if (!countable(c, (int64_t)a.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
   const int NT = round_rows(a.rows_per_tile);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * parts * NT * c.D);
-  a.join = reinterpret_cast<kv4::AttnJoin*>(a.part_ml + (size_t)2 * parts * NT);
+  place_parts(a, workspace, NT, parts);
   switch (c.D) {
     case 64: return kv4::attn_launch_64(a, NT, parts, s);
     case 128: return kv4::attn_launch_128(a, NT, parts, s);
     default: return kv4::attn_launch_256(a, NT, parts, s);
   }
+}
+
+int launch_kv4_attention_window(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
+                                int64_t qsn, int N, int Hq, float scale, int sinks, int window,
+                                const int32_t* parent, void* o, float* lse, void* workspace,
+                                cudaStream_t s) {
+  const int parts = sm_count();
+  if (parts == 0) return GDN_ERR_CUDA;
+  AttnArgs a = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
+  if (!countable(c, (int64_t)a.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
+  // no sequence is longer than the table is wide: positions less a window stay in 32 bits
+  const int longest = c.max_pages * c.page_tokens;
+  a.window = window < longest ? window : longest;
+  a.sinks = sinks < longest ? sinks : longest;
+  const int NT = round_rows(a.rows_per_tile);
+  place_parts(a, workspace, NT, parts);
+  switch (c.D) {
+    case 64: return kv4::window_launch_64(a, NT, parts, s);
+    case 128: return kv4::window_launch_128(a, NT, parts, s);
+    default: return kv4::window_launch_256(a, NT, parts, s);
+  }
+}
+
+// ---------------------------------------------------------------- shared prompts
+namespace {
+
+// Workspace of a call that reads shared pages once: the plan's numbers, each row's first part
+// of both passes, and the parts that go on from another block.
+struct SharedSpace {
+  int32_t* plan;
+  float *row_o[2], *part_o[2];
+  kv4::RowPart* row_part[2];
+  float2* part_ml[2];
+  size_t bytes;
+};
+
+SharedSpace shared_space(void* base, int B, int N, int Hq, int Hkv, int D, int n_groups, int sms) {
+  int tiles, per_tile;
+  row_tiles(N * (Hq / Hkv), &tiles, &per_tile);
+  const size_t rows = (size_t)B * N * Hq;
+  const int NT[2] = {kv4::kMaxRows, round_rows(per_tile)};
+  SharedSpace w = {};
+  uint8_t* at = static_cast<uint8_t*>(base);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = at + w.bytes;
+    w.bytes += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  w.plan = reinterpret_cast<int32_t*>(take(4 * (size_t)(4 * (int64_t)n_groups + B)));
+  for (int i = 0; i < 2; ++i) {
+    w.row_o[i] = reinterpret_cast<float*>(take(rows * D * 4));
+    w.row_part[i] = reinterpret_cast<kv4::RowPart*>(take(rows * sizeof(kv4::RowPart)));
+    w.part_o[i] = reinterpret_cast<float*>(take((size_t)sms * NT[i] * D * 4));
+    w.part_ml[i] = reinterpret_cast<float2*>(take((size_t)sms * NT[i] * 8));
+  }
+  return w;
+}
+
+// Whether rows of several sequences in one tile can save anything: where one sequence's
+// rows fill their tiles, reading the prefix once saves bytes that L2 gives anyway.
+bool rows_worth_sharing(int N, int G) {
+  const int64_t rows = (int64_t)N * G;
+  const int64_t tiles = (rows + kv4::kMaxRows - 1) / kv4::kMaxRows;
+  return rows <= 2 * kv4::kMaxRows && 4 * tiles * kv4::kMaxRows >= 5 * rows;
+}
+
+}  // namespace
+
+size_t kv4_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int n_groups) {
+  const size_t alone = kv4_attention_workspace_bytes(B, N, Hq, Hkv, D);
+  if (!rows_worth_sharing(N, Hq / Hkv)) return alone;
+  const int sms = sm_count();
+  const size_t shared =
+      shared_space(nullptr, B, N, Hq, Hkv, D, n_groups, sms > 0 ? sms : 256).bytes;
+  return shared > alone ? shared : alone;
+}
+
+int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
+                                int64_t qsn, int N, int Hq, float scale, const int32_t* parent,
+                                const int32_t* group, int n_groups, void* o, float* lse,
+                                void* workspace, cudaStream_t s) {
+  const int parts = sm_count();
+  if (parts == 0) return GDN_ERR_CUDA;
+  AttnArgs own = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
+  if (!countable(c, (int64_t)own.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
+  if (!rows_worth_sharing(N, own.G))
+    return launch_kv4_attention(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse, workspace, s);
+  // the rows of a group as if they were one sequence's, in tiles as wide as a group of the
+  // usual size fills
+  AttnArgs pre = own;
+  const int64_t most = (int64_t)c.B * own.rows_total;
+  const int64_t usual = (int64_t)((c.B + n_groups - 1) / n_groups) * own.rows_total;
+  int tiles, per_tile;
+  row_tiles((int)(usual < most ? usual : most), &tiles, &per_tile);
+  const int NT = round_rows(per_tile);
+  pre.rows_per_tile = NT;
+  pre.row_tiles = (int)((most + NT - 1) / NT);
+  if (!countable(c, (int64_t)pre.row_tiles + n_groups)) return GDN_ERR_UNSUPPORTED;
+  const SharedSpace w =
+      shared_space(workspace, c.B, N, Hq, c.Hkv, c.D, n_groups, parts);
+  int32_t* start = w.plan + 4 * (int64_t)n_groups;
+  int rc = launch_kv4_shared_plan(c, N, parent, group, n_groups, w.plan, start, s);
+  if (rc != GDN_OK) return rc;
+  pre.parent = nullptr;
+  pre.c.B = n_groups;
+  pre.c.kv_len = w.plan;
+  pre.extra = w.plan + n_groups;
+  pre.group_seq = w.plan + 2 * (int64_t)n_groups;
+  pre.group_row = w.plan + 3 * (int64_t)n_groups;
+  own.extra = start;
+  for (int i = 0; i < 2; ++i) {
+    AttnArgs& a = i == 0 ? pre : own;
+    a.row_o = w.row_o[i];
+    a.row_part = w.row_part[i];
+    a.part_o = w.part_o[i];
+    a.part_ml = w.part_ml[i];
+  }
+  const int NTo = round_rows(own.rows_per_tile);
+  switch (c.D) {
+    case 64: rc = kv4::prefix_launch_64(pre, NT, parts, s); break;
+    case 128: rc = kv4::prefix_launch_128(pre, NT, parts, s); break;
+    default: rc = kv4::prefix_launch_256(pre, NT, parts, s);
+  }
+  if (rc != GDN_OK) return rc;
+  switch (c.D) {
+    case 64: rc = kv4::own_launch_64(own, NTo, parts, s); break;
+    case 128: rc = kv4::own_launch_128(own, NTo, parts, s); break;
+    default: rc = kv4::own_launch_256(own, NTo, parts, s);
+  }
+  if (rc != GDN_OK) return rc;
+  return launch_kv4_shared_join(own, pre, NTo, NT, parts, s);
 }
 
 }  // namespace gdn

@@ -119,10 +119,26 @@ struct AttnCfg {
 };
 
 // The part of one item that a block works on: tiles [t0, t1) of `tiles` (t1 = 0: the end).
+// The item's tiles from number `near` on lie `skip` tiles further along the sequence.
 struct Seg {
   int b, h, t0, t1, tiles, len, row0, rows;
   int last;  // block that holds the item's last tile
+  int near, skip;
+  int lo;    // window: first position that the item's first node sees beside the sinks
 };
+
+// The tiles of an item.
+struct Span {
+  int tiles, near, skip;
+};
+
+// Place in the sequence of an item's tile t.
+template <Mode M>
+__device__ __forceinline__ int tile_at(const Seg& s, int t) {
+  if constexpr (M == kWindow) return t + (t >= s.near ? s.skip : 0);
+  if constexpr (M == kOwn) return t + s.skip;
+  return t;
+}
 
 // What a block's work is measured in: an item's tiles, and kLead more before them
 // for what an item costs beside its tiles (its queries, first references and
@@ -160,8 +176,11 @@ constexpr int kSegs = 16;    // ring of segments
 constexpr int kTiles = 32;   // ring of tiles' page checks; copies are fewer tiles ahead
 constexpr int kLens = 1024;  // lengths kept in shared memory
 
-template <typename C>
+template <typename C, Mode M>
 struct AttnShared {
+  // (with a second number a sequence, kPrefix and kOwn keep half as many)
+  static constexpr int LENS = M == kPrefix || M == kOwn ? kLens / 2 : kLens;
+  static constexpr int WIN = M == kWindow;
   uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
   uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
@@ -186,7 +205,10 @@ struct AttnShared {
   // for the functions that are not inlined: a reference to the kernel's parameters
   // themselves is read through global memory
   AttnArgs args;
-  int len[kLens];
+  int len[LENS];
+  int extra[M == kPrefix || M == kOwn ? LENS : 1];  // members of a group; first own tile
+  uint2 seen[WIN ? 64 : 1];                         // window: of a node's path, what it sees
+  int row_lo[WIN ? C::NT : 1];                      // and the first position before the block
 };
 
 // A wait that ends: false once any wait of the block has run out.
@@ -346,33 +368,89 @@ static __device__ __noinline__ int attn_len(const AttnArgs& a, int b, bool repor
   return n;
 }
 
-// Tiles that row tile `rt` of a sequence of `len` positions sees.
-__device__ __forceinline__ int attn_tiles(const AttnArgs& a, int len, int rt) {
+// First position that the window leaves the first node of row tile `rt` (may be negative;
+// the host keeps the window within the table's width, so this stays in 32 bits).
+__device__ __forceinline__ int attn_lo(const AttnArgs& a, int len, int rt) {
+  const int first = a.parent == nullptr ? rt * a.rows_per_tile / a.G : 0;  // a tree's root
+  return len - a.N + first - a.window + 1;
+}
+
+// Tiles that row tile `rt` of a sequence of `len` positions sees.  `extra`: kPrefix, the
+// sequences in the group (whose rows are one after another); kOwn, the first tile that is not
+// the group's.
+template <Mode M>
+__device__ __forceinline__ Span attn_span(const AttnArgs& a, int len, int extra, int rt) {
+  if constexpr (M == kPrefix) {
+    const int64_t rows = (int64_t)extra * a.rows_total;
+    return {(int64_t)rt * a.rows_per_tile < rows ? len / kTile : 0, 0, 0};
+  }
   int see = len;
   if (a.parent == nullptr) {
     const int last = min((rt + 1) * a.rows_per_tile, a.rows_total) - 1;
     see = len - a.N + last / a.G + 1;
   }
-  return see <= 0 ? 0 : (see + kTile - 1) / kTile;
+  const int tiles = see <= 0 ? 0 : (see + kTile - 1) / kTile;
+  if constexpr (M == kWindow) {
+    // tiles of sinks, and those from the window's first on
+    const int near = min(tiles, (a.sinks + kTile - 1) / kTile);
+    const int skip = max(0, attn_lo(a, len, rt) / kTile - near);
+    return {tiles - skip, near, skip};
+  }
+  if constexpr (M == kOwn) return {max(tiles - extra, 0), 0, extra};
+  return {tiles, 0, 0};
 }
 
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
-// The lengths the block works with: the first kLens are kept in shared memory.
+// A second number of a sequence (see attn_span); 0 where the mode has none.
+template <Mode M>
+__device__ __forceinline__ int attn_extra(const AttnArgs& a, int b) {
+  return M == kPrefix || M == kOwn ? max(a.extra[b], 0) : 0;
+}
+
+// Length of sequence b, by the plan where there is one (its first own tile is -1 for a
+// sequence that is skipped).
+template <Mode M>
+__device__ __forceinline__ int attn_len_of(const AttnArgs& a, int b) {
+  if constexpr (M == kPrefix) return a.c.kv_len[b];
+  if constexpr (M == kOwn) return a.extra[b] < 0 ? 0 : a.c.kv_len[b];
+  return attn_len(a, b, false);
+}
+
+// The lengths the block works with: the first LENS are kept in shared memory.
+template <Mode M, int LENS>
 struct Lens {
   const AttnArgs& a;
   const int* kept;
+  const int* kept_extra;
   __device__ __forceinline__ int operator()(int b) const {
-    return b < kLens ? kept[b] : attn_len(a, b, false);
+    return b < LENS ? kept[b] : attn_len_of<M>(a, b);
+  }
+  __device__ __forceinline__ int extra(int b) const {
+    if constexpr (M == kPrefix || M == kOwn) return b < LENS ? kept_extra[b] : attn_extra<M>(a, b);
+    return 0;
   }
 };
 
 // Lengths into shared memory, by all threads: a thread a sequence, or for
 // trees a warp a sequence (its lanes check the nodes).  Returns whether any of
 // this thread's differs from what was there.
-static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, bool report_it) {
+template <Mode M, int LENS>
+static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, int* kept_extra,
+                                              bool report_it) {
   bool changed = false;
-  const int lane = threadIdx.x & 31, n_kept = min(a.c.B, kLens);
+  const int lane = threadIdx.x & 31, n_kept = min(a.c.B, LENS);
+  if constexpr (M == kPrefix || M == kOwn) {  // checked and reported by the plan
+#pragma unroll 1
+    for (int b = threadIdx.x; b < n_kept; b += blockDim.x) {
+      const int x = *(const volatile int32_t*)(a.extra + b);
+      const int len = x < 0 ? 0 : *(const volatile int32_t*)(a.c.kv_len + b);
+      changed |= kept[b] != len || kept_extra[b] != max(x, 0);
+      kept[b] = len;
+      kept_extra[b] = max(x, 0);
+    }
+    return changed;
+  }
   const int unit = a.parent == nullptr ? 1 : 32;  // threads of a sequence
 #pragma unroll 1
   for (int b = threadIdx.x / unit; b < n_kept; b += blockDim.x / unit) {
@@ -401,39 +479,42 @@ static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, bool
   }
   if (report_it)  // the others' reports (their lengths are looked up when needed)
 #pragma unroll 1
-    for (int b = kLens + threadIdx.x; b < a.c.B; b += blockDim.x) (void)attn_len(a, b, true);
+    for (int b = LENS + threadIdx.x; b < a.c.B; b += blockDim.x) (void)attn_len(a, b, true);
   return changed;
 }
 
 // The same in units of work.
-__device__ __forceinline__ int attn_units(const AttnArgs& a, int len, int rt) {
-  const int t = attn_tiles(a, len, rt);
+template <Mode M>
+__device__ __forceinline__ int attn_units(const AttnArgs& a, int len, int extra, int rt) {
+  const int t = attn_span<M>(a, len, extra, rt).tiles;
   return t > 0 ? t + kLead : 0;
 }
 
 // Units of sequence b over all heads, by a whole warp.
-__device__ __forceinline__ int warp_cost(const AttnArgs& a, int len) {
+template <Mode M>
+__device__ __forceinline__ int warp_cost(const AttnArgs& a, int len, int extra) {
   int t = 0;
 #pragma unroll 1
-  for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_units(a, len, rt);
+  for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_units<M>(a, len, extra, rt);
   return warp_sum(t) * a.c.Hkv;
 }
 
 // The run of block `part` of `parts`: the units of all sequences are counted,
 // then the sequence that holds the run's first one is taken apart.
-static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens, int part,
+template <Mode M, int LENS>
+static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens<M, LENS>& lens, int part,
                                             int parts) {
   const int lane = threadIdx.x & 31;
   const bool by_lane = a.row_tiles <= 4;  // a lane a sequence, or the warp a sequence
   const int step = by_lane ? 32 : 1;
   // units of the sequence b0 + lane, or (of all lanes the same) of b0
   auto units = [&](int b0) {
-    if (!by_lane) return warp_cost(a, lens(b0));
+    if (!by_lane) return warp_cost<M>(a, lens(b0), lens.extra(b0));
     int x = 0;
     if (b0 + lane < a.c.B) {
-      const int len = lens(b0 + lane);
+      const int len = lens(b0 + lane), extra = lens.extra(b0 + lane);
 #pragma unroll 1
-      for (int rt = 0; rt < a.row_tiles; ++rt) x += attn_units(a, len, rt);
+      for (int rt = 0; rt < a.row_tiles; ++rt) x += attn_units<M>(a, len, extra, rt);
     }
     return x * a.c.Hkv;
   };
@@ -471,12 +552,12 @@ static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens,
     break;
   }
   int in = r.at - before;  // of the sequence's `its` tiles
-  const int per_head = its / a.c.Hkv, len = lens(r.b);
+  const int per_head = its / a.c.Hkv, len = lens(r.b), extra = lens.extra(r.b);
   r.h = in / per_head;
   in -= r.h * per_head;
 #pragma unroll 1
   for (;; ++r.rt) {
-    const int t = attn_units(a, len, r.rt);
+    const int t = attn_units<M>(a, len, extra, r.rt);
     if (in < t) break;
     in -= t;
   }
@@ -485,12 +566,14 @@ static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens& lens,
 }
 
 // The run's next segment (t1 = 0 when it is at its end).
-static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens& lens, Run& r) {
+template <Mode M, int LENS>
+static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens<M, LENS>& lens, Run& r) {
   Seg s = {};
 #pragma unroll 1
   while (r.left > 0 && r.b < a.c.B) {
-    const int len = lens(r.b);
-    const int tiles = attn_tiles(a, len, r.rt), units = tiles > 0 ? tiles + kLead : 0;
+    const int len = lens(r.b), extra = lens.extra(r.b);
+    const Span span = attn_span<M>(a, len, extra, r.rt);
+    const int tiles = span.tiles, units = tiles > 0 ? tiles + kLead : 0;
     const int rt = r.rt, h = r.h, b = r.b, end = min(units, r.u0 + r.left), taken = end - r.u0;
     const int t0 = max(r.u0 - kLead, 0), t1 = end - kLead;
     r.u0 = 0;
@@ -504,19 +587,23 @@ static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens& lens,
     s.b = b, s.h = h, s.t0 = t0, s.t1 = t1, s.tiles = tiles, s.len = len;
     s.last = t1 < tiles ? r.runs.of(r.at + tiles - t1 - 1) : 0;
     s.row0 = rt * a.rows_per_tile;
-    s.rows = min(a.rows_total - s.row0, a.rows_per_tile);
+    s.rows = min((M == kPrefix ? extra * a.rows_total : a.rows_total) - s.row0, a.rows_per_tile);
+    s.near = span.near, s.skip = span.skip;
+    if constexpr (M == kWindow) s.lo = attn_lo(a, len, rt);
     return s;
   }
   return s;
 }
 
 // Rows that see no tile at all: 0 (and -infinity), spread over the blocks; 128 threads.
-static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& lens, int D, int tid) {
+template <Mode M, int LENS>
+static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens<M, LENS>& lens, int D,
+                                              int tid) {
   const int64_t pairs = (int64_t)a.c.B * a.row_tiles;
 #pragma unroll 1
   for (int64_t i = blockIdx.x; i < pairs; i += gridDim.x) {
     const int b = (int)(i / a.row_tiles), rt = (int)(i % a.row_tiles);
-    if (attn_tiles(a, lens(b), rt) > 0) continue;
+    if (attn_span<M>(a, lens(b), 0, rt).tiles > 0) continue;
     const int row0 = rt * a.rows_per_tile, rows = min(a.rows_total - row0, a.rows_per_tile);
 #pragma unroll 1
     for (int k = 0; k < rows * a.c.Hkv; ++k) {
@@ -532,14 +619,19 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens& len
 // The query rows of a segment go to the B operand at q, ROWS neighbouring rows a
 // softmax warp.  They are copied as they are to where the operand goes (the copies
 // are this thread's cp.async, not waited for); a lane works out one row's place.
-template <int D, int NT>
+template <int D, int NT, Mode M>
 static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, int b, int h, int row0,
                                                    int rows, uint8_t* q, int warp) {
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;  // channels of a lane
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
-  const int row = row0 + r0 + lane % ROWS, n = row / a.G;
+  const int row = row0 + r0 + lane % ROWS, node = row / a.G;  // over a group's sequences
+  int n = node;
+  if constexpr (M == kPrefix) {
+    const int member = node / a.N;
+    b = a.group_seq[b] + member, n = node - member * a.N;
+  }
   const int64_t mine = b * a.q_stride_b + n * a.q_stride_n +
-                       (int64_t)(h * a.G + row - n * a.G) * D;
+                       (int64_t)(h * a.G + row - node * a.G) * D;
   const uint16_t* src = static_cast<const uint16_t*>(a.q) + ch;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
 #pragma unroll
@@ -591,12 +683,12 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&x)[W]) 
 // rows differ.  One c halves what the softmax reads per row: a 2048-token piece of a
 // prompt 385 -> 369 us, eight chains of 16 65.7 -> 63.3 us; with few rows finding it
 // costs more (48 uneven sequences 81 -> 83 us), and each row has its own.
-template <int D, int NT>
-static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>>& sh,
-                                               int b, int row0, int rows, uint8_t* q, int warp,
-                                               float to_log2) {
+template <int D, int NT, Mode M>
+static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>, M>& sh,
+                                               int b, int len, int row0, int rows, uint8_t* q,
+                                               int warp, float to_log2) {
   const int G = a.G, Hq = a.Hq;
-  const bool bf16 = a.bf16, tree = a.parent != nullptr;
+  const bool bf16 = a.bf16, tree = M != kPrefix && a.parent != nullptr;
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
@@ -633,6 +725,24 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
     for (int i = 0; i < 2; ++i)  // several warps may write the same values
       sh.path[lane + 32 * i] = make_uint2((unsigned)path[i], (unsigned)(path[i] >> 32));
     __syncwarp();
+    if constexpr (M == kWindow) {
+      // of the block, a node sees the last a.window entries of its path, and sinks
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int depth = __popcll(path[i]) - 1;
+        unsigned long long seen = path[i];
+        if (depth >= a.window)
+#pragma unroll 1
+          for (unsigned long long rest = path[i]; rest != 0; rest &= rest - 1) {
+            const int m = __ffsll((long long)rest) - 1;
+            const uint2 p = sh.path[m];
+            const int d = __popc(p.x) + __popc(p.y) - 1;
+            if (d <= depth - a.window && len - a.N + d >= a.sinks) seen &= ~(1ull << m);
+          }
+        sh.seen[lane + 32 * i] = make_uint2((unsigned)seen, (unsigned)(seen >> 32));
+      }
+      __syncwarp();
+    }
   }
   const int row = row0 + min(r0 + lane % ROWS, rows - 1), n = row / G;
   cp_async_wait_all();
@@ -690,6 +800,13 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
     sh.row_c[r] = c;
     sh.row_at[r] = n * Hq + row - n * G;
     if (tree) sh.row_path[r] = sh.path[n];
+    if constexpr (M == kWindow) {
+      if (tree) {
+        const uint2 p = sh.path[n];
+        sh.row_path[r] = sh.seen[n];
+        sh.row_lo[r] = len - a.N + __popc(p.x) + __popc(p.y) - a.window;
+      }
+    }
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -697,16 +814,17 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int D, int NT>
+template <int D, int NT, Mode M>
 __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   using C = AttnCfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ AttnShared<C> sh;
+  __shared__ AttnShared<C, M> sh;
+  constexpr int LENS = AttnShared<C, M>::LENS;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* dead = &sh.dead;
 
-  static_assert(sizeof(AttnArgs) / 4 <= 64 && 64 <= C::THREADS, "a word a thread");
+  static_assert(sizeof(AttnArgs) / 4 <= C::THREADS, "a word a thread");
   if (threadIdx.x < sizeof(AttnArgs) / 4)
     reinterpret_cast<uint32_t*>(&sh.args)[threadIdx.x] =
         reinterpret_cast<const uint32_t*>(&a)[threadIdx.x];
@@ -736,9 +854,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   // wait on the kernel before this one, from the lengths as they read then, and
   // again after it in the case that one of them has changed (with more sequences
   // than are kept, always).
-  const Lens lens = {args, sh.len};
-  const bool kept = a.c.B <= kLens;
-  (void)attn_lens(args, sh.len, false);
+  // (A plan's numbers are the kernel's before this one: there is nothing to read yet in
+  // kPrefix, and they are complete when kOwn starts, whose predecessor waited for them.)
+  const Lens<M, LENS> lens = {args, sh.len, sh.extra};
+  const bool kept = M != kPrefix && a.c.B <= LENS;
+  if constexpr (M != kPrefix) (void)attn_lens<M, LENS>(args, sh.len, sh.extra, false);
   __syncthreads();
   if (warp == C::wI + 2 && kept) {
     Run run = attn_run(args, lens, blockIdx.x, gridDim.x);
@@ -753,10 +873,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   float k_scale = 1.f;
   if (softmax && kept && sh.seg[0].t1 > 0) {
     k_scale = head_scale(sh.seg[0].h);
-    attn_rows_copy<D, NT>(args, sh.seg[0].b, sh.seg[0].h, sh.seg[0].row0, sh.seg[0].rows,
-                          smem + C::oQ, warp - C::wS);
+    attn_rows_copy<D, NT, M>(args, sh.seg[0].b, sh.seg[0].h, sh.seg[0].row0, sh.seg[0].rows,
+                             smem + C::oQ, warp - C::wS);
   }
-  const bool changed = attn_lens(args, sh.len, blockIdx.x == 0);
+  const bool changed = attn_lens<M, LENS>(args, sh.len, sh.extra, blockIdx.x == 0);
   tc::fence_before_sync();
   const bool again = __syncthreads_or(changed) || !kept;
   tc::fence_after_sync();
@@ -828,7 +948,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int quarter = warp & 3;
     const uint32_t dst = ((uint32_t)(quarter * 32) << 16) + C::cV;
     const int vt = threadIdx.x - 32 * C::wV;
-    attn_zero(args, lens, D, vt);
+    if constexpr (M == kFull || M == kWindow) attn_zero(args, lens, D, vt);
     int stage = 0, unit = 0, tile = 0;
     unsigned raw_ph = 0, unit_ph = 1;
     for (;; ++seg_no) {
@@ -841,7 +961,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         // the tile's scales to binary16, 8 positions of a group a step; those past
         // the end, or on a page that is not there, count as 0
         uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
-        const int ok = sh.tile_ok[1][tile & (kTiles - 1)], end = s.len - t * kTile;
+        const int ok = sh.tile_ok[1][tile & (kTiles - 1)];
+        const int end = s.len - tile_at<M>(s, t) * kTile;
         const bool full = ok == 15 && end >= kTile;
 #pragma unroll
         for (int i = vt; i < D; i += 128) {
@@ -908,7 +1029,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int gt = (threadIdx.x - 32 * C::wS) & 127;   // thread of the group
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
-    if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = AttnJoin{};
+    if constexpr (M == kFull || M == kWindow)
+      if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = AttnJoin{};
     // (the segment stays in the ring until its item is written: registers are short)
     auto find_seg = [&](int no) {
       if (no > 0 || again) attn_wait(&sh.seg_full[no & (kSegs - 1)], (no / kSegs) & 1, dead);
@@ -916,7 +1038,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     };
     auto fetch_rows = [&](const Seg& n) {
       k_scale = head_scale(n.h);
-      attn_rows_copy<D, NT>(args, n.b, n.h, n.row0, n.rows, smem + C::oQ, warp - C::wS);
+      attn_rows_copy<D, NT, M>(args, n.b, n.h, n.row0, n.rows, smem + C::oQ, warp - C::wS);
     };
     bool more = find_seg(0);
     if (again) {
@@ -928,13 +1050,18 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       if (barrier_any(4, 128 * C::NS, !more)) break;
       const Seg& e = sh.seg[seg_no & (kSegs - 1)];
       const float c_all =
-          attn_rows<D, NT>(args, sh, e.b, e.row0, e.rows, smem + C::oQ, warp - C::wS,
-                       a.scale * (k_scale * kLog2e));
+          attn_rows<D, NT, M>(args, sh, e.b, e.len, e.row0, e.rows, smem + C::oQ, warp - C::wS,
+                              a.scale * (k_scale * kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH) sh.neg_m[c0 + gt] = -kNone;
       tc::named_barrier(1 + group, 128);
       const int base = e.len - a.N, n_lo = e.row0 / a.G;
+      // window: the first position that all rows see (a tree has at most a.N levels)
+      const int hi = M != kWindow ? 0
+                                  : (a.parent != nullptr ? base + a.N - 1
+                                                         : base + (e.row0 + e.rows - 1) / a.G) -
+                                        a.window + 1;
       float2 l[C::NH / 2];
 #pragma unroll
       for (int i = 0; i < C::NH / 2; ++i) l[i] = make_float2(0.f, 0.f);
@@ -948,15 +1075,30 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
-        if (ok != 15 || (a.parent != nullptr ? (t + 1) * kTile > base
-                                             : (t + 1) * kTile - 1 > base + n_lo)) {
-          const int u = t * kTile + quarter * 32 + lane - base;
+        const int at = tile_at<M>(e, t);
+        if constexpr (M == kPrefix) {  // every row sees it
+          if (!((ok >> quarter) & 1)) vis = 0;
+        } else if (ok != 15 ||
+                   (a.parent != nullptr ? (at + 1) * kTile > base
+                                        : (at + 1) * kTile - 1 > base + n_lo) ||
+                   (M == kWindow && (at + 1) * kTile > a.sinks && at * kTile < hi)) {
+          const int j = at * kTile + quarter * 32 + lane, u = j - base;
           if (!((ok >> quarter) & 1)) {
             vis = 0;
           } else if (a.parent == nullptr) {
             // nodes rise with the rows: the first row of node u
             const int64_t from = (int64_t)u * a.G - e.row0 - c0;
             vis = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+            if (M == kWindow && j >= a.sinks) {
+              // and the first row that it lies too far before
+              const int64_t to = from + (int64_t)a.window * a.G;
+              vis &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
+            }
+          } else if (M == kWindow && u < 0) {
+            if (j >= a.sinks && j < hi)
+#pragma unroll 1
+              for (int r = 0; r < C::NH; ++r)
+                if (j < sh.row_lo[c0 + r]) vis &= ~(1u << r);
           } else if (u >= 0) {
             vis = 0;
             if (u < 64)
@@ -1090,9 +1232,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       more = find_seg(seg_no + 1);
       if (more) fetch_rows(sh.seg[(seg_no + 1) & (kSegs - 1)]);
       // ---- epilogue
-      const bool whole = e.t0 == 0 && e.t1 == e.tiles;
-      const int64_t item = (int64_t)e.b * a.N * a.Hq + e.h * a.G;  // output row of node 0
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (seg_no > 0);
+      // kPrefix, kOwn: every item is a part of its rows' outputs, its first one goes to the
+      // rows' own place, and at most one of a block (its first segment) goes on from another
+      constexpr bool PARTS = M == kPrefix || M == kOwn;
+      const bool whole = !PARTS && e.t0 == 0 && e.t1 == e.tiles;
+      const int first = M == kPrefix ? a.group_seq[e.b] : e.b;
+      const int64_t item = (int64_t)first * a.N * a.Hq + e.h * a.G;  // output row of node 0
+      const int64_t slot = PARTS ? blockIdx.x : 2 * (int64_t)blockIdx.x + (seg_no > 0);
       {
         float x[C::NH];
 #pragma unroll
@@ -1100,7 +1246,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const float sum = warp_transpose_reduce(x, [](float p, float q) { return p + q; });
         if (lane < C::NH) sh.part[quarter][c0 + lane] = sum;
       }
-      if (e.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
+      if (!PARTS && e.t0 == 0 && !whole)  // at most one: the rest of the item is the next blocks'
         if (threadIdx.x == 32 * C::wS)
           a.join[blockIdx.x] = {item, e.h, e.row0, e.rows, (int)slot, e.last};
       tc::named_barrier(1 + group, 128);
@@ -1114,6 +1260,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
           if (a.lse != nullptr && r < e.rows)
             a.lse[item + sh.row_at[r]] =
                 total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
+        } else if (PARTS && e.t0 == 0) {
+          if (r < e.rows)
+            a.row_part[item + sh.row_at[r]] = {
+                m, total,
+                (int)blockIdx.x | (e.t1 == e.tiles ? (int)blockIdx.x : e.last) << 16, r};
         } else {
           a.part_ml[slot * NT + r] = make_float2(m, total);
         }
@@ -1148,6 +1299,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
               out[(int64_t)at_[k] * D] =
                   a.bf16 ? Elem<GDN_BF16>::from(v) : Elem<GDN_F16>::from(v);
             }
+          }
+        } else if (PARTS && e.t0 == 0) {
+          float* out = a.row_o + item * D + ch;
+#pragma unroll
+          for (int i = 0; i < C::NH; ++i) {
+            if (i >= rows) break;
+            out[(int64_t)sh.row_at[c0 + i] * D] = __uint_as_float(o[i / 16][i % 16]);
           }
         } else {
           float* out = a.part_o + (slot * NT + c0) * D + ch;
@@ -1261,17 +1419,21 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       } else if (!next_seg()) {
         break;
       }
-      const int32_t* table = a.c.table + (int64_t)s.b * a.c.table_stride;
+      const int row = M == kPrefix ? a.group_row[s.b] : s.b;
+      const int32_t* table = a.c.table + (int64_t)row * a.c.table_stride;
       const uint8_t* head = static_cast<const uint8_t*>(a.c.pages) + from +
                             (int64_t)s.h * (a.c.page_tokens / kRec) * rec_bytes(D);
       // this lane's position, as an entry of the table and an offset in the page, two
       // tiles ahead of the copies: the page numbers are looked up that early
-      int pos = s.t0 * kTile + r * kRec;
+      int pos = tile_at<M>(s, s.t0) * kTile + r * kRec;
       int entry = pos / a.c.page_tokens, off = pos % a.c.page_tokens;
       const int entries = kTile / a.c.page_tokens, rest = kTile % a.c.page_tokens;
       int page[3], offs[3];
       auto look_up = [&](int i, int t) {
-        page[i] = lane < lanes && t < s.t1 && t * kTile + r * kRec < s.len ? table[entry] : -1;
+        const int at = tile_at<M>(s, t) * kTile + r * kRec;
+        if (M == kWindow && t == s.near && t > s.t0)  // the window's first tile
+          entry = at / a.c.page_tokens, off = at % a.c.page_tokens;
+        page[i] = lane < lanes && t < s.t1 && at < s.len ? table[entry] : -1;
         offs[i] = off;
         entry += entries;
         off += rest;
@@ -1281,7 +1443,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       look_up(1, s.t0 + 1);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        const bool want = lane < lanes && pos < s.len;  // past the end: nothing to read
+        if (M == kWindow && t == s.near && t > s.t0) pos += s.skip * kTile;
+        const bool past = lane >= lanes || pos >= s.len;  // the end: nothing to read
+        // (of a window's outer tiles, the records that some row sees)
+        const bool want = !past && (M != kWindow || pos < a.sinks || pos + kRec > s.lo);
         look_up(2, t + 2);
         const bool have = want && page[0] >= 0 && page[0] < a.c.n_pages;
         if (want && !have) report(a.c.status, GDN_ERR_PAGE_RANGE);
@@ -1290,7 +1455,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
           src += (int64_t)page[0] * a.c.page_stride + offs[0] / kRec * rec_bytes(D);
         pos += kTile;
         page[0] = page[1], offs[0] = offs[1], page[1] = page[2], offs[1] = offs[2];
-        const unsigned good = __ballot_sync(0xffffffffu, have || !want);
+        const unsigned good = __ballot_sync(0xffffffffu, have || past);
         const unsigned tx = __popc(__ballot_sync(0xffffffffu, have) & 0x55u) * C::HALF;
         const int ok = (good & 1) | ((good >> 1) & 2) | ((good >> 2) & 4) | ((good >> 3) & 8);
         if (do_k) {
@@ -1431,16 +1596,16 @@ join_kernel(const __grid_constant__ AttnArgs a, int NT) {
     a.lse[out] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, int NT>
+template <int D, int NT, Mode M>
 int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
   using C = AttnCfg<D, NT>;
-  if (cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(attn_kernel<D, NT, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::SMEM) != cudaSuccess) {
     (void)cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  const int rc = launch_pdl(attn_kernel<D, NT>, dim3(parts), dim3(C::THREADS), C::SMEM, s, a);
-  if (rc != GDN_OK) return rc;
+  const int rc = launch_pdl(attn_kernel<D, NT, M>, dim3(parts), dim3(C::THREADS), C::SMEM, s, a);
+  if (rc != GDN_OK || M == kPrefix || M == kOwn) return rc;  // (joined by shared_join_kernel)
   const dim3 block(kJoinThreads);
   if (NT == 16)
     return launch_pdl(join_kernel<D, true>, dim3(parts, a.rows_per_tile), block, 0, s, a, NT);
@@ -1449,13 +1614,13 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
                     s, a, NT);
 }
 
-template <int D>
+template <int D, Mode M>
 int attn_launch_d(const AttnArgs& a, int NT, int parts, cudaStream_t s) {
   switch (NT) {
-    case 16: return attn_launch_nt<D, 16>(a, parts, s);
-    case 32: return attn_launch_nt<D, 32>(a, parts, s);
-    case 64: return attn_launch_nt<D, 64>(a, parts, s);
-    default: return attn_launch_nt<D, 96>(a, parts, s);
+    case 16: return attn_launch_nt<D, 16, M>(a, parts, s);
+    case 32: return attn_launch_nt<D, 32, M>(a, parts, s);
+    case 64: return attn_launch_nt<D, 64, M>(a, parts, s);
+    default: return attn_launch_nt<D, 96, M>(a, parts, s);
   }
 }
 

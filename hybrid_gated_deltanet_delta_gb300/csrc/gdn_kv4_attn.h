@@ -16,6 +16,22 @@ struct AttnJoin {
   int slot, last;        // of its own part; block with the last part
 };
 
+// What a query row sees of its sequence, and where its result goes.
+enum Mode {
+  kFull,    // all that its node sees; the output
+  kWindow,  // the first `sinks` and the last `window` entries of its node's path; the output
+  kPrefix,  // the part that the sequences of a group share, their rows one after another (the
+            // cache's lengths are the shared ones); a part of the output
+  kOwn      // what lies behind that part; a part of the output
+};
+
+// The first part of a query row's output that a kPrefix or kOwn pass leaves: reference and sum,
+// the item's first block and its last one (16 bits each), and the row's place in its tile.
+struct RowPart {
+  float m, l;
+  int blocks, row;
+};
+
 struct AttnArgs {
   gdn_kv4_cache c;
   const void* q;
@@ -30,11 +46,50 @@ struct AttnArgs {
   int N, Hq, G;     // G: query heads of a kv head
   int rows_total, rows_per_tile, row_tiles;
   int bf16;
+  int window, sinks;         // kWindow
+  const int32_t* extra;      // kPrefix: sequences of a group; kOwn: first own tile (-1: skipped)
+  const int32_t* group_seq;  // kPrefix: a group's first sequence,
+  const int32_t* group_row;  // and the table row that its shared pages are taken from
+  float* row_o;              // kPrefix, kOwn: [B*N*Hq][D], each row's first part
+  RowPart* row_part;         // [B*N*Hq]
 };
 
 int attn_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 int attn_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 int attn_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int window_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int window_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int window_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int prefix_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int prefix_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int prefix_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int own_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int own_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int own_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+
+// Query rows of a tile.  K and V are brought in and dequantised once per row tile, so
+// wide ones pay: with tiles of at most 64 rows a 2048-token piece of a prompt takes 431 us,
+// eight chains of 16 (96 rows) 79.8 us and a tree of 22 (132 rows, three tiles of 44)
+// 42.8 us, with 96 367, 64.0 and 40.7 us (in turn on one box).  Rows are spread evenly over
+// the tiles.  More than 96 do not fit tensor memory beside two units of K and V (D = 256).
+constexpr int kMaxRows = 96;
+inline int round_rows(int rows) {
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kMaxRows;
+}
+inline void row_tiles(int rows, int* tiles, int* per_tile) {
+  *tiles = (rows + kMaxRows - 1) / kMaxRows;
+  *per_tile = (rows + *tiles - 1) / *tiles;
+}
 
 }  // namespace kv4
+
+// gdn_kv4_shared.cu.  plan: of each group the shared length, its sequences, the first of them
+// and the table row that holds the shared pages (n_groups each); start: of each sequence its
+// first own tile.
+int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
+                           const int32_t* group, int n_groups, int32_t* plan, int32_t* start,
+                           cudaStream_t s);
+int launch_kv4_shared_join(const kv4::AttnArgs& own, const kv4::AttnArgs& pre, int own_rows,
+                           int pre_rows, int blocks, cudaStream_t s);
+
 }  // namespace gdn

@@ -4,7 +4,7 @@ namespace gdn {
 namespace kv4 {
 
 int attn_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s) {
-  return attn_launch_d<256>(a, NT, parts, s);
+  return attn_launch_d<256, kFull>(a, NT, parts, s);
 }
 
 }  // namespace kv4

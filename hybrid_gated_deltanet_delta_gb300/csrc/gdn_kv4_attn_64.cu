@@ -4,7 +4,7 @@ namespace gdn {
 namespace kv4 {
 
 int attn_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s) {
-  return attn_launch_d<64>(a, NT, parts, s);
+  return attn_launch_d<64, kFull>(a, NT, parts, s);
 }
 
 }  // namespace kv4

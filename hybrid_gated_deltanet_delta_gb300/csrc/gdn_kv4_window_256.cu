@@ -1,0 +1,11 @@
+#include "gdn_kv4_attn.cuh"
+
+namespace gdn {
+namespace kv4 {
+
+int window_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s) {
+  return attn_launch_d<256, kWindow>(a, NT, parts, s);
+}
+
+}  // namespace kv4
+}  // namespace gdn

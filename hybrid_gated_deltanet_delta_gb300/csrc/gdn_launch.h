@@ -53,8 +53,8 @@ int launch_prefill_noalloc(const void* q, const void* k, const void* v, bool bf1
                            int dv, int chunk, float* state, float* o, int32_t* status,
                            cudaStream_t stream);
 
-// The 4-bit key/value cache (gdn_kv4_cache.cu), its attention (gdn_kv4_attn.cu)
-// and its page pool (gdn_kv4_pool.cu).
+// The 4-bit key/value cache (gdn_kv4_cache.cu, gdn_kv4_rotary.cu), its attention
+// (gdn_kv4_attn.cu) and its page pool (gdn_kv4_pool.cu).
 int launch_kv4_append(const gdn_kv4_cache& c, const void* k, const void* v, int dtype,
                       int64_t ksb, int64_t ksn, int64_t vsb, int64_t vsn, int N, cudaStream_t s);
 int launch_kv4_read(const gdn_kv4_cache& c, void* k, void* v, int dtype, int N, cudaStream_t s);
@@ -62,6 +62,19 @@ size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
                          int64_t qsn, int N, int Hq, float scale, const int32_t* parent, void* o,
                          float* lse, void* workspace, cudaStream_t s);
+int launch_kv4_append_rotary(const gdn_kv4_cache& c, const gdn_rotary& r, const void* q, int64_t qsb,
+                             int64_t qsn, int Hq, void* q_out, int64_t osb, int64_t osn,
+                             const void* k, const void* v, int dtype, int64_t ksb, int64_t ksn,
+                             int64_t vsb, int64_t vsn, int N, cudaStream_t s);
+int launch_kv4_attention_window(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
+                                int64_t qsn, int N, int Hq, float scale, int sinks, int window,
+                                const int32_t* parent, void* o, float* lse, void* workspace,
+                                cudaStream_t s);
+size_t kv4_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int n_groups);
+int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
+                                int64_t qsn, int N, int Hq, float scale, const int32_t* parent,
+                                const int32_t* group, int n_groups, void* o, float* lse,
+                                void* workspace, cudaStream_t s);
 int launch_kv4_commit(const gdn_kv4_cache& c, int64_t layer_stride, int n_layers, int N,
                       const int32_t* parent, const int32_t* accept, int32_t* len_out,
                       cudaStream_t s);

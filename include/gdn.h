@@ -84,7 +84,9 @@ typedef enum gdn_status {
   GDN_ERR_POOL_EMPTY = -12,   /* device: fewer free pages than a row needs */
   GDN_ERR_ROW_RANGE = -13,    /* device: a row outside the table, a length below 0 or beyond the
                                  table's width, or a branch onto a row that is not empty */
-  GDN_ERR_NONFINITE = -14     /* device: a NaN or infinity was given to the 4-bit cache */
+  GDN_ERR_NONFINITE = -14,    /* device: a NaN or infinity was given to the 4-bit cache */
+  GDN_ERR_POSITION_RANGE = -15 /* device: a rotary position outside the table of angles, or a
+                                 pair's axis outside the axes given */
 } gdn_status;
 
 /* GDN_F16 (IEEE binary16) is taken by the gdn_kv4_* calls only. */
@@ -462,6 +464,53 @@ int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t
                    int64_t v_stride_n, int32_t N, void* stream);
 
 /*
+ * Append with rotary positions: the queries q [B][N][Hq][D] and the keys of the block are turned
+ * by their positions on one or several axes (text: one; images and video: time, height and
+ * width), the queries are written to q_out, and keys and values appended as gdn_kv4_append does.
+ *
+ *   pairs        rotated pairs of a head: a multiple of 8, at most D/2; channels from 2*pairs on
+ *                pass as they are
+ *   adjacent     0: pair i is channels i and pairs + i; 1: channels 2i and 2i + 1
+ *   cos_sin      [n_positions][2][pairs] fp32: the cosines, then the sines of a position (so the
+ *                frequencies and their scaling are the caller's, in any precision)
+ *   positions    position of node n of sequence b on axis a at
+ *                positions[a*pos_stride_axis + b*pos_stride_b + n]
+ *   axis         [pairs] bytes: the axis that a pair goes by (sections one after another,
+ *                interleaved, or any other order); NULL: all go by axis 0
+ *
+ * A pair (i, j) with the cosine c and sine s of its axis' position becomes
+ *     y_i = x_i c - x_j s,   y_j = x_j c + x_i s
+ * in fp32, each product and the sum rounded to nearest even, nothing fused; q_out is y rounded
+ * once to dtype, and the cache takes the keys' y unrounded.  So the stored codes and q_out are
+ * fixed to the operation.
+ *
+ * q_out [B][N][Hq][D] is either q itself (with q's strides: the queries are turned in place, and
+ * channels that pass are not touched) or overlaps none of q, k and v.  q, k, v and q_out share a
+ * dtype (GDN_F32, GDN_BF16 or GDN_F16); strides in elements, multiples of 16 bytes.  Nodes that
+ * do not exist give q_out = 0, and their positions are not looked at.  A position outside
+ * [0, n_positions), or a pair's axis outside [0, n_axes), leaves the node's pairs on that axis
+ * as they are, and GDN_ERR_POSITION_RANGE is reported.  A NaN or infinity in a key is treated as
+ * gdn_kv4_append treats what the rotation makes of it.  Hq is a multiple of Hkv, at most 65535.
+ */
+typedef struct gdn_rotary {
+  const float* cos_sin;
+  const int32_t* positions;
+  const uint8_t* axis;
+  int64_t pos_stride_axis;
+  int64_t pos_stride_b;
+  int32_t n_positions;
+  int32_t n_axes;
+  int32_t pairs;
+  int32_t adjacent;
+} gdn_rotary;
+
+int gdn_kv4_append_rotary(const gdn_kv4_cache* c, const gdn_rotary* r, const void* q,
+                          int64_t q_stride_b, int64_t q_stride_n, int32_t Hq, void* q_out,
+                          int64_t out_stride_b, int64_t out_stride_n, const void* k, const void* v,
+                          int32_t dtype, int64_t k_stride_b, int64_t k_stride_n,
+                          int64_t v_stride_b, int64_t v_stride_n, int32_t N, void* stream);
+
+/*
  * Read back: the stored values of positions kv_len[b] - N .. kv_len[b] - 1 into
  * k_out and v_out [B][N][Hkv][D] (contiguous; rounded once to dtype).
  */
@@ -504,6 +553,54 @@ int gdn_kv4_attention(const gdn_kv4_cache* c, const void* q, int32_t dtype, int6
                       int64_t q_stride_n, int32_t N, int32_t Hq, float scale,
                       const int32_t* parent, void* o, float* lse, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_kv4_attention through a sliding window that leaves the first tokens visible.  Of the
+ * entries of its path (the positions before the block, then the block's nodes up to it or its
+ * ancestors, and itself: the i-th ancestor from the root is entry kv_len[b] - N + i), a node
+ * that is entry e sees the entries f with
+ *     f > e - window   or   f < sinks,
+ * so its own window's last entry is itself.  window >= 1, sinks >= 0; a window as long as the
+ * sequence gives gdn_kv4_attention's result.  In a tree the window runs along each node's own
+ * path.  Only tiles that some row sees are read.  Everything else, the workspace and its size
+ * (gdn_kv4_attention_workspace_bytes) among it, is as for gdn_kv4_attention.
+ */
+int gdn_kv4_attention_window(const gdn_kv4_cache* c, const void* q, int32_t dtype,
+                             int64_t q_stride_b, int64_t q_stride_n, int32_t N, int32_t Hq,
+                             float scale, int32_t sinks, int32_t window, const int32_t* parent,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * gdn_kv4_attention for sequences that share pages (branches of a prompt, gdn_kv4_fork): what
+ * the sequences of a group have in common is read, and multiplied, once for all of them.
+ *
+ *   group  [n_groups + 1] int32, device: group g is sequences group[g] .. group[g+1] - 1 of the
+ *          batch (so branches of one prompt stand beside each other); 1 <= n_groups <= B.
+ *          Sequences before group[0] and from group[n_groups] on share with nobody
+ *
+ * How much a group shares follows from the table: the positions before the blocks that lie on
+ * the same pages, from the first position on and in whole tiles of 128, in all sequences of the
+ * group that share a tile with the first of it.  A group that shares nothing is right as well,
+ * and a sequence that is skipped does not count.  Offsets that are not ascending within [0, B]
+ * are reported (GDN_ERR_ROW_RANGE), and nothing is shared then; where a sequence's rows fill the
+ * tensor cores' tiles by themselves, sharing saves nothing and the offsets are not looked at.
+ *
+ * The result is gdn_kv4_attention's up to the order of the sums, which depends on the lengths,
+ * the table, the groups and the device alone.  The workspace
+ * (gdn_kv4_attention_shared_workspace_bytes; 0 for sizes that the call refuses) grows with B*N*Hq;
+ * two calls that may overlap (two streams, two captured graphs) need one each.
+ * GDN_ERR_UNSUPPORTED also when B * N * Hq does not fit 31 bits.  Everything else is as for
+ * gdn_kv4_attention.
+ */
+size_t gdn_kv4_attention_shared_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                                                int32_t D, int32_t n_groups);
+
+int gdn_kv4_attention_shared(const gdn_kv4_cache* c, const void* q, int32_t dtype,
+                             int64_t q_stride_b, int64_t q_stride_n, int32_t N, int32_t Hq,
+                             float scale, const int32_t* parent, const int32_t* group,
+                             int32_t n_groups, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /*
  * Commit the accepted path of a block, for n_layers layers at once (layer l's
