@@ -1,6 +1,5 @@
-// Append to the 4-bit key/value cache: quantise a record's tokens on write (include/gdn.h),
-// with the keys as they are (gdn_kv4_cache.cu) or turned by their positions first
-// (gdn_kv4_rotary.cu).
+// Append to the 4-bit key/value cache: quantise a record's tokens on write (include/gdn.h), the
+// keys as they are (gdn_kv4_cache.cu) or turned by their positions first (gdn_kv4_rotary.cu).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -14,18 +13,6 @@ constexpr int kThreads = 256;
 // Records that N tokens can touch, whatever the offset of the first.
 inline int touched(int N) { return (int)(((int64_t)N + kRec - 2) / kRec + 1); }
 
-// Grid (records a block can touch, Hkv, B).  A thread quantises 16 channels of
-// two neighbouring tokens, the two that share the bytes of V codes.  K codes are 8
-// contiguous bytes a token and go straight to the record; V codes are staged as
-// bytes ([token pair][channel]) in shared memory and gathered by the thread that
-// owns the channel, 16 bytes of 32 tokens, merged with the record's old bytes where
-// the block covers only part of it.  Bound by the instructions on each value and
-// the latency of a block's length, page and values: 8,192 tokens of 4 heads of 256
-// channels (43 MB) were 30 us with a token a thread and a byte a code in shared
-// memory, 17.7 us with every value clamped and checked by itself, and are 14.8 us
-// this way.  Four blocks an SM (64 registers): with three 18.0 us, with five 16.9.
-// Whole 32-byte sectors a store, by exchanges between lanes, gave 14.7 us and were
-// left out.
 struct Codes {
   uint32_t w[2];  // 16 codes
   uint32_t scale;
@@ -75,98 +62,89 @@ __device__ __forceinline__ uint2 pair_bytes(uint32_t a, uint32_t b) {
   return make_uint2(__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362));
 }
 
-// Keys that are stored as they are given.
-struct NoTurn {
-  template <int DT, typename T>
-  __device__ __forceinline__ void apply(float (&)[8], const T*, int, int) const {}
+// What a block of threads appends to: the `part`-th record that the block of N tokens of
+// sequence b touches, of head h.
+struct Place {
+  uint8_t* rec;  // NULL: the page is not there
+  int base, t0;  // positions of node 0 and of the record's first token
+  int lo, hi;    // the record's tokens that are the block's; none where it touches fewer records
 };
 
-// One thread block's record: the `part`-th that the block of N tokens of sequence b touches, of
-// head h.  `make` is given what the record holds of the block and returns what turns the keys,
-// 8 channels of a token at a time.
-template <int DT, int D, typename Turn, typename Make>
-__device__ __forceinline__ void append_record(const gdn_kv4_cache& c, const void* __restrict__ kin,
-                                              const void* __restrict__ vin, int64_t ksb,
-                                              int64_t ksn, int64_t vsb, int64_t vsn, int N, int b,
-                                              int h, int part, Make make) {
-  constexpr int G = D / 16;  // scale groups
-  using T = typename Elem<DT>::T;
-  __shared__ __align__(16) uint8_t code[kRec / 2][D];
+__device__ __forceinline__ Place find_place(const gdn_kv4_cache& c, int N, int b, int h, int part) {
+  Place p = {};
   const int len = seq_len(c, b, part == 0 && h == 0 && threadIdx.x == 0);
-  const int base = len - N;
-  const int t0 = ((base > 0 ? base : 0) / kRec + part) * kRec;  // first token here
-  if (t0 >= len) return;
-  const int lo = base > t0 ? base - t0 : 0, hi = len - t0 < kRec ? len - t0 : kRec;
-  uint8_t* rec = record(c, b, h, t0);
-  if (rec == nullptr) {
-    if (threadIdx.x == 0) report(c.status, GDN_ERR_PAGE_RANGE);
-    return;
+  p.base = len - N;
+  p.t0 = ((p.base > 0 ? p.base : 0) / kRec + part) * kRec;
+  if (p.t0 >= len) return p;
+  p.lo = p.base > p.t0 ? p.base - p.t0 : 0, p.hi = len - p.t0 < kRec ? len - p.t0 : kRec;
+  p.rec = record(c, b, h, p.t0);
+  return p;
+}
+
+// Quantises channels 16*g .. of a pair of tokens; `load(slot, x)` brings in one token's.  K goes
+// to the record, V's codes to `code`.
+template <int D, typename Load>
+__device__ __forceinline__ void quantise_pair(const Place& p, bool is_v, float inv, int pair, int g,
+                                              uint8_t (*code)[D], bool& bad, Load load) {
+  constexpr int G = D / 16;  // scale groups
+  float x[2][2][8];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int slot = 2 * pair + t;
+    if (slot >= p.lo && slot < p.hi) {
+      load(slot, x[t]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[t][j >> 3][j & 7] = 0.f;
+    }
   }
-  const float inv_k = c.k_scale != nullptr ? 1.0f / c.k_scale[h] : 1.0f;
-  const float inv_v = c.v_scale != nullptr ? 1.0f / c.v_scale[h] : 1.0f;
-  const Turn turn = make(b, t0, base, lo, hi);
-  const int pair0 = lo >> 1, pairs = ((hi + 1) >> 1) - pair0;
-  bool bad = false;
-  for (int i = threadIdx.x; i < 2 * pairs * G; i += kThreads) {
-    const bool is_v = i >= pairs * G;
-    const int u = is_v ? i - pairs * G : i, pair = pair0 + u / G, g = u % G;
-    const T* src = is_v ? static_cast<const T*>(vin) + b * vsb : static_cast<const T*>(kin) + b * ksb;
-    const int64_t step = is_v ? vsn : ksn;
-    float x[2][2][8];
+  Codes q[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int slot = 2 * pair + t;
-      if (slot >= lo && slot < hi) {
-        const T* p = src + (int64_t)(t0 + slot - base) * step + (int64_t)h * D + g * 16;
-        load8<DT>(p, x[t][0]);
-        load8<DT>(p + 8, x[t][1]);
-        if (!is_v) {
-          turn.template apply<DT>(x[t][0], p, slot, 2 * g);
-          turn.template apply<DT>(x[t][1], p + 8, slot, 2 * g + 1);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[t][j >> 3][j & 7] = 0.f;
-      }
-    }
-    Codes q[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      q[t] = quantise(x[t], is_v ? inv_v : inv_k, bad);
-      const int slot = 2 * pair + t;
-      if (slot < lo || slot >= hi) continue;
-      if (is_v) {
-        rec[off_vs(D) + g * kRec + slot] = (uint8_t)q[t].scale;
-      } else {
-        *reinterpret_cast<uint2*>(rec + (g >> 1) * 512 + slot * 16 + (g & 1) * 8) =
-            make_uint2(q[t].w[0], q[t].w[1]);
-        rec[off_ks(D) + slot * G + g] = (uint8_t)q[t].scale;
-      }
-    }
+  for (int t = 0; t < 2; ++t) {
+    q[t] = quantise(x[t], inv, bad);
+    const int slot = 2 * pair + t;
+    if (slot < p.lo || slot >= p.hi) continue;
     if (is_v) {
-      const uint2 first = pair_bytes(q[0].w[0], q[1].w[0]), second = pair_bytes(q[0].w[1], q[1].w[1]);
-      *reinterpret_cast<uint4*>(&code[pair][g * 16]) =
-          make_uint4(first.x, first.y, second.x, second.y);
+      p.rec[off_vs(D) + g * kRec + slot] = (uint8_t)q[t].scale;
+    } else {
+      *reinterpret_cast<uint2*>(p.rec + (g >> 1) * 512 + slot * 16 + (g & 1) * 8) =
+          make_uint2(q[t].w[0], q[t].w[1]);
+      p.rec[off_ks(D) + slot * G + g] = (uint8_t)q[t].scale;
     }
   }
-  if (bad) report(c.status, GDN_ERR_NONFINITE);
-  __syncthreads();
+  if (is_v) {
+    const uint2 first = pair_bytes(q[0].w[0], q[1].w[0]), second = pair_bytes(q[0].w[1], q[1].w[1]);
+    *reinterpret_cast<uint4*>(&code[pair][g * 16]) =
+        make_uint4(first.x, first.y, second.x, second.y);
+  }
+}
+
+// What a channel's 16 bytes of V codes hold, where the block covers only part of them.
+template <int D>
+__device__ __forceinline__ uint4 old_v(const Place& p, int ch) {
+  return p.lo != 0 || p.hi != kRec ? *reinterpret_cast<const uint4*>(p.rec + off_v(D) + ch * 16)
+                                   : make_uint4(0, 0, 0, 0);
+}
+
+// V's codes to the record, after a barrier; `old(ch)`: what is there.
+template <int D, typename Old>
+__device__ __forceinline__ void store_v(const Place& p, const uint8_t (*code)[D], Old old_of) {
   // nibbles of the block in each word of 8 tokens
   uint32_t mine[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const int from = min(max(lo - 8 * w, 0), 8), to = min(max(hi - 8 * w, 0), 8);
+    const int from = min(max(p.lo - 8 * w, 0), 8), to = min(max(p.hi - 8 * w, 0), 8);
     mine[w] = (uint32_t)(((1ull << (4 * to)) - 1) & ~((1ull << (4 * from)) - 1));
   }
   for (int ch = threadIdx.x; ch < D; ch += kThreads) {
-    uint4* at = reinterpret_cast<uint4*>(rec + off_v(D) + ch * 16);
+    uint4* at = reinterpret_cast<uint4*>(p.rec + off_v(D) + ch * 16);
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       w[k] = (code[4 * k][ch] | (uint32_t)code[4 * k + 1][ch] << 8 |
               (uint32_t)code[4 * k + 2][ch] << 16 | (uint32_t)code[4 * k + 3][ch] << 24) & mine[k];
-    if (lo != 0 || hi != kRec) {
-      const uint4 old = *at;
+    if (p.lo != 0 || p.hi != kRec) {
+      const uint4 old = old_of(ch);
       w[0] |= old.x & ~mine[0], w[1] |= old.y & ~mine[1];
       w[2] |= old.z & ~mine[2], w[3] |= old.w & ~mine[3];
     }
