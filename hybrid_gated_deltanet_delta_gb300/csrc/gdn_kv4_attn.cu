@@ -29,6 +29,10 @@ AttnArgs attn_args(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb
   a.rows_total = N * a.G;
   row_tiles(a.rows_total, &a.row_tiles, &a.rows_per_tile);
   a.bf16 = dtype == GDN_BF16;
+  a.by_G = kv4::Divisor(a.G);
+  a.by_N = kv4::Divisor(N);
+  a.by_Hkv = kv4::Divisor(c.Hkv);
+  a.by_page = kv4::Divisor(c.page_tokens);
   return a;
 }
 
@@ -96,21 +100,18 @@ int launch_kv4_attention_window(const gdn_kv4_cache& c, const void* q, int dtype
 // ---------------------------------------------------------------- shared prompts
 namespace {
 
-// Workspace of a call that reads shared pages once: the plan's numbers, each row's first part
-// of both passes, and the parts that go on from another block.
+// Workspace of a call that reads shared pages once: the plan's numbers, each row's first own and
+// first shared part, and the parts that go on from another block.
 struct SharedSpace {
-  int32_t* plan;
-  float *row_o[2], *part_o[2];
+  SharedPlan plan;
+  float *row_o[2], *part_o;
   kv4::RowPart* row_part[2];
-  float2* part_ml[2];
+  float2* part_ml;
   size_t bytes;
 };
 
-SharedSpace shared_space(void* base, int B, int N, int Hq, int Hkv, int D, int n_groups, int sms) {
-  int tiles, per_tile;
-  row_tiles(N * (Hq / Hkv), &tiles, &per_tile);
+SharedSpace shared_space(void* base, int B, int N, int Hq, int D, int n_groups, int sms) {
   const size_t rows = (size_t)B * N * Hq;
-  const int NT[2] = {kv4::kMaxRows, round_rows(per_tile)};
   SharedSpace w = {};
   uint8_t* at = static_cast<uint8_t*>(base);
   auto take = [&](size_t bytes) {
@@ -118,13 +119,16 @@ SharedSpace shared_space(void* base, int B, int N, int Hq, int Hkv, int D, int n
     w.bytes += (bytes + 255) / 256 * 256;
     return p;
   };
-  w.plan = reinterpret_cast<int32_t*>(take(4 * (size_t)(4 * (int64_t)n_groups + B)));
+  auto ints = [&](size_t n) { return reinterpret_cast<int32_t*>(take(4 * n)); };
+  const size_t groups = n_groups, all = groups + B;
+  w.plan.len = ints(all), w.plan.extra = ints(all);
+  w.plan.group_seq = ints(groups), w.plan.group_row = ints(groups);
   for (int i = 0; i < 2; ++i) {
     w.row_o[i] = reinterpret_cast<float*>(take(rows * D * 4));
     w.row_part[i] = reinterpret_cast<kv4::RowPart*>(take(rows * sizeof(kv4::RowPart)));
-    w.part_o[i] = reinterpret_cast<float*>(take((size_t)sms * NT[i] * D * 4));
-    w.part_ml[i] = reinterpret_cast<float2*>(take((size_t)sms * NT[i] * 8));
   }
+  w.part_o = reinterpret_cast<float*>(take((size_t)sms * kv4::kMaxRows * D * 4));
+  w.part_ml = reinterpret_cast<float2*>(take((size_t)sms * kv4::kMaxRows * 8));
   return w;
 }
 
@@ -142,8 +146,7 @@ size_t kv4_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv, int D
   const size_t alone = kv4_attention_workspace_bytes(B, N, Hq, Hkv, D);
   if (!rows_worth_sharing(N, Hq / Hkv)) return alone;
   const int sms = sm_count();
-  const size_t shared =
-      shared_space(nullptr, B, N, Hq, Hkv, D, n_groups, sms > 0 ? sms : 256).bytes;
+  const size_t shared = shared_space(nullptr, B, N, Hq, D, n_groups, sms > 0 ? sms : 256).bytes;
   return shared > alone ? shared : alone;
 }
 
@@ -153,54 +156,37 @@ int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype
                                 void* workspace, cudaStream_t s) {
   const int parts = sm_count();
   if (parts == 0) return GDN_ERR_CUDA;
-  AttnArgs own = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
-  if (!countable(c, (int64_t)own.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
-  if (!rows_worth_sharing(N, own.G))
+  AttnArgs a = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
+  if (!countable(c, (int64_t)a.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
+  if (!rows_worth_sharing(N, a.G))
     return launch_kv4_attention(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse, workspace, s);
   // the rows of a group as if they were one sequence's, in tiles as wide as a group of the
   // usual size fills
-  AttnArgs pre = own;
-  const int64_t most = (int64_t)c.B * own.rows_total;
-  const int64_t usual = (int64_t)((c.B + n_groups - 1) / n_groups) * own.rows_total;
+  const int64_t usual = (int64_t)((c.B + n_groups - 1) / n_groups) * a.rows_total;
   int tiles, per_tile;
-  row_tiles((int)(usual < most ? usual : most), &tiles, &per_tile);
+  row_tiles((int)usual, &tiles, &per_tile);
   const int NT = round_rows(per_tile);
-  pre.rows_per_tile = NT;
-  pre.row_tiles = (int)((most + NT - 1) / NT);
-  if (!countable(c, (int64_t)pre.row_tiles + n_groups)) return GDN_ERR_UNSUPPORTED;
-  const SharedSpace w =
-      shared_space(workspace, c.B, N, Hq, c.Hkv, c.D, n_groups, parts);
-  int32_t* start = w.plan + 4 * (int64_t)n_groups;
-  int rc = launch_kv4_shared_plan(c, N, parent, group, n_groups, w.plan, start, s);
+  // (items of the groups: their rows are the batch's; units of work are up to ten a tile)
+  const int64_t items = (int64_t)c.B * a.rows_total / NT + n_groups + (int64_t)a.row_tiles * c.B;
+  if (!countable(c, 10 * items)) return GDN_ERR_UNSUPPORTED;
+  const SharedSpace w = shared_space(workspace, c.B, N, Hq, c.D, n_groups, parts);
+  int rc = launch_kv4_shared_plan(c, N, parent, group, n_groups, w.plan, s);
   if (rc != GDN_OK) return rc;
-  pre.parent = nullptr;
-  pre.c.B = n_groups;
-  pre.c.kv_len = w.plan;
-  pre.extra = w.plan + n_groups;
-  pre.group_seq = w.plan + 2 * (int64_t)n_groups;
-  pre.group_row = w.plan + 3 * (int64_t)n_groups;
-  own.extra = start;
-  for (int i = 0; i < 2; ++i) {
-    AttnArgs& a = i == 0 ? pre : own;
-    a.row_o = w.row_o[i];
-    a.row_part = w.row_part[i];
-    a.part_o = w.part_o[i];
-    a.part_ml = w.part_ml[i];
-  }
-  const int NTo = round_rows(own.rows_per_tile);
+  a.n_groups = n_groups;
+  a.plan_len = w.plan.len;
+  a.plan_extra = w.plan.extra;
+  a.group_seq = w.plan.group_seq;
+  a.group_row = w.plan.group_row;
+  for (int i = 0; i < 2; ++i) a.row_o[i] = w.row_o[i], a.row_part[i] = w.row_part[i];
+  a.part_o = w.part_o;
+  a.part_ml = w.part_ml;
   switch (c.D) {
-    case 64: rc = kv4::prefix_launch_64(pre, NT, parts, s); break;
-    case 128: rc = kv4::prefix_launch_128(pre, NT, parts, s); break;
-    default: rc = kv4::prefix_launch_256(pre, NT, parts, s);
+    case 64: rc = kv4::shared_launch_64(a, NT, parts, s); break;
+    case 128: rc = kv4::shared_launch_128(a, NT, parts, s); break;
+    default: rc = kv4::shared_launch_256(a, NT, parts, s);
   }
   if (rc != GDN_OK) return rc;
-  switch (c.D) {
-    case 64: rc = kv4::own_launch_64(own, NTo, parts, s); break;
-    case 128: rc = kv4::own_launch_128(own, NTo, parts, s); break;
-    default: rc = kv4::own_launch_256(own, NTo, parts, s);
-  }
-  if (rc != GDN_OK) return rc;
-  return launch_kv4_shared_join(own, pre, NTo, NT, parts, s);
+  return launch_kv4_shared_join(a, NT, parts, s);
 }
 
 }  // namespace gdn

@@ -124,7 +124,8 @@ struct Seg {
   int b, h, t0, t1, tiles, len, row0, rows;
   int last;  // block that holds the item's last tile
   int near, skip;
-  int lo;    // window: first position that the item's first node sees beside the sinks
+  int lo;     // window: first position that the item's first node sees beside the sinks
+  int group;  // shared: the rows are those of a group's sequences, b the group
 };
 
 // The tiles of an item.
@@ -136,7 +137,7 @@ struct Span {
 template <Mode M>
 __device__ __forceinline__ int tile_at(const Seg& s, int t) {
   if constexpr (M == kWindow) return t + (t >= s.near ? s.skip : 0);
-  if constexpr (M == kOwn) return t + s.skip;
+  if constexpr (M == kShared) return t + s.skip;
   return t;
 }
 
@@ -148,21 +149,35 @@ __device__ __forceinline__ int tile_at(const Seg& s, int t) {
 // 68.9 us, a tree of 22 nodes 45.7, 44.7, 45.2 and 44.3 us.
 constexpr int kLead = 6;
 
+// Shared: tiles of an item of few rows and of one of many stand in one run, so units are finer
+// there: a tile counts 4 and 2 for each of the softmax groups with rows of the item, and what
+// goes with an item kSharedLead and kSharedMore for each of them.
+constexpr int kSharedLead = 40, kSharedMore = 6, kMostWeight = 10;
+template <int NT>
+__device__ __forceinline__ int row_groups(int rows) {
+  return NT < 64 ? 1 : (min(rows, NT) + 31) / 32;
+}
+
+// One copy of a division's instructions.
+static __device__ __noinline__ int quotient(int n, int d) { return (uint32_t)n / (uint32_t)d; }
+
 // Equal runs of `total` units for at most `parts` blocks: the first `extra` runs
 // have one unit more.  (The host keeps the count below 2^31.)
 struct Runs {
   int each, extra, parts;
   Runs() = default;
-  __device__ __forceinline__ Runs(int total, int n) {
-    parts = min(total, n);  // no empty runs in between
-    each = parts > 0 ? total / parts : 0;
+  // `least`: units that a run has at least (with as many in a tile, no run within an item
+  // is without a tile)
+  __device__ __forceinline__ Runs(int total, int n, int least = 1) {
+    parts = least == 1 ? min(total, n) : total > 0 ? min(max(total / least, 1), n) : 0;
+    each = parts > 0 ? quotient(total, parts) : 0;
     extra = total - each * parts;
   }
   __device__ __forceinline__ int start(int part) const { return each * part + min(part, extra); }
   // the run that holds unit x
   __device__ __forceinline__ int of(int x) const {
     const int head = extra * (each + 1);
-    return x < head ? x / (each + 1) : extra + (x - head) / each;
+    return x < head ? quotient(x, each + 1) : extra + quotient(x - head, each);
   }
 };
 
@@ -175,11 +190,12 @@ struct Run {
 constexpr int kSegs = 16;    // ring of segments
 constexpr int kTiles = 32;   // ring of tiles' page checks; copies are fewer tiles ahead
 constexpr int kLens = 1024;  // lengths kept in shared memory
+constexpr int kHeads = 16;   // kv heads whose scales are
 
 template <typename C, Mode M>
 struct AttnShared {
-  // (with a second number a sequence, kPrefix and kOwn keep half as many)
-  static constexpr int LENS = M == kPrefix || M == kOwn ? kLens / 2 : kLens;
+  // (kShared keeps a second number a sequence and half as many sequences)
+  static constexpr int LENS = M == kShared ? kLens / 2 : kLens;
   static constexpr int WIN = M == kWindow;
   uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
@@ -206,7 +222,9 @@ struct AttnShared {
   // themselves is read through global memory
   AttnArgs args;
   int len[LENS];
-  int extra[M == kPrefix || M == kOwn ? LENS : 1];  // members of a group; first own tile
+  int extra[M == kShared ? LENS : 1];               // sequences of a group; first own tile
+  int scan[32];                                     // of the warps' units
+  float scale[2][kHeads];                           // k_scale, v_scale of the first kv heads
   uint2 seen[WIN ? 64 : 1];                         // window: of a node's path, what it sees
   int row_lo[WIN ? C::NT : 1];                      // and the first position before the block
 };
@@ -371,23 +389,39 @@ static __device__ __noinline__ int attn_len(const AttnArgs& a, int b, bool repor
 // First position that the window leaves the first node of row tile `rt` (may be negative;
 // the host keeps the window within the table's width, so this stays in 32 bits).
 __device__ __forceinline__ int attn_lo(const AttnArgs& a, int len, int rt) {
-  const int first = a.parent == nullptr ? rt * a.rows_per_tile / a.G : 0;  // a tree's root
+  const int first = a.parent == nullptr ? a.by_G(rt * a.rows_per_tile) : 0;  // a tree's root
   return len - a.N + first - a.window + 1;
 }
 
-// Tiles that row tile `rt` of a sequence of `len` positions sees.  `extra`: kPrefix, the
-// sequences in the group (whose rows are one after another); kOwn, the first tile that is not
-// the group's.
+// What the block's work is of: sequences, or kShared groups and then sequences.
 template <Mode M>
-__device__ __forceinline__ Span attn_span(const AttnArgs& a, int len, int extra, int rt) {
-  if constexpr (M == kPrefix) {
-    const int64_t rows = (int64_t)extra * a.rows_total;
-    return {(int64_t)rt * a.rows_per_tile < rows ? len / kTile : 0, 0, 0};
-  }
+__device__ __forceinline__ int attn_count(const AttnArgs& a) {
+  return M == kShared ? a.n_groups + a.c.B : a.c.B;
+}
+
+// Row tiles of one of them, and query rows of row tile `rt`.
+template <int NT, Mode M>
+__device__ __forceinline__ int attn_row_tiles(const AttnArgs& a, int v, int extra) {
+  if (M == kShared && v < a.n_groups) return (extra * a.rows_total + NT - 1) / NT;
+  return a.row_tiles;
+}
+
+template <int NT, Mode M>
+__device__ __forceinline__ int attn_row_count(const AttnArgs& a, int v, int extra, int rt) {
+  if (M == kShared && v < a.n_groups) return min(extra * a.rows_total - rt * NT, NT);
+  return min(a.rows_total - rt * a.rows_per_tile, a.rows_per_tile);
+}
+
+// Tiles that row tile `rt` of a sequence of `len` positions sees.  `extra` (kShared): of a group
+// the sequences, whose rows are one after another and see all of `len`; of a sequence the first
+// tile that is not its group's.
+template <Mode M>
+__device__ __forceinline__ Span attn_span(const AttnArgs& a, int v, int len, int extra, int rt) {
+  if (M == kShared && v < a.n_groups) return {len / kTile, 0, 0};
   int see = len;
   if (a.parent == nullptr) {
     const int last = min((rt + 1) * a.rows_per_tile, a.rows_total) - 1;
-    see = len - a.N + last / a.G + 1;
+    see = len - a.N + a.by_G(last) + 1;
   }
   const int tiles = see <= 0 ? 0 : (see + kTile - 1) / kTile;
   if constexpr (M == kWindow) {
@@ -396,25 +430,16 @@ __device__ __forceinline__ Span attn_span(const AttnArgs& a, int len, int extra,
     const int skip = max(0, attn_lo(a, len, rt) / kTile - near);
     return {tiles - skip, near, skip};
   }
-  if constexpr (M == kOwn) return {max(tiles - extra, 0), 0, extra};
+  if constexpr (M == kShared) return {max(tiles - extra, 0), 0, extra};
   return {tiles, 0, 0};
 }
 
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
-// A second number of a sequence (see attn_span); 0 where the mode has none.
+// Length of a sequence (kShared: by the plan, 0 for one that is skipped).
 template <Mode M>
-__device__ __forceinline__ int attn_extra(const AttnArgs& a, int b) {
-  return M == kPrefix || M == kOwn ? max(a.extra[b], 0) : 0;
-}
-
-// Length of sequence b, by the plan where there is one (its first own tile is -1 for a
-// sequence that is skipped).
-template <Mode M>
-__device__ __forceinline__ int attn_len_of(const AttnArgs& a, int b) {
-  if constexpr (M == kPrefix) return a.c.kv_len[b];
-  if constexpr (M == kOwn) return a.extra[b] < 0 ? 0 : a.c.kv_len[b];
-  return attn_len(a, b, false);
+__device__ __forceinline__ int attn_len_of(const AttnArgs& a, int v) {
+  return M == kShared ? a.plan_len[v] : attn_len(a, v, false);
 }
 
 // The lengths the block works with: the first LENS are kept in shared memory.
@@ -423,34 +448,21 @@ struct Lens {
   const AttnArgs& a;
   const int* kept;
   const int* kept_extra;
-  __device__ __forceinline__ int operator()(int b) const {
-    return b < LENS ? kept[b] : attn_len_of<M>(a, b);
+  __device__ __forceinline__ int operator()(int v) const {
+    return v < LENS ? kept[v] : attn_len_of<M>(a, v);
   }
-  __device__ __forceinline__ int extra(int b) const {
-    if constexpr (M == kPrefix || M == kOwn) return b < LENS ? kept_extra[b] : attn_extra<M>(a, b);
-    return 0;
+  __device__ __forceinline__ int extra(int v) const {
+    return M != kShared ? 0 : v < LENS ? kept_extra[v] : max(a.plan_extra[v], 0);
   }
 };
 
 // Lengths into shared memory, by all threads: a thread a sequence, or for
 // trees a warp a sequence (its lanes check the nodes).  Returns whether any of
 // this thread's differs from what was there.
-template <Mode M, int LENS>
-static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, int* kept_extra,
-                                              bool report_it) {
+template <int LENS>
+static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, bool report_it) {
   bool changed = false;
   const int lane = threadIdx.x & 31, n_kept = min(a.c.B, LENS);
-  if constexpr (M == kPrefix || M == kOwn) {  // checked and reported by the plan
-#pragma unroll 1
-    for (int b = threadIdx.x; b < n_kept; b += blockDim.x) {
-      const int x = *(const volatile int32_t*)(a.extra + b);
-      const int len = x < 0 ? 0 : *(const volatile int32_t*)(a.c.kv_len + b);
-      changed |= kept[b] != len || kept_extra[b] != max(x, 0);
-      kept[b] = len;
-      kept_extra[b] = max(x, 0);
-    }
-    return changed;
-  }
   const int unit = a.parent == nullptr ? 1 : 32;  // threads of a sequence
 #pragma unroll 1
   for (int b = threadIdx.x / unit; b < n_kept; b += blockDim.x / unit) {
@@ -484,54 +496,96 @@ static __device__ __noinline__ bool attn_lens(const AttnArgs& a, int* kept, int*
 }
 
 // The same in units of work.
-template <Mode M>
-__device__ __forceinline__ int attn_units(const AttnArgs& a, int len, int extra, int rt) {
-  const int t = attn_span<M>(a, len, extra, rt).tiles;
+template <int NT, Mode M>
+__device__ __forceinline__ int attn_units(const AttnArgs& a, int v, int len, int extra, int rt) {
+  const int t = attn_span<M>(a, v, len, extra, rt).tiles;
+  if constexpr (M == kShared)
+  {
+    const int g = row_groups<NT>(attn_row_count<NT, M>(a, v, extra, rt));
+    return t > 0 ? kSharedLead + g * kSharedMore + t * (4 + 2 * g) : 0;
+  }
   return t > 0 ? t + kLead : 0;
 }
 
+// Units of one head of a sequence or group whose row tiles are few, or (a group's) all alike but
+// for the last.
+template <int NT, Mode M>
+__device__ __forceinline__ int head_units(const AttnArgs& a, int v, int len, int extra) {
+  if (M == kShared && v < a.n_groups) {
+    const int n = attn_row_tiles<NT, M>(a, v, extra);
+    if (n == 0) return 0;
+    return (n - 1) * attn_units<NT, M>(a, v, len, extra, 0) +
+           attn_units<NT, M>(a, v, len, extra, n - 1);
+  }
+  int x = 0;
+#pragma unroll 1
+  for (int rt = 0; rt < a.row_tiles; ++rt) x += attn_units<NT, M>(a, v, len, extra, rt);
+  return x;
+}
+
 // Units of sequence b over all heads, by a whole warp.
-template <Mode M>
-__device__ __forceinline__ int warp_cost(const AttnArgs& a, int len, int extra) {
+template <int NT, Mode M>
+__device__ __forceinline__ int warp_cost(const AttnArgs& a, int b, int len) {
   int t = 0;
 #pragma unroll 1
-  for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_units<M>(a, len, extra, rt);
+  for (int rt = threadIdx.x & 31; rt < a.row_tiles; rt += 32) t += attn_units<NT, M>(a, b, len, 0, rt);
   return warp_sum(t) * a.c.Hkv;
+}
+
+template <Mode M>
+constexpr int kLeastRun = M == kShared ? kMostWeight : 1;
+
+// The run that starts `in` units into sequence (or group) v: its head and row tile.
+template <int NT, Mode M>
+__device__ __forceinline__ void find_item(const AttnArgs& a, Run& r, int v, int len, int extra,
+                                          int units, int in) {
+  const int per_head = a.by_Hkv(units);
+  r.b = v;
+  r.h = quotient(in, per_head);
+  in -= r.h * per_head;
+  if (M == kShared && v < a.n_groups) {
+    const int one = attn_units<NT, M>(a, v, len, extra, 0);
+    r.rt = min(quotient(in, one), attn_row_tiles<NT, M>(a, v, extra) - 1);
+    in -= r.rt * one;
+  } else {
+#pragma unroll 1
+    for (r.rt = 0;; ++r.rt) {
+      const int t = attn_units<NT, M>(a, v, len, extra, r.rt);
+      if (in < t) break;
+      in -= t;
+    }
+  }
+  r.u0 = in;
 }
 
 // The run of block `part` of `parts`: the units of all sequences are counted,
 // then the sequence that holds the run's first one is taken apart.
-template <Mode M, int LENS>
+template <int NT, Mode M, int LENS>
 static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens<M, LENS>& lens, int part,
                                             int parts) {
-  const int lane = threadIdx.x & 31;
-  const bool by_lane = a.row_tiles <= 4;  // a lane a sequence, or the warp a sequence
+  const int lane = threadIdx.x & 31, count = attn_count<M>(a);
+  const bool by_lane = M == kShared || a.row_tiles <= 4;  // a lane a sequence, or the warp a sequence
   const int step = by_lane ? 32 : 1;
   // units of the sequence b0 + lane, or (of all lanes the same) of b0
   auto units = [&](int b0) {
-    if (!by_lane) return warp_cost<M>(a, lens(b0), lens.extra(b0));
-    int x = 0;
-    if (b0 + lane < a.c.B) {
-      const int len = lens(b0 + lane), extra = lens.extra(b0 + lane);
-#pragma unroll 1
-      for (int rt = 0; rt < a.row_tiles; ++rt) x += attn_units<M>(a, len, extra, rt);
-    }
-    return x * a.c.Hkv;
+    if (!by_lane) return warp_cost<NT, M>(a, b0, lens(b0));
+    const int v = b0 + lane;
+    return v < count ? head_units<NT, M>(a, v, lens(v), lens.extra(v)) * a.c.Hkv : 0;
   };
   int total = 0, mine = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.c.B; b0 += step) {
+  for (int b0 = 0; b0 < count; b0 += step) {
     mine = units(b0);
     total += by_lane ? warp_sum(mine) : mine;
   }
-  Run r = {0, 0, 0, 0, 0, 0, Runs(total, parts)};
+  Run r = {0, 0, 0, 0, 0, 0, Runs(total, parts, kLeastRun<M>)};
   if (part >= r.runs.parts) return r;
   r.at = r.runs.start(part);
   r.left = r.runs.start(part + 1) - r.at;
   int before = 0, its = 0;
 #pragma unroll 1
   for (int b0 = 0;; b0 += step) {
-    if (a.c.B > step) mine = units(b0);  // else it is still there
+    if (count > step) mine = units(b0);  // else it is still there
     int upto = mine;
     if (by_lane) {
 #pragma unroll
@@ -551,45 +605,84 @@ static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens<M, LEN
     r.b = b0 + l;
     break;
   }
-  int in = r.at - before;  // of the sequence's `its` tiles
-  const int per_head = its / a.c.Hkv, len = lens(r.b), extra = lens.extra(r.b);
-  r.h = in / per_head;
-  in -= r.h * per_head;
-#pragma unroll 1
-  for (;; ++r.rt) {
-    const int t = attn_units<M>(a, len, extra, r.rt);
-    if (in < t) break;
-    in -= t;
-  }
-  r.u0 = in;
+  find_item<NT, M>(a, r, r.b, lens(r.b), lens.extra(r.b), its, r.at - before);
   return r;
 }
 
+// The same by all threads of the block, a thread a sequence (or group), of which there are at
+// most as many as threads; `out` is written by one of them.
+template <int NT, Mode M, int LENS>
+static __device__ __noinline__ void attn_run_all(const AttnArgs& a, const Lens<M, LENS>& lens,
+                                                 int* scan, Run& out) {
+  const int v = threadIdx.x, lane = v & 31, warp = v >> 5, warps = blockDim.x >> 5;
+  int len = 0, extra = 0, mine = 0;
+  if (v < attn_count<M>(a)) {
+    len = lens(v), extra = lens.extra(v);
+    mine = head_units<NT, M>(a, v, len, extra) * a.c.Hkv;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  const int theirs = lane < warps ? scan[lane] : 0;
+  const int total = warp_sum(theirs);
+  const int before = warp_sum(lane < warp ? theirs : 0) + upto - mine;
+  Run r = {0, 0, 0, 0, 0, 0, Runs(total, gridDim.x, kLeastRun<M>)};
+  if ((int)blockIdx.x >= r.runs.parts) {
+    if (v == 0) out = r;
+    return;
+  }
+  r.at = r.runs.start(blockIdx.x);
+  r.left = r.runs.start(blockIdx.x + 1) - r.at;
+  if (before <= r.at && r.at < before + mine) {
+    find_item<NT, M>(a, r, v, len, extra, mine, r.at - before);
+    out = r;
+  }
+}
+
 // The run's next segment (t1 = 0 when it is at its end).
-template <Mode M, int LENS>
+template <int NT, Mode M, int LENS>
 static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens<M, LENS>& lens, Run& r) {
   Seg s = {};
 #pragma unroll 1
-  while (r.left > 0 && r.b < a.c.B) {
+  while (r.left > 0 && r.b < attn_count<M>(a)) {
     const int len = lens(r.b), extra = lens.extra(r.b);
-    const Span span = attn_span<M>(a, len, extra, r.rt);
-    const int tiles = span.tiles, units = tiles > 0 ? tiles + kLead : 0;
+    const Span span = attn_span<M>(a, r.b, len, extra, r.rt);
+    const int rows = attn_row_count<NT, M>(a, r.b, extra, r.rt);
+    const int groups = row_groups<NT>(rows);
+    const int lead = M == kShared ? kSharedLead + groups * kSharedMore : kLead;
+    const int weight = M == kShared ? 4 + 2 * groups : 1;
+    const int tiles = span.tiles, units = tiles > 0 ? lead + tiles * weight : 0;
     const int rt = r.rt, h = r.h, b = r.b, end = min(units, r.u0 + r.left), taken = end - r.u0;
-    const int t0 = max(r.u0 - kLead, 0), t1 = end - kLead;
+    // a tile belongs to the run that its first unit is in
+    auto tile_of = [&](int u) {
+      const int x = max(u - lead + weight - 1, 0);
+      return M != kShared ? x : weight == 6 ? x / 6 : weight == 8 ? x / 8 : x / 10;
+    };
+    const int t0 = tile_of(r.u0), t1 = tile_of(end);
+    const int start = r.at - r.u0;  // of the item
     r.u0 = 0;
     r.left -= taken;
     r.at += taken;
-    if (++r.rt == a.row_tiles) {
+    if (++r.rt >= attn_row_tiles<NT, M>(a, b, extra)) {
       r.rt = 0;
       if (++r.h == a.c.Hkv) r.h = 0, ++r.b;
     }
     if (t1 <= t0) continue;  // no tiles, or the lead alone
     s.b = b, s.h = h, s.t0 = t0, s.t1 = t1, s.tiles = tiles, s.len = len;
-    s.last = t1 < tiles ? r.runs.of(r.at + tiles - t1 - 1) : 0;
-    s.row0 = rt * a.rows_per_tile;
-    s.rows = min((M == kPrefix ? extra * a.rows_total : a.rows_total) - s.row0, a.rows_per_tile);
+    s.last = t1 < tiles ? r.runs.of(start + lead + (tiles - 1) * weight) : 0;
+    s.row0 = rt * (M == kShared && b < a.n_groups ? NT : a.rows_per_tile);
+    s.rows = rows;
     s.near = span.near, s.skip = span.skip;
     if constexpr (M == kWindow) s.lo = attn_lo(a, len, rt);
+    if constexpr (M == kShared) {
+      s.group = b < a.n_groups;
+      if (!s.group) s.b = b - a.n_groups;
+    }
     return s;
   }
   return s;
@@ -603,7 +696,7 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens<M, L
 #pragma unroll 1
   for (int64_t i = blockIdx.x; i < pairs; i += gridDim.x) {
     const int b = (int)(i / a.row_tiles), rt = (int)(i % a.row_tiles);
-    if (attn_span<M>(a, lens(b), 0, rt).tiles > 0) continue;
+    if (attn_span<M>(a, b, lens(b), 0, rt).tiles > 0) continue;
     const int row0 = rt * a.rows_per_tile, rows = min(a.rows_total - row0, a.rows_per_tile);
 #pragma unroll 1
     for (int k = 0; k < rows * a.c.Hkv; ++k) {
@@ -621,13 +714,13 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens<M, L
 // are this thread's cp.async, not waited for); a lane works out one row's place.
 template <int D, int NT, Mode M>
 static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, int b, int h, int row0,
-                                                   int rows, uint8_t* q, int warp) {
+                                                   int rows, int group, uint8_t* q, int warp) {
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;  // channels of a lane
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
-  const int row = row0 + r0 + lane % ROWS, node = row / a.G;  // over a group's sequences
+  const int row = row0 + r0 + lane % ROWS, node = a.by_G(row);  // over a group's sequences
   int n = node;
-  if constexpr (M == kPrefix) {
-    const int member = node / a.N;
+  if (M == kShared && group) {
+    const int member = a.by_N(node);
     b = a.group_seq[b] + member, n = node - member * a.N;
   }
   const int64_t mine = b * a.q_stride_b + n * a.q_stride_n +
@@ -685,10 +778,10 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&x)[W]) 
 // costs more (48 uneven sequences 81 -> 83 us), and each row has its own.
 template <int D, int NT, Mode M>
 static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>, M>& sh,
-                                               int b, int len, int row0, int rows, uint8_t* q,
-                                               int warp, float to_log2) {
+                                               int b, int len, int row0, int rows, int group,
+                                               uint8_t* q, int warp, float to_log2) {
   const int G = a.G, Hq = a.Hq;
-  const bool bf16 = a.bf16, tree = M != kPrefix && a.parent != nullptr;
+  const bool bf16 = a.bf16, tree = a.parent != nullptr && !(M == kShared && group);
   constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
@@ -744,7 +837,7 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
       __syncwarp();
     }
   }
-  const int row = row0 + min(r0 + lane % ROWS, rows - 1), n = row / G;
+  const int row = row0 + min(r0 + lane % ROWS, rows - 1), n = a.by_G(row);
   cp_async_wait_all();
   uint32_t x[ROWS][E / 2];
   unsigned mine = 0;  // the lane's row's largest magnitude
@@ -820,6 +913,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShared<C, M> sh;
   constexpr int LENS = AttnShared<C, M>::LENS;
+  static_assert(sizeof(AttnShared<C, M>) + C::SMEM <= 227 * 1024, "shared memory of a block");
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* dead = &sh.dead;
@@ -853,32 +947,54 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   // The block's run follows from the lengths alone.  It is worked out before the
   // wait on the kernel before this one, from the lengths as they read then, and
   // again after it in the case that one of them has changed (with more sequences
-  // than are kept, always).
-  // (A plan's numbers are the kernel's before this one: there is nothing to read yet in
-  // kPrefix, and they are complete when kOwn starts, whose predecessor waited for them.)
+  // than are kept, always).  kShared reads its plan's numbers, which that kernel writes.
   const Lens<M, LENS> lens = {args, sh.len, sh.extra};
-  const bool kept = M != kPrefix && a.c.B <= LENS;
-  if constexpr (M != kPrefix) (void)attn_lens<M, LENS>(args, sh.len, sh.extra, false);
-  __syncthreads();
-  if (warp == C::wI + 2 && kept) {
-    Run run = attn_run(args, lens, blockIdx.x, gridDim.x);
-    const Seg first = attn_seg(args, lens, run);
-    if (lane == 0) sh.run = run, sh.seg[0] = first;
+  const bool kept = attn_count<M>(a) <= LENS;
+  const bool by_thread = (M == kShared || (M == kWindow && a.row_tiles <= 4)) &&
+                         attn_count<M>(a) <= C::THREADS;
+  auto find_run = [&]() {  // by all threads
+    if (by_thread && kept) {
+      attn_run_all<NT, M>(args, lens, sh.scan, sh.run);
+      __syncthreads();
+    }
+    if (warp == C::wI + 2) {
+      Run run = by_thread && kept ? sh.run : attn_run<NT, M>(args, lens, blockIdx.x, gridDim.x);
+      const Seg first = attn_seg<NT, M>(args, lens, run);
+      if (lane == 0) sh.run = run, sh.seg[0] = first;
+    }
+  };
+  if constexpr (M != kShared) {
+    (void)attn_lens<LENS>(args, sh.len, false);
+    __syncthreads();
+    if (kept) find_run();
   }
   __syncthreads();
   pdl_enter();
-  // the first segment's queries are on their way while the lengths are read again
   const bool softmax = warp >= C::wS && warp < C::wI;
-  auto head_scale = [&](int h) { return a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.f; };
-  float k_scale = 1.f;
-  if (softmax && kept && sh.seg[0].t1 > 0) {
-    k_scale = head_scale(sh.seg[0].h);
-    attn_rows_copy<D, NT, M>(args, sh.seg[0].b, sh.seg[0].h, sh.seg[0].row0, sh.seg[0].rows,
-                             smem + C::oQ, warp - C::wS);
+  if (threadIdx.x < 2 * kHeads) {
+    const int h = threadIdx.x & (kHeads - 1);
+    const float* scales = threadIdx.x < kHeads ? a.c.k_scale : a.c.v_scale;
+    sh.scale[threadIdx.x / kHeads][h] = scales != nullptr && h < a.c.Hkv ? scales[h] : 1.f;
   }
-  const bool changed = attn_lens<M, LENS>(args, sh.len, sh.extra, blockIdx.x == 0);
+  bool changed = false;
+  if constexpr (M == kShared) {
+#pragma unroll 1
+    for (int v = threadIdx.x; v < min(attn_count<M>(a), LENS); v += C::THREADS)
+      sh.len[v] = a.plan_len[v], sh.extra[v] = max(a.plan_extra[v], 0);
+    __syncthreads();
+    find_run();
+  } else {
+    // the first segment's queries are on their way while the lengths are read again
+    if (softmax && kept && sh.seg[0].t1 > 0)
+      attn_rows_copy<D, NT, M>(args, sh.seg[0].b, sh.seg[0].h, sh.seg[0].row0, sh.seg[0].rows, 0,
+                               smem + C::oQ, warp - C::wS);
+    changed = attn_lens<LENS>(args, sh.len, blockIdx.x == 0);
+  }
   tc::fence_before_sync();
-  const bool again = __syncthreads_or(changed) || !kept;
+  const bool again = __syncthreads_or(changed) || (M != kShared && !kept);
+  auto head_scale = [&](int kind, const float* scales, int h) {
+    return h < kHeads ? sh.scale[kind][h] : scales != nullptr ? scales[h] : 1.f;
+  };
   tc::fence_after_sync();
   // all 512 columns are this block's, so its tensor memory begins at address 0, and
   // the addresses below are column numbers known at compile time
@@ -948,7 +1064,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int quarter = warp & 3;
     const uint32_t dst = ((uint32_t)(quarter * 32) << 16) + C::cV;
     const int vt = threadIdx.x - 32 * C::wV;
-    if constexpr (M == kFull || M == kWindow) attn_zero(args, lens, D, vt);
+    if constexpr (M != kShared) attn_zero(args, lens, D, vt);
     int stage = 0, unit = 0, tile = 0;
     unsigned raw_ph = 0, unit_ph = 1;
     for (;; ++seg_no) {
@@ -1029,7 +1145,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     const int gt = (threadIdx.x - 32 * C::wS) & 127;   // thread of the group
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     int tile = 0;
-    if constexpr (M == kFull || M == kWindow)
+    if constexpr (M != kShared)
       if (threadIdx.x == 32 * C::wS) a.join[blockIdx.x] = AttnJoin{};
     // (the segment stays in the ring until its item is written: registers are short)
     auto find_seg = [&](int no) {
@@ -1037,11 +1153,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       return sh.seg[no & (kSegs - 1)].t1 > 0 && !__any_sync(0xffffffffu, *dead);
     };
     auto fetch_rows = [&](const Seg& n) {
-      k_scale = head_scale(n.h);
-      attn_rows_copy<D, NT, M>(args, n.b, n.h, n.row0, n.rows, smem + C::oQ, warp - C::wS);
+      attn_rows_copy<D, NT, M>(args, n.b, n.h, n.row0, n.rows, n.group, smem + C::oQ,
+                               warp - C::wS);
     };
     bool more = find_seg(0);
-    if (again) {
+    if (again || M == kShared) {
       cp_async_wait_all();  // of the early copy, to the same place
       if (more) fetch_rows(sh.seg[0]);
     }
@@ -1050,17 +1166,18 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       if (barrier_any(4, 128 * C::NS, !more)) break;
       const Seg& e = sh.seg[seg_no & (kSegs - 1)];
       const float c_all =
-          attn_rows<D, NT, M>(args, sh, e.b, e.len, e.row0, e.rows, smem + C::oQ, warp - C::wS,
-                              a.scale * (k_scale * kLog2e));
+          attn_rows<D, NT, M>(args, sh, e.b, e.len, e.row0, e.rows, e.group, smem + C::oQ,
+                              warp - C::wS,
+                              a.scale * (head_scale(0, a.c.k_scale, e.h) * kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH) sh.neg_m[c0 + gt] = -kNone;
       tc::named_barrier(1 + group, 128);
-      const int base = e.len - a.N, n_lo = e.row0 / a.G;
+      const int base = e.len - a.N, n_lo = a.by_G(e.row0);
       // window: the first position that all rows see (a tree has at most a.N levels)
       const int hi = M != kWindow ? 0
                                   : (a.parent != nullptr ? base + a.N - 1
-                                                         : base + (e.row0 + e.rows - 1) / a.G) -
+                                                         : base + a.by_G(e.row0 + e.rows - 1)) -
                                         a.window + 1;
       float2 l[C::NH / 2];
 #pragma unroll
@@ -1070,13 +1187,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const int buf = tile & 1;
         const unsigned ph = (tile >> 1) & 1;
         attn_wait(&sh.s_full[buf], ph, dead);
+        if (M == kShared && c0 >= e.rows) {  // no rows of the item in this group
+          if (lane == 0) mbar_arrive(&sh.s_empty[buf]), mbar_arrive(&sh.p_full[buf]);
+          continue;
+        }
         tc::fence_after_sync();
         const int ok = sh.tile_ok[0][tile & (kTiles - 1)];
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
         const int at = tile_at<M>(e, t);
-        if constexpr (M == kPrefix) {  // every row sees it
+        if (M == kShared && e.group) {  // every row sees it
           if (!((ok >> quarter) & 1)) vis = 0;
         } else if (ok != 15 ||
                    (a.parent != nullptr ? (at + 1) * kTile > base
@@ -1232,11 +1353,15 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       more = find_seg(seg_no + 1);
       if (more) fetch_rows(sh.seg[(seg_no + 1) & (kSegs - 1)]);
       // ---- epilogue
-      // kPrefix, kOwn: every item is a part of its rows' outputs, its first one goes to the
+      // kShared: every item is a part of its rows' outputs, its first one goes to the
       // rows' own place, and at most one of a block (its first segment) goes on from another
-      constexpr bool PARTS = M == kPrefix || M == kOwn;
+      constexpr bool PARTS = M == kShared;
+      if (PARTS && c0 >= e.rows) {
+        if (lane == 0) mbar_arrive(&sh.o_empty), mbar_arrive(&sh.seg_empty[seg_no & (kSegs - 1)]);
+        continue;
+      }
       const bool whole = !PARTS && e.t0 == 0 && e.t1 == e.tiles;
-      const int first = M == kPrefix ? a.group_seq[e.b] : e.b;
+      const int first = PARTS && e.group ? a.group_seq[e.b] : e.b;
       const int64_t item = (int64_t)first * a.N * a.Hq + e.h * a.G;  // output row of node 0
       const int64_t slot = PARTS ? blockIdx.x : 2 * (int64_t)blockIdx.x + (seg_no > 0);
       {
@@ -1256,13 +1381,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         const float m = -sh.neg_m[r];
         float inv = 1.f;
         if (whole) {
-          inv = total != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[e.h] : 1.f) / total : 0.f;
+          inv = total != 0.f ? head_scale(1, a.c.v_scale, e.h) / total : 0.f;
           if (a.lse != nullptr && r < e.rows)
             a.lse[item + sh.row_at[r]] =
                 total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
         } else if (PARTS && e.t0 == 0) {
           if (r < e.rows)
-            a.row_part[item + sh.row_at[r]] = {
+            a.row_part[e.group][item + sh.row_at[r]] = {
                 m, total,
                 (int)blockIdx.x | (e.t1 == e.tiles ? (int)blockIdx.x : e.last) << 16, r};
         } else {
@@ -1301,7 +1426,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
             }
           }
         } else if (PARTS && e.t0 == 0) {
-          float* out = a.row_o + item * D + ch;
+          float* out = a.row_o[e.group] + item * D + ch;
 #pragma unroll
           for (int i = 0; i < C::NH; ++i) {
             if (i >= rows) break;
@@ -1323,13 +1448,15 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     cp_async_wait_all();  // (only where a wait ran out are there any)
   } else if (warp == C::wI) {
     // ------------------------------------------------ S^T products (one elected lane)
-    constexpr uint32_t id = idesc_f16(NT, false);
+    uint32_t id = idesc_f16(NT, false);
     // descriptors advance by 16-byte units in their low word
     const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oQ), 16, 1024);
     int tile = 0, ku = 0;
     unsigned ku_ph = 0;
     for (; next_seg(); ++seg_no) {
       attn_wait(&sh.q_full, seg_no & 1, dead);
+      // as many columns as softmax groups have rows of the item
+      if (M == kShared && NT > 32) id = idesc_f16(min((s.rows + 31) / 32 * 32, NT), false);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int buf = tile & 1;
@@ -1354,12 +1481,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     }
   } else if (warp == C::wI + 1) {
     // ------------------------------------------------ O^T products (one elected lane)
-    constexpr uint32_t id = idesc_f16(NT, true);
+    uint32_t id = idesc_f16(NT, true);
     const uint64_t desc = tc::sdesc_sw128(smem_addr(smem + C::oP), kTile * 128, 1024);
     int tile = 0, vu = 0;
     unsigned vu_ph = 0;
     for (; next_seg(); ++seg_no) {
       attn_wait(&sh.o_empty, (seg_no & 1) ^ 1, dead);
+      if (M == kShared && NT > 32) id = idesc_f16(min((s.rows + 31) / 32 * 32, NT), true);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int buf = tile & 1;
@@ -1394,7 +1522,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     // ------------------------------------------------ the run's segments, the records in
     const bool lead = warp == C::wI + 2, do_k = C::FW == 1 || lead, do_v = C::FW == 1 || !lead;
     Run run = sh.run;
-    if (lead && again) run = attn_run(args, lens, blockIdx.x, gridDim.x);
+    if (lead && again) run = attn_run<NT, M>(args, lens, blockIdx.x, gridDim.x);
     // lanes 2r and 2r + 1: codes and scales of record r's K half, lanes 8 + 2r and
     // 9 + 2r: of its V half (the first eight lanes where a warp has V alone)
     const int lanes = C::FW == 1 ? 16 : 8;
@@ -1407,7 +1535,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     for (;; ++seg_no) {
       if (lead) {
         const bool ready = seg_no == 0 && !again;
-        s = ready ? sh.seg[0] : attn_seg(args, lens, run);
+        s = ready ? sh.seg[0] : attn_seg<NT, M>(args, lens, run);
         const int i = seg_no & (kSegs - 1);
         // (the ring's first pass: empty, and the first segment's readers may be ahead)
         if (seg_no >= kSegs) attn_wait(&sh.seg_empty[i], ((seg_no / kSegs) & 1) ^ 1, dead);
@@ -1419,20 +1547,20 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       } else if (!next_seg()) {
         break;
       }
-      const int row = M == kPrefix ? a.group_row[s.b] : s.b;
+      const int row = M == kShared && s.group ? a.group_row[s.b] : s.b;
       const int32_t* table = a.c.table + (int64_t)row * a.c.table_stride;
       const uint8_t* head = static_cast<const uint8_t*>(a.c.pages) + from +
                             (int64_t)s.h * (a.c.page_tokens / kRec) * rec_bytes(D);
       // this lane's position, as an entry of the table and an offset in the page, two
       // tiles ahead of the copies: the page numbers are looked up that early
       int pos = tile_at<M>(s, s.t0) * kTile + r * kRec;
-      int entry = pos / a.c.page_tokens, off = pos % a.c.page_tokens;
-      const int entries = kTile / a.c.page_tokens, rest = kTile % a.c.page_tokens;
+      int entry = a.by_page(pos), off = pos - entry * a.c.page_tokens;
+      const int entries = a.by_page(kTile), rest = kTile - entries * a.c.page_tokens;
       int page[3], offs[3];
       auto look_up = [&](int i, int t) {
         const int at = tile_at<M>(s, t) * kTile + r * kRec;
         if (M == kWindow && t == s.near && t > s.t0)  // the window's first tile
-          entry = at / a.c.page_tokens, off = at % a.c.page_tokens;
+          entry = a.by_page(at), off = at - entry * a.c.page_tokens;
         page[i] = lane < lanes && t < s.t1 && at < s.len ? table[entry] : -1;
         offs[i] = off;
         entry += entries;
@@ -1605,7 +1733,7 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
     return GDN_ERR_CUDA;
   }
   const int rc = launch_pdl(attn_kernel<D, NT, M>, dim3(parts), dim3(C::THREADS), C::SMEM, s, a);
-  if (rc != GDN_OK || M == kPrefix || M == kOwn) return rc;  // (joined by shared_join_kernel)
+  if (rc != GDN_OK || M == kShared) return rc;  // (joined by shared_join_kernel)
   const dim3 block(kJoinThreads);
   if (NT == 16)
     return launch_pdl(join_kernel<D, true>, dim3(parts, a.rows_per_tile), block, 0, s, a, NT);

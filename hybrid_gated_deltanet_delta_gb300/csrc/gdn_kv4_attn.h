@@ -20,16 +20,33 @@ struct AttnJoin {
 enum Mode {
   kFull,    // all that its node sees; the output
   kWindow,  // the first `sinks` and the last `window` entries of its node's path; the output
-  kPrefix,  // the part that the sequences of a group share, their rows one after another (the
-            // cache's lengths are the shared ones); a part of the output
-  kOwn      // what lies behind that part; a part of the output
+  kShared   // what the sequences of a group share, their rows one after another, and what each
+            // has behind it; parts of the output
 };
 
-// The first part of a query row's output that a kPrefix or kOwn pass leaves: reference and sum,
-// the item's first block and its last one (16 bits each), and the row's place in its tile.
+// The first part of a query row's output that a kShared pass leaves: reference and sum, the
+// item's first block and its last one (16 bits each), and the row's place in its tile.
 struct RowPart {
   float m, l;
   int blocks, row;
+};
+
+// Division of 0 <= n < 2^31 by a number that the host knows: (n m / 2^32 + n) / 2^s with
+// s = ceil(log2 d), m = 2^32 (2^s - d) / d + 1 rounded down (Granlund and Montgomery, 1994).
+// The kernels' few hundred instructions before their first tile are fetched anew in every
+// launch, and a division is some twenty of them.
+struct Divisor {
+  uint32_t m, s;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) : m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s);
+  }
+#endif
 };
 
 struct AttnArgs {
@@ -46,12 +63,16 @@ struct AttnArgs {
   int N, Hq, G;     // G: query heads of a kv head
   int rows_total, rows_per_tile, row_tiles;
   int bf16;
+  Divisor by_G, by_N, by_Hkv, by_page;  // page: its tokens
   int window, sinks;         // kWindow
-  const int32_t* extra;      // kPrefix: sequences of a group; kOwn: first own tile (-1: skipped)
-  const int32_t* group_seq;  // kPrefix: a group's first sequence,
+  // kShared: of the groups and then of the sequences, the shared length and the length (0: it is
+  // skipped); a group's sequences and a sequence's first own tile (-1: it is skipped)
+  const int32_t *plan_len, *plan_extra;
+  const int32_t* group_seq;  // a group's first sequence,
   const int32_t* group_row;  // and the table row that its shared pages are taken from
-  float* row_o;              // kPrefix, kOwn: [B*N*Hq][D], each row's first part
-  RowPart* row_part;         // [B*N*Hq]
+  int n_groups;
+  float* row_o[2];           // [B*N*Hq][D], each row's first own part; and first shared one
+  RowPart* row_part[2];      // [B*N*Hq]
 };
 
 int attn_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
@@ -60,12 +81,9 @@ int attn_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 int window_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 int window_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 int window_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int prefix_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int prefix_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int prefix_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int own_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int own_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
-int own_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int shared_launch_64(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int shared_launch_128(const AttnArgs& a, int NT, int parts, cudaStream_t s);
+int shared_launch_256(const AttnArgs& a, int NT, int parts, cudaStream_t s);
 
 // Query rows of a tile.  K and V are brought in and dequantised once per row tile, so
 // wide ones pay: with tiles of at most 64 rows a 2048-token piece of a prompt takes 431 us,
@@ -83,13 +101,14 @@ inline void row_tiles(int rows, int* tiles, int* per_tile) {
 
 }  // namespace kv4
 
-// gdn_kv4_shared.cu.  plan: of each group the shared length, its sequences, the first of them
-// and the table row that holds the shared pages (n_groups each); start: of each sequence its
-// first own tile.
+// gdn_kv4_shared.cu: the numbers of AttnArgs that a kShared pass reads, and the sum of the parts
+// that it leaves (`rows`: of a slot of part_o).
+struct SharedPlan {
+  int32_t *len, *extra, *group_seq, *group_row;
+};
 int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
-                           const int32_t* group, int n_groups, int32_t* plan, int32_t* start,
+                           const int32_t* group, int n_groups, const SharedPlan& plan,
                            cudaStream_t s);
-int launch_kv4_shared_join(const kv4::AttnArgs& own, const kv4::AttnArgs& pre, int own_rows,
-                           int pre_rows, int blocks, cudaStream_t s);
+int launch_kv4_shared_join(const kv4::AttnArgs& a, int rows, int blocks, cudaStream_t s);
 
 }  // namespace gdn

@@ -1,5 +1,5 @@
 // Attention over the 4-bit cache for sequences that share pages: the plan before, and the join
-// after, the two passes of gdn_kv4_attn.cuh (kPrefix and kOwn).
+// after, the pass of gdn_kv4_attn.cuh (kShared) over what groups share and sequences have alone.
 //
 //   o = (2^(m_p - m) O_p + 2^(m_o - m) O_o) / (2^(m_p - m) l_p + 2^(m_o - m) l_o)
 //
@@ -22,17 +22,18 @@ constexpr float kNone = -3.402823466e38f;
 // A block a group.  The group's first sequence with a whole tile before its block is the one
 // whose table row the shared pages are taken from; the others share with it what lies on the
 // same pages of both, in whole tiles.  What all of those share that share a tile at all is the
-// group's prefix.  Writes of each group the shared length, its sequences, the first of them and
-// that row; of each sequence its first own tile, -1 where it is skipped.  Bound by the latency
-// of the lengths and of the rows' entries after them.
+// group's prefix.  Bound by the latency of the lengths and of the rows' entries after them.
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kKept = 512;  // sequences of a group whose numbers stay in shared memory
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
-            const int32_t* __restrict__ group, int n_groups, int32_t* __restrict__ plan,
-            int32_t* start) {
+            const int32_t* __restrict__ group, int n_groups, SharedPlan plan) {
   __shared__ int ref, shortest, sharers;
   __shared__ int differ[kPlanWarps];  // first entry of a sequence's row that is another page
+  __shared__ int kept[kKept];
+  int32_t* start = plan.extra + n_groups;  // -1 for a sequence that is skipped
+  int32_t* lens = plan.len + n_groups;
   const int g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_enter();
   if (tid == 0) ref = c.B, shortest = 0x7fffffff, sharers = 0;
@@ -41,25 +42,28 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
     const int x = group[i];
     ok = ok && x >= 0 && x <= c.B && (i == n_groups || x <= group[i + 1]);
   }
+  const int lo = group[g], hi = group[g + 1];
   ok = __syncthreads_and(ok);
   // tokens before a sequence's block, -1 for one that is skipped; by a warp
   auto before = [&](int b) {
-    const int len = seq_len(c, b, lane == 0);
-    if (len == 0) return -1;
-    bool good = true;
-    if (parent != nullptr) {
+    int len = seq_len(c, b, lane == 0);
+    if (len > 0 && parent != nullptr) {
       const int32_t* p = parent + (int64_t)b * N;
+      bool good = true;
       for (int n = lane; n < N; n += 32) {
         const int up = p[n];
         good = good && (n == 0 ? up == -1 : up >= 0 && up < n);
       }
-      good = __all_sync(0xffffffffu, good);
-      if (!good && lane == 0) report(c.status, GDN_ERR_BAD_TREE);
+      if (!__all_sync(0xffffffffu, good)) {
+        if (lane == 0) report(c.status, GDN_ERR_BAD_TREE);
+        len = 0;
+      }
     }
-    return good ? max(len - N, 0) : -1;
+    if (lane == 0) lens[b] = len;
+    return len > 0 ? max(len - N, 0) : -1;
   };
   if (!ok && g == 0 && tid == 0) report(c.status, GDN_ERR_ROW_RANGE);
-  const int first = ok ? group[g] : 0, end = ok ? group[g + 1] : 0;
+  const int first = ok ? lo : 0, end = ok ? hi : 0;
   if (g == 0) {  // sequences of no group
     const int from = ok ? group[0] : c.B, to = ok ? group[n_groups] : c.B;
     for (int i = warp; i < from + c.B - to; i += kPlanWarps) {
@@ -67,17 +71,19 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
       if (lane == 0) start[b] = x < 0 ? -1 : 0;
     }
   }
+  // of sequence first + i: tokens before its block, where they are a tile, then tiles shared
+  int32_t* held = end - first <= kKept ? kept : start + first;
   for (int b = first + warp; b < end; b += kPlanWarps) {
     const int x = before(b);
     if (lane == 0) {
-      start[b] = x < kTile ? min(x, 0) : x;  // (tokens, for now)
+      held[b - first] = x < kTile ? min(x, 0) : x;
       if (x >= kTile) atomicMin(&ref, b);
     }
   }
   __syncthreads();
   const int r = ref;
   if (r < end) {
-    const int held = start[r];
+    const int most = held[r - first];
     const int32_t* row = c.table + (int64_t)r * c.table_stride;
     // up to kPlanWarps sequences at once, the warps spread over them
     for (int b0 = r + 1; b0 < end; b0 += kPlanWarps) {
@@ -86,21 +92,21 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
       __syncthreads();
       const int m = warp / each, turn = warp % each, b = b0 + m;
       if (m < count) {
-        const int common = min(start[b], held);
+        const int common = min(held[b - first], most);
         const int pages = common <= 0 ? 0 : (common + c.page_tokens - 1) / c.page_tokens;
         const int32_t* mine = c.table + (int64_t)b * c.table_stride;
-        constexpr int U = 8;
+        constexpr int U = 16;
         for (int j0 = turn * 32 * U; j0 < pages; j0 += each * 32 * U) {
-          bool other[U];
+          int other[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int j = j0 + u * 32 + lane;
-            other[u] = j < pages && mine[j] != row[j];
+            other[u] = j < pages ? mine[j] ^ row[j] : 0;
           }
           int at = 0x7fffffff;
 #pragma unroll
           for (int u = U - 1; u >= 0; --u)
-            if (other[u]) at = j0 + u * 32 + lane;
+            if (other[u] != 0) at = j0 + u * 32 + lane;
           at = __reduce_min_sync(0xffffffffu, at);
           if (at != 0x7fffffff) {
             if (lane == 0) atomicMin(&differ[m], at);
@@ -110,23 +116,23 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
       }
       __syncthreads();
       if (tid < count) {
-        const int base = start[b0 + tid];
+        const int base = held[b0 + tid - first];
         const int64_t same = (int64_t)differ[tid] * c.page_tokens;
-        const int tiles = base <= 0 ? 0 : (int)min((int64_t)min(base, held), same) / kTile;
-        if (base >= 0) start[b0 + tid] = tiles;
+        const int tiles = base <= 0 ? 0 : (int)min((int64_t)min(base, most), same) / kTile;
+        if (base >= 0) held[b0 + tid - first] = tiles;
         if (tiles > 0) atomicMin(&shortest, tiles), atomicAdd(&sharers, 1);
       }
       __syncthreads();
     }
   }
   const int tiles = sharers > 0 ? shortest : 0;
-  for (int b = first + tid; b < end; b += kPlanThreads)
-    if (start[b] > 0) start[b] = tiles;
+  for (int i = tid; i < end - first; i += kPlanThreads)
+    start[first + i] = held[i] > 0 ? tiles : held[i];
   if (tid == 0) {
-    plan[g] = tiles * kTile;
-    plan[n_groups + g] = end - first;
-    plan[2 * (int64_t)n_groups + g] = first;
-    plan[3 * (int64_t)n_groups + g] = r < end ? r : first;
+    plan.len[g] = tiles * kTile;
+    plan.extra[g] = end - first;
+    plan.group_seq[g] = first;
+    plan.group_row[g] = r < end ? r : first;
   }
 }
 
@@ -136,18 +142,9 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
 // pass's, in block order, and then the shared one's.
 constexpr int kJoinThreads = 256;
 
-struct JoinSide {
-  const float* row_o;
-  const RowPart* row_part;
-  const float* part_o;
-  const float2* part_ml;
-  int NT;
-};
-
 template <int D, bool ONE_ROW>
 __global__ void __launch_bounds__(kJoinThreads)
-shared_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ JoinSide own,
-                   const __grid_constant__ JoinSide pre, int blocks) {
+shared_join_kernel(const __grid_constant__ AttnArgs a, int NT, int blocks) {
   constexpr int Q = D / 4, NP = kJoinThreads / Q, STEP = ONE_ROW ? NP : 1;
   __shared__ __align__(16) float acc[ONE_ROW ? NP : 1][D];
   __shared__ float2 sums[NP];
@@ -157,20 +154,21 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ J
   if (row >= (int64_t)a.c.B * a.N * a.Hq) return;  // ONE_ROW: none
   const int64_t node = row / a.Hq;
   const int b = (int)(node / a.N), n = (int)(node % a.N), head = (int)(row % a.Hq);
-  const int from = a.extra[b];
-  const bool there = from >= 0 && (int64_t)a.c.kv_len[b] - a.N + n >= 0;
-  // first block, parts and row of each side; (a pass whose waits ran out may have left no
-  // numbers here, so they are kept in range)
-  const RowPart mine = there ? own.row_part[row] : RowPart{};
-  const RowPart theirs = there && from > 0 ? pre.row_part[row] : RowPart{};
-  auto side = [&](const RowPart& p, int NT, int& first, int& at) {
-    first = min(p.blocks & 0xffff, blocks - 1);
-    at = min(max(p.row, 0), NT - 1);
-    return min(max((p.blocks >> 16 & 0xffff) - first, 0), blocks - 1 - first) + 1;
-  };
-  int first[2], at[2];
-  const int n_own = there ? side(mine, own.NT, first[0], at[0]) : 0;
-  const int parts = n_own + (there && from > 0 ? side(theirs, pre.NT, first[1], at[1]) : 0);
+  const int from = a.plan_extra[a.n_groups + b];
+  const bool there = from >= 0 && a.plan_len[a.n_groups + b] - a.N + n >= 0;
+  // first block, parts and row of the own (0) and the shared side (1); (a pass whose waits ran
+  // out may have left no numbers here, so they are kept in range)
+  RowPart head_of[2] = {};
+  int first[2] = {}, at[2] = {}, count[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!there || (i == 1 && from == 0)) continue;
+    head_of[i] = a.row_part[i][row];
+    first[i] = min(head_of[i].blocks & 0xffff, blocks - 1);
+    at[i] = min(max(head_of[i].row, 0), NT - 1);
+    count[i] = min(max((head_of[i].blocks >> 16 & 0xffff) - first[i], 0), blocks - 1 - first[i]) + 1;
+  }
+  const int parts = count[0] + count[1];
   float top = kNone, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto larger = [](float p, float q) { return q > p || q != q ? q : p; };  // NaN stays
@@ -185,17 +183,17 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ J
       ml[u] = make_float2(kNone, 0.f);
       p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < parts) {
-        const bool is_pre = i >= n_own;
-        const JoinSide& s = is_pre ? pre : own;
-        const int k = is_pre ? i - n_own : i;
+        const bool shared = i >= count[0];
+        const int k = shared ? i - count[0] : i;
         if (k == 0) {
-          ml[u] = is_pre ? make_float2(theirs.m, theirs.l) : make_float2(mine.m, mine.l);
-          p[u] = __ldcg(reinterpret_cast<const float4*>(s.row_o + row * D) + quad);
+          ml[u] = shared ? make_float2(head_of[1].m, head_of[1].l)
+                         : make_float2(head_of[0].m, head_of[0].l);
+          p[u] = __ldcg(reinterpret_cast<const float4*>(a.row_o[shared] + row * D) + quad);
         } else {
-          const int64_t slot = (int64_t)((is_pre ? first[1] : first[0]) + k) * s.NT +
-                               (is_pre ? at[1] : at[0]);
-          ml[u] = __ldcg(s.part_ml + slot);
-          p[u] = __ldcg(reinterpret_cast<const float4*>(s.part_o + slot * D) + quad);
+          const int64_t slot = (int64_t)((shared ? first[1] : first[0]) + k) * NT +
+                               (shared ? at[1] : at[0]);
+          ml[u] = __ldcg(a.part_ml + slot);
+          p[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot * D) + quad);
         }
       }
     }
@@ -243,33 +241,30 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ J
 }
 
 template <int D>
-int join_d(const AttnArgs& own, const JoinSide& o, const JoinSide& p, int blocks, cudaStream_t s) {
-  const int64_t rows = (int64_t)own.c.B * own.N * own.Hq;
+int join_d(const AttnArgs& a, int NT, int blocks, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.c.B * a.N * a.Hq;
   constexpr int NP = kJoinThreads / (D / 4);
   if (rows <= 8 * blocks)
     return launch_pdl(shared_join_kernel<D, true>, dim3((unsigned)rows), dim3(kJoinThreads), 0, s,
-                      own, o, p, blocks);
+                      a, NT, blocks);
   return launch_pdl(shared_join_kernel<D, false>, dim3((unsigned)((rows + NP - 1) / NP)),
-                    dim3(kJoinThreads), 0, s, own, o, p, blocks);
+                    dim3(kJoinThreads), 0, s, a, NT, blocks);
 }
 
 }  // namespace
 
 int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
-                           const int32_t* group, int n_groups, int32_t* plan, int32_t* start,
+                           const int32_t* group, int n_groups, const SharedPlan& plan,
                            cudaStream_t s) {
   return launch_pdl(plan_kernel, dim3(n_groups), dim3(kPlanThreads), 0, s, c, N, parent, group,
-                    n_groups, plan, start);
+                    n_groups, plan);
 }
 
-int launch_kv4_shared_join(const kv4::AttnArgs& own, const kv4::AttnArgs& pre, int own_rows,
-                           int pre_rows, int blocks, cudaStream_t s) {
-  const JoinSide o = {own.row_o, own.row_part, own.part_o, own.part_ml, own_rows};
-  const JoinSide p = {pre.row_o, pre.row_part, pre.part_o, pre.part_ml, pre_rows};
-  switch (own.c.D) {
-    case 64: return join_d<64>(own, o, p, blocks, s);
-    case 128: return join_d<128>(own, o, p, blocks, s);
-    default: return join_d<256>(own, o, p, blocks, s);
+int launch_kv4_shared_join(const kv4::AttnArgs& a, int rows, int blocks, cudaStream_t s) {
+  switch (a.c.D) {
+    case 64: return join_d<64>(a, rows, blocks, s);
+    case 128: return join_d<128>(a, rows, blocks, s);
+    default: return join_d<256>(a, rows, blocks, s);
   }
 }
 
