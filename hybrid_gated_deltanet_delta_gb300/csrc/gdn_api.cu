@@ -196,9 +196,10 @@ int kv4_checks(const gdn_kv4_cache* c, int32_t N) {
   return GDN_OK;
 }
 
-// Query rows of a batch, that the join of shared and own parts counts in 31 bits.
+// Query rows of a batch, that the join of shared and own parts counts in 31 bits (a block of it
+// goes up to 15 past the last).
 bool kv4_shared_rows(int32_t B, int32_t N, int32_t Hq) {
-  return (int64_t)N * Hq <= 0x7fffffff / B;
+  return (int64_t)N * Hq <= 0x7ffffff0 / B;
 }
 
 // What every form of the attention checks, but for the size of its workspace.

@@ -120,9 +120,9 @@ SharedSpace shared_space(void* base, int B, int N, int Hq, int D, int n_groups, 
     return p;
   };
   auto ints = [&](size_t n) { return reinterpret_cast<int32_t*>(take(4 * n)); };
-  const size_t groups = n_groups, all = groups + B;
+  const size_t all = (size_t)n_groups + B;
   w.plan.len = ints(all), w.plan.extra = ints(all);
-  w.plan.group_seq = ints(groups), w.plan.group_row = ints(groups);
+  w.plan.first = reinterpret_cast<uint32_t*>(ints(all));
   for (int i = 0; i < 2; ++i) {
     w.row_o[i] = reinterpret_cast<float*>(take(rows * D * 4));
     w.row_part[i] = reinterpret_cast<kv4::RowPart*>(take(rows * sizeof(kv4::RowPart)));
@@ -175,8 +175,8 @@ int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype
   a.n_groups = n_groups;
   a.plan_len = w.plan.len;
   a.plan_extra = w.plan.extra;
-  a.group_seq = w.plan.group_seq;
-  a.group_row = w.plan.group_row;
+  a.plan_first = w.plan.first;
+  a.by_Hq = kv4::Divisor(Hq);
   for (int i = 0; i < 2; ++i) a.row_o[i] = w.row_o[i], a.row_part[i] = w.row_part[i];
   a.part_o = w.part_o;
   a.part_ml = w.part_ml;

@@ -75,7 +75,7 @@ constexpr unsigned kMostP = 0x7800;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaitPolls = 1 << 20;  // bound of every wait
 
-template <int D_, int NT_>
+template <int D_, int NT_, Mode M_>
 struct AttnCfg {
   static constexpr int D = D_, NT = NT_;
   static constexpr int MB = D == 256 ? 2 : 1;  // 128-channel blocks of O^T
@@ -97,8 +97,9 @@ struct AttnCfg {
   static constexpr int KU = 2, VU = 2;
   // of the K and V warps' units: with many rows all roles' loops together strain the
   // instruction cache (a 2048-token piece of a prompt: unrolled 377 us, rolled 365), with
-  // few they do less (131072 tokens: unrolled 37.3 us, rolled 38.4)
-  static constexpr int UNROLL = NT < 64 ? 8 : 1;
+  // few they do less (131072 tokens: unrolled 37.3 us, rolled 38.4), but where items are short
+  // (a window of 1,024 over 48 sequences: unrolled 41.7 us, rolled 41.1)
+  static constexpr int UNROLL = NT < 64 && M_ == kFull ? 8 : 1;
   static constexpr int cS = KW * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
   static_assert(cV + VU * VW * 16 * MB <= 512, "TMEM");
   // shared memory
@@ -125,7 +126,8 @@ struct Seg {
   int last;  // block that holds the item's last tile
   int near, skip;
   int lo;     // window: first position that the item's first node sees beside the sinks
-  int group;  // shared: the rows are those of a group's sequences, b the group
+  int group;  // shared: the rows are those of a group's sequences, b the first of them
+  int row;    // of the page table
 };
 
 // The tiles of an item.
@@ -194,8 +196,8 @@ constexpr int kHeads = 16;   // kv heads whose scales are
 
 template <typename C, Mode M>
 struct AttnShared {
-  // (kShared keeps a second number a sequence and half as many sequences)
-  static constexpr int LENS = M == kShared ? kLens / 2 : kLens;
+  // (kShared keeps three numbers a sequence, of fewer sequences)
+  static constexpr int LENS = M == kShared ? kLens * 3 / 8 : kLens;
   static constexpr int WIN = M == kWindow;
   uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
   uint64_t k_full[C::KU], k_empty[C::KU], v_full[C::VU], v_empty[C::VU];
@@ -223,6 +225,7 @@ struct AttnShared {
   AttnArgs args;
   int len[LENS];
   int extra[M == kShared ? LENS : 1];               // sequences of a group; first own tile
+  uint32_t first[M == kShared ? LENS : 1];          // a group's first sequence and table row
   int scan[32];                                     // of the warps' units
   float scale[2][kHeads];                           // k_scale, v_scale of the first kv heads
   uint2 seen[WIN ? 64 : 1];                         // window: of a node's path, what it sees
@@ -448,11 +451,15 @@ struct Lens {
   const AttnArgs& a;
   const int* kept;
   const int* kept_extra;
+  const uint32_t* kept_first;
   __device__ __forceinline__ int operator()(int v) const {
     return v < LENS ? kept[v] : attn_len_of<M>(a, v);
   }
   __device__ __forceinline__ int extra(int v) const {
     return M != kShared ? 0 : v < LENS ? kept_extra[v] : max(a.plan_extra[v], 0);
+  }
+  __device__ __forceinline__ uint32_t first(int v) const {
+    return v < LENS ? kept_first[v] : a.plan_first[v];
   }
 };
 
@@ -605,8 +612,33 @@ static __device__ __noinline__ Run attn_run(const AttnArgs& a, const Lens<M, LEN
     r.b = b0 + l;
     break;
   }
-  find_item<NT, M>(a, r, r.b, lens(r.b), lens.extra(r.b), its, r.at - before);
-  return r;
+  if (by_lane) {
+    find_item<NT, M>(a, r, r.b, lens(r.b), lens.extra(r.b), its, r.at - before);
+    return r;
+  }
+  // 32 row tiles of the head at once
+  const int per_head = a.by_Hkv(its), len = lens(r.b);
+  int in = r.at - before;
+  r.h = quotient(in, per_head);
+  in -= r.h * per_head;
+#pragma unroll 1
+  for (;; r.rt += 32) {
+    const int t = r.rt + lane < a.row_tiles ? attn_units<NT, M>(a, r.b, len, 0, r.rt + lane) : 0;
+    int upto = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, upto > in);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      r.rt += l;
+      r.u0 = in - (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, t, l));
+      return r;
+    }
+    in -= __shfl_sync(0xffffffffu, upto, 31);
+  }
 }
 
 // The same by all threads of the block, a thread a sequence (or group), of which there are at
@@ -679,9 +711,11 @@ static __device__ __noinline__ Seg attn_seg(const AttnArgs& a, const Lens<M, LEN
     s.rows = rows;
     s.near = span.near, s.skip = span.skip;
     if constexpr (M == kWindow) s.lo = attn_lo(a, len, rt);
+    s.row = b;
     if constexpr (M == kShared) {
       s.group = b < a.n_groups;
-      if (!s.group) s.b = b - a.n_groups;
+      const uint32_t first = lens.first(b);
+      s.b = first & 0xffff, s.row = first >> 16;
     }
     return s;
   }
@@ -715,19 +749,19 @@ static __device__ __noinline__ void attn_zero(const AttnArgs& a, const Lens<M, L
 template <int D, int NT, Mode M>
 static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, int b, int h, int row0,
                                                    int rows, int group, uint8_t* q, int warp) {
-  constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;  // channels of a lane
+  constexpr int E = D / 32, ROWS = AttnCfg<D, NT, M>::ROWS;  // channels of a lane
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
   const int row = row0 + r0 + lane % ROWS, node = a.by_G(row);  // over a group's sequences
   int n = node;
   if (M == kShared && group) {
     const int member = a.by_N(node);
-    b = a.group_seq[b] + member, n = node - member * a.N;
+    b += member, n = node - member * a.N;
   }
   const int64_t mine = b * a.q_stride_b + n * a.q_stride_n +
                        (int64_t)(h * a.G + row - node * a.G) * D;
   const uint16_t* src = static_cast<const uint16_t*>(a.q) + ch;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
-#pragma unroll
+#pragma unroll 1  // (run once an item: its instructions count more than its steps)
   for (int i = 0; i < ROWS; ++i) {
     const int r = r0 + i;
     uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
@@ -777,12 +811,12 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&x)[W]) 
 // prompt 385 -> 369 us, eight chains of 16 65.7 -> 63.3 us; with few rows finding it
 // costs more (48 uneven sequences 81 -> 83 us), and each row has its own.
 template <int D, int NT, Mode M>
-static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT>, M>& sh,
+static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<AttnCfg<D, NT, M>, M>& sh,
                                                int b, int len, int row0, int rows, int group,
                                                uint8_t* q, int warp, float to_log2) {
   const int G = a.G, Hq = a.Hq;
   const bool bf16 = a.bf16, tree = a.parent != nullptr && !(M == kShared && group);
-  constexpr int E = D / 32, ROWS = AttnCfg<D, NT>::ROWS;
+  constexpr int E = D / 32, ROWS = AttnCfg<D, NT, M>::ROWS;
   const int lane = threadIdx.x & 31, ch = lane * E, r0 = warp * ROWS;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
   auto place = [&](int r) { return q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); };
@@ -856,9 +890,9 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
                          : __half2float(__ushort_as_half((unsigned short)mine));
   const int e = (int)(__float_as_uint(top) >> 23);
   int most = 0, least = 255;  // of the rows but those of zeros, infinities and NaN
-  if constexpr (AttnCfg<D, NT>::COMMON) {
+  if constexpr (AttnCfg<D, NT, M>::COMMON) {
     if (lane < ROWS) sh.row_e[r0 + lane] = e;
-    tc::named_barrier(4, 128 * AttnCfg<D, NT>::NS);
+    tc::named_barrier(4, 128 * AttnCfg<D, NT, M>::NS);
 #pragma unroll
     for (int r = lane; r < NT; r += 32) {
       const int o = sh.row_e[r];
@@ -867,7 +901,7 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
   }
-  const bool same = AttnCfg<D, NT>::COMMON && most - least <= 8;
+  const bool same = AttnCfg<D, NT, M>::COMMON && most - least <= 8;
   // the largest magnitude to [2^8, 2^9)
   const int of = same ? most : e;
   const int up = of == 0 || of == 255 ? 127 : min(262 - of, 252);
@@ -908,8 +942,8 @@ static __device__ __noinline__ float attn_rows(const AttnArgs& a, AttnShared<Att
 
 // ---------------------------------------------------------------- the kernel
 template <int D, int NT, Mode M>
-__global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = AttnCfg<D, NT>;
+__global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+  using C = AttnCfg<D, NT, M>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShared<C, M> sh;
   constexpr int LENS = AttnShared<C, M>::LENS;
@@ -948,7 +982,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   // wait on the kernel before this one, from the lengths as they read then, and
   // again after it in the case that one of them has changed (with more sequences
   // than are kept, always).  kShared reads its plan's numbers, which that kernel writes.
-  const Lens<M, LENS> lens = {args, sh.len, sh.extra};
+  const Lens<M, LENS> lens = {args, sh.len, sh.extra, sh.first};
   const bool kept = attn_count<M>(a) <= LENS;
   const bool by_thread = (M == kShared || (M == kWindow && a.row_tiles <= 4)) &&
                          attn_count<M>(a) <= C::THREADS;
@@ -968,9 +1002,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
     __syncthreads();
     if (kept) find_run();
   }
+  const bool softmax = warp >= C::wS && warp < C::wI;
   __syncthreads();
   pdl_enter();
-  const bool softmax = warp >= C::wS && warp < C::wI;
   if (threadIdx.x < 2 * kHeads) {
     const int h = threadIdx.x & (kHeads - 1);
     const float* scales = threadIdx.x < kHeads ? a.c.k_scale : a.c.v_scale;
@@ -980,7 +1014,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
   if constexpr (M == kShared) {
 #pragma unroll 1
     for (int v = threadIdx.x; v < min(attn_count<M>(a), LENS); v += C::THREADS)
-      sh.len[v] = a.plan_len[v], sh.extra[v] = max(a.plan_extra[v], 0);
+      sh.len[v] = a.plan_len[v], sh.extra[v] = max(a.plan_extra[v], 0), sh.first[v] = a.plan_first[v];
     __syncthreads();
     find_run();
   } else {
@@ -1361,8 +1395,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
         continue;
       }
       const bool whole = !PARTS && e.t0 == 0 && e.t1 == e.tiles;
-      const int first = PARTS && e.group ? a.group_seq[e.b] : e.b;
-      const int64_t item = (int64_t)first * a.N * a.Hq + e.h * a.G;  // output row of node 0
+      const int64_t item = (int64_t)e.b * a.N * a.Hq + e.h * a.G;  // output row of node 0
       const int64_t slot = PARTS ? blockIdx.x : 2 * (int64_t)blockIdx.x + (seg_no > 0);
       {
         float x[C::NH];
@@ -1547,8 +1580,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::THREADS, 1) attn_kernel(const 
       } else if (!next_seg()) {
         break;
       }
-      const int row = M == kShared && s.group ? a.group_row[s.b] : s.b;
-      const int32_t* table = a.c.table + (int64_t)row * a.c.table_stride;
+      const int32_t* table = a.c.table + (int64_t)(M == kShared ? s.row : s.b) * a.c.table_stride;
       const uint8_t* head = static_cast<const uint8_t*>(a.c.pages) + from +
                             (int64_t)s.h * (a.c.page_tokens / kRec) * rec_bytes(D);
       // this lane's position, as an entry of the table and an offset in the page, two
@@ -1726,7 +1758,7 @@ join_kernel(const __grid_constant__ AttnArgs a, int NT) {
 
 template <int D, int NT, Mode M>
 int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
-  using C = AttnCfg<D, NT>;
+  using C = AttnCfg<D, NT, M>;
   if (cudaFuncSetAttribute(attn_kernel<D, NT, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::SMEM) != cudaSuccess) {
     (void)cudaGetLastError();

@@ -68,9 +68,9 @@ struct AttnArgs {
   // kShared: of the groups and then of the sequences, the shared length and the length (0: it is
   // skipped); a group's sequences and a sequence's first own tile (-1: it is skipped)
   const int32_t *plan_len, *plan_extra;
-  const int32_t* group_seq;  // a group's first sequence,
-  const int32_t* group_row;  // and the table row that its shared pages are taken from
+  const uint32_t* plan_first;  // and the first sequence (in 16 bits) and row of the page table (16)
   int n_groups;
+  Divisor by_Hq;
   float* row_o[2];           // [B*N*Hq][D], each row's first own part; and first shared one
   RowPart* row_part[2];      // [B*N*Hq]
 };
@@ -104,7 +104,8 @@ inline void row_tiles(int rows, int* tiles, int* per_tile) {
 // gdn_kv4_shared.cu: the numbers of AttnArgs that a kShared pass reads, and the sum of the parts
 // that it leaves (`rows`: of a slot of part_o).
 struct SharedPlan {
-  int32_t *len, *extra, *group_seq, *group_row;
+  int32_t *len, *extra;
+  uint32_t* first;
 };
 int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
                            const int32_t* group, int n_groups, const SharedPlan& plan,

@@ -19,24 +19,52 @@ constexpr int kTile = 128;
 constexpr float kNone = -3.402823466e38f;
 
 // ---------------------------------------------------------------- plan
-// A block a group.  The group's first sequence with a whole tile before its block is the one
-// whose table row the shared pages are taken from; the others share with it what lies on the
-// same pages of both, in whole tiles.  What all of those share that share a tile at all is the
-// group's prefix.  Bound by the latency of the lengths and of the rows' entries after them.
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kKept = 512;  // sequences of a group whose numbers stay in shared memory
+// A cluster of blocks a group, a share of its sequences each.  The group's first sequence with a
+// whole tile before its block is the one whose table row the shared pages are taken from; the
+// others share with it what lies on the same pages of both, in whole tiles.  What all of those
+// share that share a tile at all is the group's prefix.  Bound by the latency of the lengths and
+// of the rows' entries after them.
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32, kPlanBlocks = 8;
+constexpr int kKept = 512;  // sequences of a share whose numbers stay in shared memory
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t x;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(x));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t x;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(x));
+  return x;
+}
+
+// Every thread of the cluster; what was written before it is seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::
+                   : "memory");
+}
+
+// A word of shared memory of block `rank` of the cluster.
+__device__ __forceinline__ int cluster_load(const int* p, uint32_t rank) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  int x;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
             const int32_t* __restrict__ group, int n_groups, SharedPlan plan) {
-  __shared__ int ref, shortest, sharers;
+  __shared__ int ref, shortest;
   __shared__ int differ[kPlanWarps];  // first entry of a sequence's row that is another page
   __shared__ int kept[kKept];
   int32_t* start = plan.extra + n_groups;  // -1 for a sequence that is skipped
-  int32_t* lens = plan.len + n_groups;
-  const int g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int blocks = cluster_size(), rank = cluster_rank(), g = blockIdx.x / blocks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_enter();
-  if (tid == 0) ref = c.B, shortest = 0x7fffffff, sharers = 0;
+  if (tid == 0) ref = c.B, shortest = 0x7fffffff;
   bool ok = true;
   for (int i = tid; i <= n_groups; i += kPlanThreads) {
     const int x = group[i];
@@ -44,7 +72,10 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
   }
   const int lo = group[g], hi = group[g + 1];
   ok = __syncthreads_and(ok);
-  // tokens before a sequence's block, -1 for one that is skipped; by a warp
+  if (!ok && g == 0 && rank == 0 && tid == 0) report(c.status, GDN_ERR_ROW_RANGE);
+  const int first = ok ? lo : 0, end = ok ? hi : 0;
+  // tokens before a sequence's block, -1 for one that is skipped; by a warp, which writes down
+  // the sequence's numbers
   auto before = [&](int b) {
     int len = seq_len(c, b, lane == 0);
     if (len > 0 && parent != nullptr) {
@@ -59,80 +90,87 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
         len = 0;
       }
     }
-    if (lane == 0) lens[b] = len;
+    if (lane == 0) plan.len[n_groups + b] = len, plan.first[n_groups + b] = b | (uint32_t)b << 16;
     return len > 0 ? max(len - N, 0) : -1;
   };
-  if (!ok && g == 0 && tid == 0) report(c.status, GDN_ERR_ROW_RANGE);
-  const int first = ok ? lo : 0, end = ok ? hi : 0;
   if (g == 0) {  // sequences of no group
     const int from = ok ? group[0] : c.B, to = ok ? group[n_groups] : c.B;
-    for (int i = warp; i < from + c.B - to; i += kPlanWarps) {
+    for (int i = rank * kPlanWarps + warp; i < from + c.B - to; i += blocks * kPlanWarps) {
       const int b = i < from ? i : to + i - from, x = before(b);
       if (lane == 0) start[b] = x < 0 ? -1 : 0;
     }
   }
-  // of sequence first + i: tokens before its block, where they are a tile, then tiles shared
-  int32_t* held = end - first <= kKept ? kept : start + first;
-  for (int b = first + warp; b < end; b += kPlanWarps) {
-    const int x = before(b);
-    if (lane == 0) {
-      held[b - first] = x < kTile ? min(x, 0) : x;
-      if (x >= kTile) atomicMin(&ref, b);
-    }
+  // the first sequence with a tile (whether or not its tree is one: its pages serve as well)
+  for (int b = first + tid; b < end; b += kPlanThreads)
+    if (seq_len(c, b, false) - N >= kTile) atomicMin(&ref, b);
+  // this block's sequences are first + rank, first + rank + blocks, ..
+  const int mine = end - first > rank ? (end - first - rank + blocks - 1) / blocks : 0;
+  auto seq = [&](int i) { return first + rank + i * blocks; };
+  // of sequence seq(i): tokens before its block, then tiles shared (kept, or in its place)
+  auto held = [&](int i) -> int& { return mine <= kKept ? kept[i] : start[seq(i)]; };
+  for (int i = warp; i < mine; i += kPlanWarps) {
+    const int x = before(seq(i));
+    if (lane == 0) held(i) = x < kTile ? min(x, 0) : x;
   }
   __syncthreads();
-  const int r = ref;
-  if (r < end) {
-    const int most = held[r - first];
-    const int32_t* row = c.table + (int64_t)r * c.table_stride;
-    // up to kPlanWarps sequences at once, the warps spread over them
-    for (int b0 = r + 1; b0 < end; b0 += kPlanWarps) {
-      const int count = min(end - b0, kPlanWarps), each = kPlanWarps / count;
-      if (tid < kPlanWarps) differ[tid] = 0x7fffffff;
-      __syncthreads();
-      const int m = warp / each, turn = warp % each, b = b0 + m;
-      if (m < count) {
-        const int common = min(held[b - first], most);
-        const int pages = common <= 0 ? 0 : (common + c.page_tokens - 1) / c.page_tokens;
-        const int32_t* mine = c.table + (int64_t)b * c.table_stride;
-        constexpr int U = 16;
-        for (int j0 = turn * 32 * U; j0 < pages; j0 += each * 32 * U) {
-          int other[U];
+  const int r = ref, most = r < end ? seq_len(c, r, false) - N : 0;
+  const int32_t* row = c.table + (int64_t)(r < end ? r : 0) * c.table_stride;
+  // up to kPlanWarps sequences at once, the warps spread over them
+  for (int i0 = 0; i0 < mine; i0 += kPlanWarps) {
+    const int count = min(mine - i0, kPlanWarps), each = kPlanWarps / count;
+    if (tid < kPlanWarps) differ[tid] = 0x7fffffff;
+    __syncthreads();
+    const int m = warp / each, turn = warp % each, b = seq(i0 + m);
+    if (m < count && b != r) {
+      const int common = min(held(i0 + m), most);
+      const int pages = common <= 0 ? 0 : (common + c.page_tokens - 1) / c.page_tokens;
+      const int32_t* other = c.table + (int64_t)b * c.table_stride;
+      constexpr int U = 8;
+      for (int j0 = turn * 32 * U; j0 < pages; j0 += each * 32 * U) {
+        int x[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int j = j0 + u * 32 + lane;
-            other[u] = j < pages ? mine[j] ^ row[j] : 0;
-          }
-          int at = 0x7fffffff;
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * 32 + lane;
+          x[u] = j < pages ? other[j] ^ row[j] : 0;
+        }
+        int at = 0x7fffffff;
 #pragma unroll
-          for (int u = U - 1; u >= 0; --u)
-            if (other[u] != 0) at = j0 + u * 32 + lane;
-          at = __reduce_min_sync(0xffffffffu, at);
-          if (at != 0x7fffffff) {
-            if (lane == 0) atomicMin(&differ[m], at);
-            break;
-          }
+        for (int u = U - 1; u >= 0; --u)
+          if (x[u] != 0) at = j0 + u * 32 + lane;
+        at = __reduce_min_sync(0xffffffffu, at);
+        if (at != 0x7fffffff) {
+          if (lane == 0) atomicMin(&differ[m], at);
+          break;
         }
       }
-      __syncthreads();
-      if (tid < count) {
-        const int base = held[b0 + tid - first];
-        const int64_t same = (int64_t)differ[tid] * c.page_tokens;
-        const int tiles = base <= 0 ? 0 : (int)min((int64_t)min(base, most), same) / kTile;
-        if (base >= 0) held[b0 + tid - first] = tiles;
-        if (tiles > 0) atomicMin(&shortest, tiles), atomicAdd(&sharers, 1);
-      }
-      __syncthreads();
     }
+    __syncthreads();
+    if (tid < count) {
+      int& x = held(i0 + tid);
+      const int64_t same = (int64_t)differ[tid] * c.page_tokens;
+      if (x > 0) {
+        x = (int)min((int64_t)min(x, most), same) / kTile;
+        if (x > 0 && seq(i0 + tid) != r) atomicMin(&shortest, x);
+      }
+    }
+    __syncthreads();
   }
-  const int tiles = sharers > 0 ? shortest : 0;
-  for (int i = tid; i < end - first; i += kPlanThreads)
-    start[first + i] = held[i] > 0 ? tiles : held[i];
-  if (tid == 0) {
+  // over the group's blocks
+  int least = shortest;
+  if (blocks > 1) {
+    cluster_sync();
+    for (int k = 0; k < blocks; ++k) least = min(least, cluster_load(&shortest, k));
+    cluster_sync();  // no block ends while its memory is read
+  }
+  const int tiles = least == 0x7fffffff ? 0 : least;  // (nobody shares with the first)
+  for (int i = tid; i < mine; i += kPlanThreads) {
+    const int x = held(i);
+    start[seq(i)] = x > 0 ? tiles : x;
+  }
+  if (tid == 0 && rank == 0) {
     plan.len[g] = tiles * kTile;
     plan.extra[g] = end - first;
-    plan.group_seq[g] = first;
-    plan.group_row[g] = r < end ? r : first;
+    plan.first[g] = first | (uint32_t)(r < end ? r : first) << 16;
   }
 }
 
@@ -150,23 +188,21 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, int NT, int blocks) {
   __shared__ float2 sums[NP];
   pdl_enter();
   const int quad = threadIdx.x % Q, lot = threadIdx.x / Q;
-  const int64_t row = ONE_ROW ? blockIdx.x : (int64_t)blockIdx.x * NP + lot;
-  if (row >= (int64_t)a.c.B * a.N * a.Hq) return;  // ONE_ROW: none
-  const int64_t node = row / a.Hq;
-  const int b = (int)(node / a.N), n = (int)(node % a.N), head = (int)(row % a.Hq);
+  const int row = ONE_ROW ? blockIdx.x : blockIdx.x * NP + lot;  // (31 bits hold them)
+  if (row >= a.c.B * a.N * a.Hq) return;  // ONE_ROW: none
+  const RowPart part[2] = {a.row_part[0][row], a.row_part[1][row]};  // (of a pass before, maybe)
+  const int node = a.by_Hq(row), b = a.by_N(node), n = node - b * a.N, head = row - node * a.Hq;
   const int from = a.plan_extra[a.n_groups + b];
   const bool there = from >= 0 && a.plan_len[a.n_groups + b] - a.N + n >= 0;
   // first block, parts and row of the own (0) and the shared side (1); (a pass whose waits ran
   // out may have left no numbers here, so they are kept in range)
-  RowPart head_of[2] = {};
-  int first[2] = {}, at[2] = {}, count[2] = {};
+  int first[2], at[2], count[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (!there || (i == 1 && from == 0)) continue;
-    head_of[i] = a.row_part[i][row];
-    first[i] = min(head_of[i].blocks & 0xffff, blocks - 1);
-    at[i] = min(max(head_of[i].row, 0), NT - 1);
-    count[i] = min(max((head_of[i].blocks >> 16 & 0xffff) - first[i], 0), blocks - 1 - first[i]) + 1;
+    first[i] = min(part[i].blocks & 0xffff, blocks - 1);
+    at[i] = min(max(part[i].row, 0), NT - 1);
+    count[i] = min(max((part[i].blocks >> 16 & 0xffff) - first[i], 0), blocks - 1 - first[i]) + 1;
+    if (!there || (i == 1 && from == 0)) count[i] = 0;
   }
   const int parts = count[0] + count[1];
   float top = kNone, sum = 0.f;
@@ -186,9 +222,8 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, int NT, int blocks) {
         const bool shared = i >= count[0];
         const int k = shared ? i - count[0] : i;
         if (k == 0) {
-          ml[u] = shared ? make_float2(head_of[1].m, head_of[1].l)
-                         : make_float2(head_of[0].m, head_of[0].l);
-          p[u] = __ldcg(reinterpret_cast<const float4*>(a.row_o[shared] + row * D) + quad);
+          ml[u] = shared ? make_float2(part[1].m, part[1].l) : make_float2(part[0].m, part[0].l);
+          p[u] = __ldcg(reinterpret_cast<const float4*>(a.row_o[shared] + (int64_t)row * D) + quad);
         } else {
           const int64_t slot = (int64_t)((shared ? first[1] : first[0]) + k) * NT +
                                (shared ? at[1] : at[0]);
@@ -229,12 +264,12 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, int NT, int blocks) {
     }
   }
   const float inv =
-      sum != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[head / a.G] : 1.f) / sum : 0.f;
+      sum != 0.f ? (a.c.v_scale != nullptr ? a.c.v_scale[a.by_G(head)] : 1.f) / sum : 0.f;
   const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   uint16_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = a.bf16 ? Elem<GDN_BF16>::from(v[i]) : Elem<GDN_F16>::from(v[i]);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + quad * 4) =
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (int64_t)row * D + quad * 4) =
       make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
   if (a.lse != nullptr && quad == 0)
     a.lse[row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -256,8 +291,26 @@ int join_d(const AttnArgs& a, int NT, int blocks, cudaStream_t s) {
 int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
                            const int32_t* group, int n_groups, const SharedPlan& plan,
                            cudaStream_t s) {
-  return launch_pdl(plan_kernel, dim3(n_groups), dim3(kPlanThreads), 0, s, c, N, parent, group,
-                    n_groups, plan);
+  // several blocks where the usual group has many sequences: 32 of 520 pages take 8 us less in
+  // eight, eight of 133 2 us more
+  const int blocks = c.B > 8 * (int64_t)n_groups ? kPlanBlocks : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n_groups * blocks);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, plan_kernel, c, N, parent, group, n_groups, plan) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  return launch_status();
 }
 
 int launch_kv4_shared_join(const kv4::AttnArgs& a, int rows, int blocks, cudaStream_t s) {
