@@ -208,7 +208,7 @@ shared_join_kernel(const __grid_constant__ AttnArgs a, int NT, int blocks) {
   float top = kNone, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto larger = [](float p, float q) { return q > p || q != q ? q : p; };  // NaN stays
-  constexpr int U = 8;
+  constexpr int U = ONE_ROW ? 4 : 2;
 #pragma unroll 1
   for (int i0 = ONE_ROW ? lot : 0; i0 < parts; i0 += U * STEP) {
     float2 ml[U];
