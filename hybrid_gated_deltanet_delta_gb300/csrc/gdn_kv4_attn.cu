@@ -140,6 +140,24 @@ bool rows_worth_sharing(int N, int G) {
   return rows <= 2 * kv4::kMaxRows && 4 * tiles * kv4::kMaxRows >= 5 * rows;
 }
 
+// And whether it does by the most that there can be to read: plan, longer prologue and join
+// cost some 12 us, and the more rows a sequence has the less there is to win.  Measured (shared /
+// each sequence for itself, us; W: tiles of 128, and six more an item, of all items at the
+// table's width):
+//   rows of a kv head      W too small                       W large enough
+//    4, D 128    2,176: 26 / 20   4,352: 31 / 31     5,248: 27 / 35   17,536: 34 / 92
+//    6, D 256    2,176: 31 / 27   2,624: 29 / 32     5,248: 34 / 48   35,072: 77 / 223
+//   24, D 256    2,624: 38 / 36   4,352: 49 / 53    10,496: 70 / 102  35,072: 135 / 275
+//   32, D 128    5,248: 49 / 44  10,496: 72 / 74    20,992: 112 / 134 70,144: 278 / 419
+//   48, D 256    5,248: 63 / 61   8,768: 78 / 89    17,536: 129 / 164 35,072: 230 / 309
+//   66, D 256    5,248: 74 / 75   8,768: 98 / 111   17,536: 165 / 199 35,072: 326 / 379
+bool worth_sharing(const gdn_kv4_cache& c, int rows, int row_tiles, int n_groups) {
+  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128 + 6;
+  const int64_t most = (int64_t)c.B * c.Hkv * row_tiles * tiles;
+  return c.B > n_groups &&
+         most * c.D >= 500000 + 22000 * (int64_t)(rows < kv4::kMaxRows ? rows : kv4::kMaxRows);
+}
+
 }  // namespace
 
 size_t kv4_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int n_groups) {
@@ -158,7 +176,7 @@ int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype
   if (parts == 0) return GDN_ERR_CUDA;
   AttnArgs a = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
   if (!countable(c, (int64_t)a.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
-  if (!rows_worth_sharing(N, a.G))
+  if (!rows_worth_sharing(N, a.G) || !worth_sharing(c, a.rows_total, a.row_tiles, n_groups))
     return launch_kv4_attention(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse, workspace, s);
   // the rows of a group as if they were one sequence's, in tiles as wide as a group of the
   // usual size fills

@@ -583,8 +583,10 @@ int gdn_kv4_attention_window(const gdn_kv4_cache* c, const void* q, int32_t dtyp
  * the same pages, from the first position on and in whole tiles of 128, in all sequences of the
  * group that share a tile with the first of it.  A group that shares nothing is right as well,
  * and a sequence that is skipped does not count.  Offsets that are not ascending within [0, B]
- * are reported (GDN_ERR_ROW_RANGE), and nothing is shared then; where a sequence's rows fill the
- * tensor cores' tiles by themselves, sharing saves nothing and the offsets are not looked at.
+ * are reported (GDN_ERR_ROW_RANGE), and nothing is shared then.  Where sharing cannot pay by the
+ * sizes (the rows of a sequence fill the tensor cores' tiles by themselves, the table's width
+ * leaves little to read, or there are as many groups as sequences) every sequence is read for
+ * itself, and the offsets are not looked at.
  *
  * The result is gdn_kv4_attention's up to the order of the sums, which depends on the lengths,
  * the table, the groups and the device alone.  The workspace

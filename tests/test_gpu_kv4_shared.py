@@ -14,12 +14,14 @@ pytestmark = pytest.mark.gpu
 
 class Branches:
     """Sequences of several groups: the first shared[g] pages of a group's are the same ones.
-    groups: (members, shared pages); lens: of all sequences."""
+    groups: (members, shared pages); lens: of all sequences.  The table is as wide as a
+    million tokens, so that sharing pays by the sizes (narrow=True: no wider than
+    needed, and each sequence is read for itself)."""
 
-    def __init__(self, rng, groups, lens, H, D, P):
+    def __init__(self, rng, groups, lens, H, D, P, narrow=False):
         self.H, self.D, self.P, self.lens = H, D, P, np.asarray(lens)
         held = [-(-max(0, n) // P) for n in lens]
-        self.width = max(1, max(held)) + 1
+        self.width = max(held) + 1 if narrow else -(-(1 << 20) // P)
         n_pages = sum(held) + 2
         order = list(rng.permutation(n_pages))
         self.table = np.full((len(lens), self.width), -1, np.int64)
@@ -103,10 +105,11 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("narrow", [False, True])
 @pytest.mark.parametrize("dtype, groups, lens, N, Hq, H, D, P, tree", CASES)
-def test_shared(gpu_lib, dtype, groups, lens, N, Hq, H, D, P, tree):
+def test_shared(gpu_lib, dtype, groups, lens, N, Hq, H, D, P, tree, narrow):
     rng = np.random.default_rng(sum(lens) + N * D + Hq)
-    s = Branches(rng, groups, lens, H, D, P)
+    s = Branches(rng, groups, lens, H, D, P, narrow)
     parent = rand_trees(rng, len(lens), N) if tree else None
     q = queries(rng, len(lens), N, Hq, D, dtype)
     o, lse = s.attend(gpu_lib, q, parent)
@@ -145,7 +148,7 @@ def test_skipped_sequences_leave_the_group_its_prefix(gpu_lib):
     q = queries(rng, 6, 5, 4, 128, "bf16")
     parent = rand_trees(rng, 6, 5)
     for row, n, code in ((0, -1, gpu_lib.GDN_ERR_ROW_RANGE), (2, 0, 0),
-                         (3, 1 << 20, gpu_lib.GDN_ERR_ROW_RANGE),
+                         (3, 1 << 21, gpu_lib.GDN_ERR_ROW_RANGE),
                          (4, None, gpu_lib.GDN_ERR_BAD_TREE)):
         lens, par = s.lens.copy(), parent.copy()
         if n is None:
@@ -222,7 +225,7 @@ def test_many_sequences(gpu_lib):
     rng = np.random.default_rng(46)
     B = 1300
     lens = rng.integers(128, 160, B)
-    s = Branches(rng, [(2, 4)] * 600 + [(100, 4)], lens, 1, 64, 32)
+    s = Branches(rng, [(2, 4)] * 600 + [(100, 4)], lens, 1, 64, 32, narrow=True)
     q = queries(rng, B, 1, 2, 64, "f16")
     o, lse = s.attend(gpu_lib, q)
     assert int(s.status.item()) == 0
@@ -275,7 +278,7 @@ def test_rounds_of_branches(gpu_lib):
     H, Hq, D, P, N, F, prompt = 2, 6, 64, 32, 5, 3, 170
     n_pages = 12
     pages = t.zeros(n_pages, H, 1, 36 * D, dtype=t.uint8, device="cuda")
-    table, kv_len = i32(np.full((F + 1, 12), -1)), i32(np.zeros(F + 1))
+    table, kv_len = i32(np.full((F + 1, 32768), -1)), i32(np.zeros(F + 1))
     holders, status = i32(np.zeros(n_pages)), status_word()
     ws = t.empty(max(gpu_lib.gdn_kv4_reserve_workspace_bytes(F),
                      gpu_lib.gdn_kv4_attention_workspace_bytes(F, N, Hq, H, D),
