@@ -1677,7 +1677,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
 // each), 5.2 us for one sequence (4 items, 38 parts each).
 constexpr int kJoinThreads = 256;
 
-template <int D, bool ONE_ROW>
+template <int D, bool ONE_ROW, int U>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const __grid_constant__ AttnArgs a, int NT) {
   constexpr int Q = D / 4, NP = kJoinThreads / Q, STEP = ONE_ROW ? NP : 1;
@@ -1692,37 +1692,53 @@ join_kernel(const __grid_constant__ AttnArgs a, int NT) {
   auto at = [&](int i) {
     return (i == 0 ? (int64_t)j.slot : 2 * ((int64_t)blockIdx.x + i)) * NT + r;
   };
-  // a running maximum, so that nothing is read twice and the reads overlap
+  // a running maximum, raised eight parts at a time, so that nothing is read twice and the reads
+  // overlap: those of U parts
+  constexpr int E = 8;
   float top = kNone, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto larger = [](float p, float q) { return q > p || q != q ? q : p; };  // NaN stays
-  constexpr int U = 8;
 #pragma unroll 1
-  for (int i0 = ONE_ROW ? group : 0; i0 < parts; i0 += U * STEP) {
-    float2 ml[U];
+  for (int i0 = ONE_ROW ? group : 0; i0 < parts; i0 += E * STEP) {
+    float2 ml[E];
     float4 p[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < E; ++u) {
       const int i = i0 + u * STEP;
       ml[u] = make_float2(kNone, 0.f);
-      p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (u < U) p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < parts) {
         ml[u] = a.part_ml[at(i)];
-        p[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
+        if (u < U) p[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
       }
     }
     float m = top;
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = larger(m, ml[u].x);
+    for (int u = 0; u < E; ++u) m = larger(m, ml[u].x);
     const float keep = exp2_fast(top - m);
     top = m;
     sum *= keep;
     o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+    auto add = [&](float2 of, float4 x) {
+      const float w = exp2_fast(of.x - m);
+      sum += w * of.y;
+      o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+    };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float w = exp2_fast(ml[u].x - m);
-      sum += w * ml[u].y;
-      o.x += w * p[u].x, o.y += w * p[u].y, o.z += w * p[u].z, o.w += w * p[u].w;
+    for (int u = 0; u < U; ++u) add(ml[u], p[u]);
+    if constexpr (U < E) {
+#pragma unroll
+      for (int u0 = U; u0 < E; u0 += U) {
+        if (i0 + u0 * STEP >= parts) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + (u0 + u) * STEP;
+          p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < parts) p[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * D) + quad);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(ml[u0 + u], p[u]);
+      }
     }
   }
   if constexpr (ONE_ROW) {
@@ -1768,10 +1784,15 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
   if (rc != GDN_OK || M == kShared) return rc;  // (joined by shared_join_kernel)
   const dim3 block(kJoinThreads);
   if (NT == 16)
-    return launch_pdl(join_kernel<D, true>, dim3(parts, a.rows_per_tile), block, 0, s, a, NT);
+    return launch_pdl(join_kernel<D, true, 8>, dim3(parts, a.rows_per_tile), block, 0, s, a, NT);
   constexpr int NP = kJoinThreads / (D / 4);
-  return launch_pdl(join_kernel<D, false>, dim3(parts, (a.rows_per_tile + NP - 1) / NP), block, 0,
-                    s, a, NT);
+  const dim3 grid(parts, (a.rows_per_tile + NP - 1) / NP);
+  // Few parts an item: two in flight, and more threads.  A 2048-token piece of a prompt through
+  // a window of 1,024 (512 items) takes 106.4 us with two and 110.3 with eight, a tree of 22
+  // nodes at 32,768 tokens (8 items of 19 parts) 43.6 and 41.8.
+  if ((int64_t)a.c.B * a.c.Hkv * a.row_tiles * 8 >= parts)
+    return launch_pdl(join_kernel<D, false, 2>, grid, block, 0, s, a, NT);
+  return launch_pdl(join_kernel<D, false, 8>, grid, block, 0, s, a, NT);
 }
 
 template <int D, Mode M>
