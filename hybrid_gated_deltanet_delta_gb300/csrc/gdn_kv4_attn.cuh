@@ -1238,7 +1238,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
                                         : (at + 1) * kTile - 1 > base + n_lo) ||
                    (M == kWindow && (at + 1) * kTile > a.sinks && at * kTile < hi)) {
           const int j = at * kTile + quarter * 32 + lane, u = j - base;
-          if (!((ok >> quarter) & 1)) {
+          if (!((ok >> quarter) & 1) || u >= a.N) {
+            // (what lies past the end was not copied, and rows past the last node would see it:
+            // a NaN there raised all rows' references at every tile)
             vis = 0;
           } else if (a.parent == nullptr) {
             // nodes rise with the rows: the first row of node u
