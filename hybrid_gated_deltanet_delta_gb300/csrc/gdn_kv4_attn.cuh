@@ -1,5 +1,5 @@
 // Attention over the 4-bit key/value cache on the fifth-generation tensor cores
-// (include/gdn.h; instantiated per head size by gdn_kv4_attn_*.cu).
+// (include/gdn.h; instantiated per head size and mode by gdn_kv4_{attn,window,shared}_*.cu).
 //
 //     o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q.k_j - m),  c = scale * k_scale * log2 e
 //
@@ -18,6 +18,14 @@
 // the lengths itself; the grid depends on the device alone).  A block whose run
 // starts or ends inside an item writes that part's O, m and l to the workspace,
 // and join_kernel adds the parts in block order; whole items are written at once.
+//
+// A window (kWindow) leaves an item two stretches of tiles, the sinks' and its own, which are
+// numbered through; records of them that no row sees are not copied.  Where sequences share pages
+// (kShared, planned and joined by gdn_kv4_shared.cu) the run goes over two kinds of items: what a
+// group shares, with the rows of all its sequences one after another, and each sequence's tiles
+// behind it.  Either leaves parts: an item's first to its rows' own place, the others to the
+// block's.  A kernel is as wide as a usual group's rows; an item of fewer rows takes the softmax
+// groups and the products' columns that it has rows for.
 //
 // Warps of a block, connected by mbarriers only:
 //   4 of K      position = TMEM lane; codes * scale -> binary16 -> TMEM, in units of 64 or
@@ -43,16 +51,29 @@
 //
 // What bounds it.  With few rows the bytes: a tile of 36.8 KB (D = 256) takes 0.93 us a
 // block, 39.6 GB/s an SM of 43.8 measured for a copy; 131072 tokens of 4 heads take
-// 37.9 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
+// 38.7 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
 // item's output and the join.  With 96 rows the softmax warps: 1.6 us a tile, of which 0.5
 // us is the exponentials' issue at 80 registers, the tensor pipe 0.8 us; a 2048-token piece
-// of a prompt at 8192 tokens takes 362 to 371 us over runs, 975 to 997 TFLOP/s of 1,880
-// measured.
+// of a prompt at 8192 tokens takes 350 us, 1,030 TFLOP/s of 1,937 measured.
+//   Where items are short, what an item costs beside its tiles: 2.5 to 3.6 us with few rows, 8 us
+// with 96 (device timer, a block's softmax: sums and the next rows' copies 1 to 2.4 us, output
+// 0.3 to 1.8, rows to binary16 1.1 to 2, first product 0.5 to 1.1, first references 0.5 to 1.3).
+// A window of 1,024 over 48 uneven sequences of 32/8 heads of 128 takes 40.7 us (2.9 items a
+// block and 23 tiles of 0.83 us), a 2048-token piece of a prompt through it 106 us (3.9 items, 34
+// tiles of 1.6 us).  32 branches of 32,768 shared tokens: 61 us, 9 of them before the first
+// product (the plan's wait, then run, segment, rows), 1.54 us a tile, 6 for the join.  Much of
+// what is done once is bound by the fetch of its instructions: divisions by numbers that the host
+// knows as products, and rolled loops, took 4 of 47 us off the 48 sequences.
 // Measured and left out (us for 131072 tokens / the prompt, against the figure of the
 // time): the products issued by the K and V warps themselves, 55 / 500 against 50 / 464;
 // two streams of tiles, each with softmax warps, 58 / 693 against 50 / 464; steps of two
 // tiles with few rows, 41.8 against 39.9; a second group of K and V warps with few rows,
-// 170 against 152 for 48 sequences; softmax groups of 24 rows, - / 500 against 401.
+// 170 against 152 for 48 sequences; softmax groups of 24 rows, - / 500 against 401.  For a
+// window's short items: two blocks of 16 rows an SM, with half the tensor memory each, 47.4
+// against 47.2 (48 sequences; a tile takes 1.73 us then, 0.83 alone); queries brought in by warps
+// of their own, an item ahead, 42.2 against 40.7 with 16 rows (20 warps of 96 registers), 154
+// against 110 with 96 (one warp more: it takes 18 us for 96 rows); queries copied by one warp in
+// bulk copies of 128 bytes, 138 against 106.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -153,7 +174,9 @@ constexpr int kLead = 6;
 
 // Shared: tiles of an item of few rows and of one of many stand in one run, so units are finer
 // there: a tile counts 4 and 2 for each of the softmax groups with rows of the item, and what
-// goes with an item kSharedLead and kSharedMore for each of them.
+// goes with an item kSharedLead and kSharedMore for each of them.  Measured (32 branches of
+// 32,768 tokens / 8 x 8 draft chains / 2 x 8 draft trees, us): a lead of 16 82.5 / 114.8 / 170,
+// 30 + 6 a group 69.6 / 97.8 / 108.1, 40 + 6 67.1 / 94.3 / 109.3, 50 + 10 70.0 / 94.6 / 111.
 constexpr int kSharedLead = 40, kSharedMore = 6, kMostWeight = 10;
 template <int NT>
 __device__ __forceinline__ int row_groups(int rows) {

@@ -177,7 +177,10 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
 // ---------------------------------------------------------------- join
 // A thread has four channels of one row; with few rows (ONE_ROW) the block's threads share one
 // row and take every NP-th part each, else each D/4 of them take a row.  The parts are the own
-// pass's, in block order, and then the shared one's.
+// ones, in block order, and then the shared ones.  Bound by latency: the numbers of the plan and of
+// the row, then the parts; 6 us after the pass for 8,192 rows of 128 channels.  With eight parts
+// in flight 9.5 us, with two 6; one row a block up to 8 rows an SM (32 branches: 62.0 us in all,
+// up to 2 rows 66.6; 8 x 8 chains, always one row a block, 115.7 against 92.8).
 constexpr int kJoinThreads = 256;
 
 template <int D, bool ONE_ROW>

@@ -140,7 +140,7 @@ def test_shared_workspace_sizes(lib):  # noqa: F811
     size = lib.gdn_kv4_attention_shared_workspace_bytes
     plain = lib.gdn_kv4_attention_workspace_bytes
     assert size(32, 1, 24, 4, 256, 1) >= 2 * 32 * 24 * 256 * 4
-    assert size(32, 1, 24, 4, 256, 32) > size(32, 1, 24, 4, 256, 1)
+    assert size(32, 4, 24, 4, 256, 32) > size(32, 1, 24, 4, 256, 32) >= size(32, 1, 24, 4, 256, 1)
     assert size(32, 1, 24, 4, 256, 33) == 0 and size(32, 1, 24, 4, 256, 0) == 0
     assert size(0, 1, 24, 4, 256, 1) == 0 and size(8, 1, 25, 4, 256, 1) == 0
     assert size(8, 1, 24, 4, 80, 1) == 0
