@@ -176,8 +176,11 @@ int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype
   if (parts == 0) return GDN_ERR_CUDA;
   AttnArgs a = attn_args(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse);
   if (!countable(c, (int64_t)a.row_tiles * c.B)) return GDN_ERR_UNSUPPORTED;
-  if (!rows_worth_sharing(N, a.G) || !worth_sharing(c, a.rows_total, a.row_tiles, n_groups))
+  auto alone = [&]() {
     return launch_kv4_attention(c, q, dtype, qsb, qsn, N, Hq, scale, parent, o, lse, workspace, s);
+  };
+  if (!rows_worth_sharing(N, a.G) || !worth_sharing(c, a.rows_total, a.row_tiles, n_groups))
+    return alone();
   // the rows of a group as if they were one sequence's, in tiles as wide as a group of the
   // usual size fills
   const int64_t usual = (int64_t)((c.B + n_groups - 1) / n_groups) * a.rows_total;
@@ -186,7 +189,7 @@ int launch_kv4_attention_shared(const gdn_kv4_cache& c, const void* q, int dtype
   const int NT = round_rows(per_tile);
   // (items of the groups: their rows are the batch's; units of work are up to ten a tile)
   const int64_t items = (int64_t)c.B * a.rows_total / NT + n_groups + (int64_t)a.row_tiles * c.B;
-  if (!countable(c, 10 * items)) return GDN_ERR_UNSUPPORTED;
+  if (!countable(c, 10 * items)) return alone();
   const SharedSpace w = shared_space(workspace, c.B, N, Hq, c.D, n_groups, parts);
   int rc = launch_kv4_shared_plan(c, N, parent, group, n_groups, w.plan, s);
   if (rc != GDN_OK) return rc;

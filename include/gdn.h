@@ -53,7 +53,8 @@
  *    launched.  Errors that depend on device data (a malformed tree, an
  *    out-of-range accept index or slot) are written to the optional device
  *    word `status` (first error wins; the caller zeroes it) and the affected
- *    sequence is skipped; kernels never trap and never wait on other blocks.
+ *    sequence is skipped; kernels never trap and never wait on other blocks (but
+ *    for those of their own cluster, which the hardware runs together).
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -585,8 +586,9 @@ int gdn_kv4_attention_window(const gdn_kv4_cache* c, const void* q, int32_t dtyp
  * and a sequence that is skipped does not count.  Offsets that are not ascending within [0, B]
  * are reported (GDN_ERR_ROW_RANGE), and nothing is shared then.  Where sharing cannot pay by the
  * sizes (the rows of a sequence fill the tensor cores' tiles by themselves, the table's width
- * leaves little to read, or there are as many groups as sequences) every sequence is read for
- * itself, and the offsets are not looked at.
+ * leaves little to read, there are as many groups as sequences, or the work counted in tenths of
+ * tiles would not fit 31 bits) every sequence is read for itself, and the offsets are not looked
+ * at.
  *
  * The result is gdn_kv4_attention's up to the order of the sums, which depends on the lengths,
  * the table, the groups and the device alone.  The workspace

@@ -79,6 +79,15 @@ class Branches:
         assert t.equal(got[0][0], got[1][0]) and t.equal(got[0][1], got[1][1])
         return o, lse
 
+    def attend_once(self, gpu_lib, q):
+        t = torch()
+        kw = self.gpu()
+        o, lse = t.empty_like(q), t.empty(q.shape[:3], device="cuda")
+        gpu_lib.gdn_kv4_attention_shared(q, self.g_pages, self.g_table, self.g_len, self.g_group,
+                                         o, self.space(gpu_lib, q, len(self.group) - 1),
+                                         scale=q.shape[3] ** -0.5, lse=lse, **kw)
+        return o, lse
+
     def want(self, q, parent=None):
         N, D = q.shape[1], q.shape[3]
         return forms.attention(self.cache, self.table, self.lens, self.P, q.double().cpu().numpy(),
@@ -268,6 +277,97 @@ def test_two_graphs_with_workspaces_of_their_own(gpu_lib):
         for s, q, o, *_ in runs:
             assert int(s.status.item()) == 0
             forms.check(o, None, s.want(q), 500, DT["bf16"][1], 128)
+
+
+def test_a_large_group_in_a_graph(gpu_lib):
+    """One group of more sequences than a block of the plan takes, captured; replays follow the
+    table, and the bits are those of the call itself."""
+    rng, t = np.random.default_rng(49), torch()
+    s = Branches(rng, [(20, 6)], rng.integers(400, 480, 20), 1, 64, 64)
+    kw = s.gpu()
+    q = queries(rng, 20, 1, 4, 64, "f16")
+    o = t.empty(q.shape, dtype=q.dtype, device="cuda")
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        call = gpu_lib.bind_kv4_attention_shared(q, s.g_pages, s.g_table, s.g_len, s.g_group, o,
+                                                 s.space(gpu_lib, q, 1), scale=0.125, **kw)
+        call()
+        side.synchronize()
+        first = o.clone()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g, stream=side):
+            call()
+    for step in range(2):
+        if step:   # one row's third page becomes a page of its own, of the same contents
+            s.g_pages = None
+            spare = s.table[7, 6]
+            s.table[7, 2], s.lens[7] = spare, 300
+            s.pages[spare] = s.pages[s.table[0, 2]]
+            call._keep[2].copy_(cuda(s.pages))
+            s.g_table.copy_(i32(s.table))
+            s.g_len.copy_(i32(s.lens))
+        t.cuda.synchronize()
+        g.replay()
+        t.cuda.synchronize()
+        assert int(s.status.item()) == 0
+        assert step or t.equal(o, first)
+        forms.check(o, None, s.want(q), 480, DT["f16"][1], 64)
+
+
+def test_lengths_written_just_before_the_call(gpu_lib):
+    """Lengths and tables rewritten on the stream between calls that follow each other: every call
+    goes by what they are then."""
+    rng, t = np.random.default_rng(50), torch()
+    s = Branches(rng, [(4, 5), (3, 4)], [500, 480, 450, 470, 400, 390, 380], 2, 64, 64)
+    kw = s.gpu()
+    q = queries(rng, 7, 2, 4, 64, "bf16")
+    ws = [s.space(gpu_lib, q, 2), t.empty(gpu_lib.gdn_kv4_attention_workspace_bytes(7, 2, 4, 2, 64),
+                                          dtype=t.uint8, device="cuda")]
+    lens = [i32(s.lens - d) for d in (0, 130, 64, 250, 1, 300)]
+
+    def run(out, k):
+        if k % 2:
+            gpu_lib.gdn_kv4_attention_window(q, s.g_pages, s.g_table, s.g_len, out, ws[1],
+                                             scale=0.125, window=150, sinks=3, **kw)
+        else:
+            gpu_lib.gdn_kv4_attention_shared(q, s.g_pages, s.g_table, s.g_len, s.g_group, out,
+                                             ws[0], scale=0.125, **kw)
+
+    alone = []
+    for n in lens:
+        for k in range(2):
+            s.g_len.copy_(n)
+            t.cuda.synchronize()
+            alone.append(t.empty(q.shape, dtype=q.dtype, device="cuda"))
+            run(alone[-1], k)
+            t.cuda.synchronize()
+    for order in ((0, 1, 2, 3, 4, 5), (5, 3, 1, 0, 2, 4)):
+        outs = [t.empty(q.shape, dtype=q.dtype, device="cuda") for _ in alone]
+        for i in order:
+            for k in range(2):
+                t.add(lens[i], 0, out=s.g_len)
+                run(outs[2 * i + k], k)
+        t.cuda.synchronize()
+        for got, want in zip(outs, alone):
+            assert t.equal(got, want)
+    assert int(s.status.item()) == 0
+
+
+def test_a_nan_query_stays_with_its_rows(gpu_lib):
+    """A NaN and an infinity in one branch's queries: its rows are no numbers, the others' stay
+    within their bound."""
+    rng, t = np.random.default_rng(51), torch()
+    s = Branches(rng, [(5, 5)], [500, 480, 450, 470, 400], 2, 128, 64)
+    q = queries(rng, 5, 3, 4, 128, "bf16").contiguous()
+    want = s.want(q)
+    q[1, 2, 3, 5], q[3, 0, 0, 9] = float("nan"), float("inf")
+    o, lse = s.attend_once(gpu_lib, q)
+    bad = [(1, 2, 3), (3, 0, 0)]
+    for at in bad:
+        assert t.isnan(o[at]).any()
+        o[at], lse[at] = t.from_numpy(want[0][at]).to(o.dtype), float(want[1][at])
+    forms.check(o, lse, want, 500, DT["bf16"][1], 128)
 
 
 def test_rounds_of_branches(gpu_lib):
