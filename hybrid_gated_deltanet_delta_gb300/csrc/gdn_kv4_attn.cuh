@@ -19,8 +19,8 @@
 // starts or ends inside an item writes that part's O, m and l to the workspace,
 // and join_kernel adds the parts in block order; whole items are written at once.
 //
-// A window (kWindow) leaves an item two stretches of tiles, the sinks' and its own, which are
-// numbered through; records of them that no row sees are not copied.  Where sequences share pages
+// A window (kWindow) leaves an item two stretches of records, the sinks' and its own, which are
+// numbered through and taken four a tile.  Where sequences share pages
 // (kShared, planned and joined by gdn_kv4_shared.cu) the run goes over two kinds of items: what a
 // group shares, with the rows of all its sequences one after another, and each sequence's tiles
 // behind it.  Either leaves parts: an item's first to its rows' own place, the others to the
@@ -58,12 +58,13 @@
 //   Where items are short, what an item costs beside its tiles: 2.5 to 3.6 us with few rows, 8 us
 // with 96 (device timer, a block's softmax: sums and the next rows' copies 1 to 2.4 us, output
 // 0.3 to 1.8, rows to binary16 1.1 to 2, first product 0.5 to 1.1, first references 0.5 to 1.3).
-// A window of 1,024 over 48 uneven sequences of 32/8 heads of 128 takes 40.7 us (2.9 items a
-// block and 23 tiles of 0.83 us), a 2048-token piece of a prompt through it 106 us (3.9 items, 34
+// A window of 1,024 over 48 uneven sequences of 32/8 heads of 128 takes 37.0 us (2.9 items a
+// block and 21 tiles of 0.83 us), a 2048-token piece of a prompt through it 106 us (3.9 items, 34
 // tiles of 1.6 us).  32 branches of 32,768 shared tokens: 61 us, 9 of them before the first
 // product (the plan's wait, then run, segment, rows), 1.54 us a tile, 6 for the join.  Much of
 // what is done once is bound by the fetch of its instructions: divisions by numbers that the host
-// knows as products, and rolled loops, took 4 of 47 us off the 48 sequences.
+// knows as products, and rolled loops, took 4 of 47 us off the 48 sequences, and
+// records of sinks and window in common tiles 4 of 41.
 // Measured and left out (us for 131072 tokens / the prompt, against the figure of the
 // time): the products issued by the K and V warps themselves, 55 / 500 against 50 / 464;
 // two streams of tiles, each with softmax warps, 58 / 693 against 50 / 464; steps of two
@@ -141,7 +142,7 @@ struct AttnCfg {
 };
 
 // The part of one item that a block works on: tiles [t0, t1) of `tiles` (t1 = 0: the end).
-// The item's tiles from number `near` on lie `skip` tiles further along the sequence.
+// The item's records from number `near` on lie `skip` records further along the sequence.
 struct Seg {
   int b, h, t0, t1, tiles, len, row0, rows;
   int last;  // block that holds the item's last tile
@@ -151,17 +152,16 @@ struct Seg {
   int row;    // of the page table
 };
 
-// The tiles of an item.
+// The tiles of an item, and its records' places.
 struct Span {
   int tiles, near, skip;
 };
 
-// Place in the sequence of an item's tile t.
+// Place in the sequence of record r (0..3) of an item's tile t, in records.
 template <Mode M>
-__device__ __forceinline__ int tile_at(const Seg& s, int t) {
-  if constexpr (M == kWindow) return t + (t >= s.near ? s.skip : 0);
-  if constexpr (M == kShared) return t + s.skip;
-  return t;
+__device__ __forceinline__ int record_at(const Seg& s, int t, int r) {
+  const int i = t * (kTile / kRec) + r;
+  return M == kFull ? i : i + (i >= s.near ? s.skip : 0);
 }
 
 // What a block's work is measured in: an item's tiles, and kLead more before them
@@ -449,14 +449,18 @@ __device__ __forceinline__ Span attn_span(const AttnArgs& a, int v, int len, int
     const int last = min((rt + 1) * a.rows_per_tile, a.rows_total) - 1;
     see = len - a.N + a.by_G(last) + 1;
   }
+  constexpr int R = kTile / kRec;
   const int tiles = see <= 0 ? 0 : (see + kTile - 1) / kTile;
   if constexpr (M == kWindow) {
-    // tiles of sinks, and those from the window's first on
-    const int near = min(tiles, (a.sinks + kTile - 1) / kTile);
-    const int skip = max(0, attn_lo(a, len, rt) / kTile - near);
-    return {tiles - skip, near, skip};
+    // records of sinks, and those from the window's first on.  With whole tiles of both an item
+    // had up to two more: 48 sequences through 1,024 and 4 tokens 40.9 us against 37.0, eight
+    // trees through 2,047 and 64 39.6 against 36.7.
+    const int records = see <= 0 ? 0 : (see + kRec - 1) / kRec;
+    const int near = min(records, (a.sinks + kRec - 1) / kRec);
+    const int skip = max(0, attn_lo(a, len, rt) / kRec - near);
+    return {(records - skip + R - 1) / R, near, skip};
   }
-  if constexpr (M == kShared) return {max(tiles - extra, 0), 0, extra};
+  if constexpr (M == kShared) return {max(tiles - extra, 0), 0, extra * R};
   return {tiles, 0, 0};
 }
 
@@ -1135,8 +1139,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
         // the end, or on a page that is not there, count as 0
         uint8_t* vs = smem + C::oVS + (tile & 1) * C::VSB;
         const int ok = sh.tile_ok[1][tile & (kTiles - 1)];
-        const int end = s.len - tile_at<M>(s, t) * kTile;
-        const bool full = ok == 15 && end >= kTile;
+        const int last = s.len - record_at<M>(s, t, kTile / kRec - 1) * kRec;
+        const bool full = ok == 15 && last >= kRec;
 #pragma unroll
         for (int i = vt; i < D; i += 128) {
           const int r = i / (D / 4), go = i % (D / 4);
@@ -1144,7 +1148,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
               *reinterpret_cast<const uint2*>(raw + r * C::HALF + 16 * D + go * 8);
           uint32_t w[4] = {e4m3x2(s8.x), e4m3x2(s8.x >> 16), e4m3x2(s8.y), e4m3x2(s8.y >> 16)};
           if (!full) {
-            const int n = (ok >> r) & 1 ? end - (r * kRec + (go & 3) * 8) : 0;
+            const int end = s.len - record_at<M>(s, t, r) * kRec;
+            const int n = (ok >> r) & 1 ? end - (go & 3) * 8 : 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               w[q] = n >= 2 * q + 2 ? w[q] : n == 2 * q + 1 ? (w[q] & 0xffffu) : 0u;
@@ -1253,14 +1258,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
         const uint32_t sa = lane_base + C::cS + buf * C::NT + c0;
         // rows that see this position, where not all rows see all of the tile
         unsigned vis = ~0u;
-        const int at = tile_at<M>(e, t);
+        const int at = record_at<M>(e, t, quarter) * kRec;  // the warp's record
         if (M == kShared && e.group) {  // every row sees it
           if (!((ok >> quarter) & 1)) vis = 0;
         } else if (ok != 15 ||
-                   (a.parent != nullptr ? (at + 1) * kTile > base
-                                        : (at + 1) * kTile - 1 > base + n_lo) ||
-                   (M == kWindow && (at + 1) * kTile > a.sinks && at * kTile < hi)) {
-          const int j = at * kTile + quarter * 32 + lane, u = j - base;
+                   (a.parent != nullptr ? at + kRec > base : at + kRec - 1 > base + n_lo) ||
+                   (M == kWindow && at + kRec > a.sinks && at < hi)) {
+          const int j = at + lane, u = j - base;
           if (!((ok >> quarter) & 1) || u >= a.N) {
             // (what lies past the end was not copied, and rows past the last node would see it:
             // a NaN there raised all rows' references at every tile)
@@ -1610,14 +1614,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
                             (int64_t)s.h * (a.c.page_tokens / kRec) * rec_bytes(D);
       // this lane's position, as an entry of the table and an offset in the page, two
       // tiles ahead of the copies: the page numbers are looked up that early
-      int pos = tile_at<M>(s, s.t0) * kTile + r * kRec;
+      int pos = record_at<M>(s, s.t0, r) * kRec;
       int entry = a.by_page(pos), off = pos - entry * a.c.page_tokens;
       const int entries = a.by_page(kTile), rest = kTile - entries * a.c.page_tokens;
       int page[3], offs[3];
+      auto jumps = [&](int t) {  // from the sinks' records to the window's
+        const int i = t * (kTile / kRec) + r - s.near;
+        return M == kWindow && t > s.t0 && i >= 0 && i < kTile / kRec;
+      };
       auto look_up = [&](int i, int t) {
-        const int at = tile_at<M>(s, t) * kTile + r * kRec;
-        if (M == kWindow && t == s.near && t > s.t0)  // the window's first tile
-          entry = a.by_page(at), off = at - entry * a.c.page_tokens;
+        const int at = record_at<M>(s, t, r) * kRec;
+        if (jumps(t)) entry = a.by_page(at), off = at - entry * a.c.page_tokens;
         page[i] = lane < lanes && t < s.t1 && at < s.len ? table[entry] : -1;
         offs[i] = off;
         entry += entries;
@@ -1628,9 +1635,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
       look_up(1, s.t0 + 1);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
-        if (M == kWindow && t == s.near && t > s.t0) pos += s.skip * kTile;
+        if (jumps(t)) pos += s.skip * kRec;
         const bool past = lane >= lanes || pos >= s.len;  // the end: nothing to read
-        // (of a window's outer tiles, the records that some row sees)
+        // (of a window's records, those that some row sees)
         const bool want = !past && (M != kWindow || pos < a.sinks || pos + kRec > s.lo);
         look_up(2, t + 2);
         const bool have = want && page[0] >= 0 && page[0] < a.c.n_pages;

@@ -69,6 +69,30 @@ def test_window(gpu_lib, dtype, lens, N, Hq, H, D, P, tree, window, sinks):
     forms.check(o, lse, want, max(1, max(lens)), DT[dtype][1], D)
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("sinks", [0, 31, 32, 33, 64, 97, 128, 161])
+def test_sinks_and_window_share_tiles(gpu_lib, sinks, tree):
+    """The window's records follow the sinks' at any place of a tile; pages of 96 tokens end
+    inside it, and what lies between is not there."""
+    rng = np.random.default_rng(1000 + sinks + tree)
+    lens, N, P, window = [1000, 999, 231, 40, 683], 5, 96, 77
+    s = Setup(rng, lens, 2, 128, P)
+    cache = s.fill(rng)
+    parent = rand_trees(rng, len(lens), N) if tree else None
+    q = queries(rng, len(lens), N, 6, 128, "bf16")
+    table = s.table.copy()
+    for b, L in enumerate(lens):
+        for j in range(s.width):
+            if j * P >= sinks and (j + 1) * P <= L - N - window + 1:
+                s.table[b, j] = -1
+    o, lse = attend(gpu_lib, s, q, window, sinks, parent)
+    assert int(s.status.item()) == 0
+    want = forms.attention(cache, table, s.lens, P, q.double().cpu().numpy(), 128 ** -0.5, s.ks,
+                           s.vs, lambda b, n: forms.visible(
+                               n, N, None if parent is None else parent[b], window, sinks))
+    forms.check(o, lse, want, max(lens), DT["bf16"][1], 128)
+
+
 @pytest.mark.parametrize("N, tree", [(1, False), (40, False), (13, True)])
 def test_a_window_as_long_as_the_sequence(gpu_lib, N, tree):
     rng, t = np.random.default_rng(N), torch()
