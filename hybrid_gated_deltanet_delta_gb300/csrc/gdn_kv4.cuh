@@ -18,15 +18,18 @@ __host__ __device__ constexpr int off_v(int D) { return 16 * D; }
 __host__ __device__ constexpr int off_ks(int D) { return 32 * D; }
 __host__ __device__ constexpr int off_vs(int D) { return 34 * D; }
 
-// Length of sequence b; one out of range counts as 0 (and is reported by
-// whoever passes `report_it`).
-__device__ __forceinline__ int seq_len(const gdn_kv4_cache& c, int b, bool report_it) {
-  const int n = c.kv_len[b];
+// A length as it counts: one out of range as 0 (and is reported by whoever passes `report_it`).
+__device__ __forceinline__ int check_len(const gdn_kv4_cache& c, int n, bool report_it) {
   if (n < 0 || (int64_t)n > (int64_t)c.max_pages * c.page_tokens) {
     if (report_it) report(c.status, GDN_ERR_ROW_RANGE);
     return 0;
   }
   return n;
+}
+
+// Length of sequence b.
+__device__ __forceinline__ int seq_len(const gdn_kv4_cache& c, int b, bool report_it) {
+  return check_len(c, c.kv_len[b], report_it);
 }
 
 // The record of head h that holds position `pos` of sequence b, or NULL when
