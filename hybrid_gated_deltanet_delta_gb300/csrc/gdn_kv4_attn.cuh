@@ -58,7 +58,7 @@
 //   Where items are short, what an item costs beside its tiles: 2.5 to 3.6 us with few rows, 8 us
 // with 96 (device timer, a block's softmax: sums and the next rows' copies 1 to 2.4 us, output
 // 0.3 to 1.8, rows to binary16 1.1 to 2, first product 0.5 to 1.1, first references 0.5 to 1.3).
-// A window of 1,024 over 48 uneven sequences of 32/8 heads of 128 takes 37.0 us (2.9 items a
+// A window of 1,024 over 48 uneven sequences of 32/8 heads of 128 takes 36.9 us (2.9 items a
 // block and 21 tiles of 0.83 us), a 2048-token piece of a prompt through it 106 us (3.9 items, 34
 // tiles of 1.6 us).  32 branches of 32,768 shared tokens: 61 us, 9 of them before the first
 // product (the plan's wait, then run, segment, rows), 1.54 us a tile, 6 for the join.  Much of
@@ -1032,10 +1032,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
   const bool softmax = warp >= C::wS && warp < C::wI;
   __syncthreads();
   pdl_enter();
-  if (threadIdx.x < 2 * kHeads) {
-    const int h = threadIdx.x & (kHeads - 1);
-    const float* scales = threadIdx.x < kHeads ? a.c.k_scale : a.c.v_scale;
-    sh.scale[threadIdx.x / kHeads][h] = scales != nullptr && h < a.c.Hkv ? scales[h] : 1.f;
+  // by the last warp: the first ones wait for lengths (48 sequences through a window 37.1 us with
+  // the first warp, here 36.9; a token at 131,072 39.0 and 38.65)
+  if (threadIdx.x >= C::THREADS - 2 * kHeads) {
+    const int i = threadIdx.x - (C::THREADS - 2 * kHeads), h = i & (kHeads - 1);
+    const float* scales = i < kHeads ? a.c.k_scale : a.c.v_scale;
+    sh.scale[i / kHeads][h] = scales != nullptr && h < a.c.Hkv ? scales[h] : 1.f;
   }
   bool changed = false;
   if constexpr (M == kShared) {
