@@ -68,6 +68,7 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
   const int blocks = cluster_size(), rank = cluster_rank(), g = blockIdx.x / blocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) ref = c.B, shortest = least = 0x7fffffff;
+  __syncwarp();  // the barrier is one instruction of whole warps
   if (blocks > 1) cluster_arrive();  // waited for before the first write to another block
   pdl_enter();
   const int early = tid < c.B ? c.kv_len[tid] : 0;
