@@ -114,6 +114,13 @@ struct Elem<GDN_F16> {
   static __device__ __forceinline__ T from(float x) { return __half_as_ushort(__float2half_rn(x)); }
 };
 
+template <int DT>
+__device__ __forceinline__ float to_float(typename Elem<DT>::T x) {
+  if constexpr (DT == GDN_F32) return x;
+  if constexpr (DT == GDN_BF16) return __uint_as_float((uint32_t)x << 16);
+  if constexpr (DT == GDN_F16) return __half2float(__ushort_as_half(x));
+}
+
 // 8 consecutive elements at p (16-byte aligned) as fp32.
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, float (&x)[8]) {

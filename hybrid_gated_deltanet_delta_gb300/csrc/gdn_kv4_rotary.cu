@@ -37,7 +37,8 @@ __device__ __forceinline__ int position(const gdn_rotary& r, int b, int node, in
   return p < r.n_positions ? p : -1;
 }
 
-// Cosine and sine of a pair at a position; 1 and 0 where there is none.
+// Cosine and sine of a pair at a position; 1 and 0 where there is none (but for such a pair to
+// stay as it is takes more: 0 times an infinity is no number, and -0 + 0 is +0).
 __device__ __forceinline__ float2 angle_of(const gdn_rotary& r, int pos, int pair) {
   if (pos < 0) return make_float2(1.f, 0.f);
   const float* at = r.cos_sin + 2 * (int64_t)pos * r.pairs + pair;
@@ -122,6 +123,54 @@ struct Chunk {
   }
 };
 
+// The pairs of a block's queries where some have no position: one by one, and those left alone.
+// (Of its own, so that the usual way does without the registers.)
+template <int DT>
+static __device__ __noinline__ void turn_some_queries(const gdn_rotary& r, const Queries& q, int D,
+                                                      int b, int node0, int count, int missing,
+                                                      const float* cs) {
+  using T = typename Elem<DT>::T;
+  const T* in = static_cast<const T*>(q.in) + b * q.in_b;
+  T* out = static_cast<T*>(q.out) + b * q.out_b;
+  for (int64_t i = threadIdx.x; i < (int64_t)count * q.Hq * r.pairs; i += kThreads) {
+    const int pair = (int)(i % r.pairs), row = (int)(i / r.pairs);
+    const int token = row / q.Hq, head = row - token * q.Hq, node = node0 + token;
+    const int first = r.adjacent ? 2 * pair : pair, second = first + (r.adjacent ? 1 : r.pairs);
+    const T* from = in + node * q.in_n + (int64_t)head * D;
+    T* to = out + node * q.out_n + (int64_t)head * D;
+    if (token < missing) {
+      to[first] = to[second] = 0;
+      continue;
+    }
+    const T u = from[first], w = from[second];
+    if (position(r, b, node, r.axis != nullptr ? r.axis[pair] : 0) < 0) {
+      to[first] = u, to[second] = w;
+      continue;
+    }
+    const float x = to_float<DT>(u), y = to_float<DT>(w);
+    const float c = cs[2 * token * r.pairs + pair], s = cs[(2 * token + 1) * r.pairs + pair];
+    to[first] = Elem<DT>::from(__fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s)));
+    to[second] = Elem<DT>::from(__fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s)));
+  }
+}
+
+// Of the record's keys (turned, by this thread), the pairs without a position: as they were.
+template <int DT>
+static __device__ __noinline__ void pass_keys(const gdn_rotary& r, int lo, int hi, int node0,
+                                              const typename Elem<DT>::T* k0, int64_t ksn, int b,
+                                              float* turned) {
+  const int whole = r.pairs >> 3;
+  for (int i = threadIdx.x; i < (hi - lo) * whole; i += kThreads) {
+    const int t = i / whole, slot = lo + t, chunk = i - t * whole;
+    for (int pair = 8 * chunk; pair < 8 * chunk + 8; ++pair) {
+      if (position(r, b, node0 + slot, r.axis != nullptr ? r.axis[pair] : 0) >= 0) continue;
+      const int first = r.adjacent ? 2 * pair : pair, second = first + (r.adjacent ? 1 : r.pairs);
+      turned[slot * 2 * r.pairs + first] = to_float<DT>(k0[slot * ksn + first]);
+      turned[slot * 2 * r.pairs + second] = to_float<DT>(k0[slot * ksn + second]);
+    }
+  }
+}
+
 // Rows (token and head) that a thread visits, `step` apart.
 struct Rows {
   int token, head, by_token, by_head, Hq;
@@ -188,8 +237,9 @@ __device__ __forceinline__ void turn_queries(const gdn_kv4_cache& c, const gdn_r
         if (to[u] != nullptr) x[u].store(to[u]), y[u].store(to[u] + 8);
     }
   }
-  __syncthreads();
-  {
+  if (__syncthreads_or(bad)) {
+    turn_some_queries<DT>(r, q, D, b, node0, count, missing, cs);
+  } else {
     const int shift = lanes_for(whole), item = threadIdx.x & ((1 << shift) - 1);
     const int tokens = item < whole ? count : 0, apart = r.adjacent ? 8 : r.pairs;
     Rows at(threadIdx.x >> shift, kThreads >> shift, q.Hq);
@@ -283,7 +333,10 @@ append_rotary_kernel(const __grid_constant__ gdn_kv4_cache c, const __grid_const
     st_f4(y + apart, x[1][0], x[1][1], x[1][2], x[1][3]);
     st_f4(y + apart + 4, x[1][4], x[1][5], x[1][6], x[1][7]);
   }
-  if (off_table) report(c.status, GDN_ERR_POSITION_RANGE);
+  if (off_table) {
+    report(c.status, GDN_ERR_POSITION_RANGE);
+    pass_keys<DT>(r, at.lo, at.hi, at.t0 - at.base, k0, ksn, b, turned);
+  }
   if (at.rec == nullptr) {
     if (threadIdx.x == 0) report(c.status, GDN_ERR_PAGE_RANGE);
     return;
