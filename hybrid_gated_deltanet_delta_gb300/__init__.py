@@ -661,7 +661,8 @@ def bind_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_
     pairs = cos_sin.shape[2]
     _need(axis is None or (axis.dtype == torch.uint8 and axis.is_contiguous() and
                            tuple(axis.shape) == (pairs,)), "axis must be contiguous uint8 [pairs]")
-    _need(q_out.data_ptr() != q.data_ptr() or q_out.stride() == q.stride() or q.numel() == 0,
+    _need(q_out.data_ptr() != q.data_ptr() or q.numel() == 0 or
+          all(n == 1 or s == o for n, s, o in zip(q.shape, q.stride(), q_out.stride())),
           "q_out in q's place must have q's strides")
     _on_device(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, axis, k_scale, v_scale,
                status)

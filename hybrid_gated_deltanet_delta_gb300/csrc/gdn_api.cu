@@ -442,7 +442,9 @@ int gdn_kv4_append_rotary(const gdn_kv4_cache* c, const gdn_rotary* r, const voi
   if (q == nullptr || q_out == nullptr || k == nullptr || v == nullptr || r->cos_sin == nullptr ||
       r->positions == nullptr)
     return GDN_ERR_INVALID_ARG;
-  if (q == q_out && (q_stride_b != out_stride_b || q_stride_n != out_stride_n))
+  // in place (an axis of one has no steps)
+  if (q == q_out &&
+      ((c->B > 1 && q_stride_b != out_stride_b) || (N > 1 && q_stride_n != out_stride_n)))
     return GDN_ERR_INVALID_ARG;
   if (!gdn::aligned16(q) || !gdn::aligned16(q_out) || !gdn::aligned16(k) || !gdn::aligned16(v) ||
       !gdn::aligned16(r->cos_sin) || !ok_ptr4(r->positions))

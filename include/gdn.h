@@ -485,8 +485,8 @@ int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t
  * once to dtype, and the cache takes the keys' y unrounded.  So the stored codes and q_out are
  * fixed to the operation.
  *
- * q_out [B][N][Hq][D] is either q itself (with q's strides: the queries are turned in place, and
- * channels that pass are not touched) or overlaps none of q, k and v.  q, k, v and q_out share a
+ * q_out [B][N][Hq][D] is either q itself (with q's strides on axes longer than one: the queries
+ * are turned in place, and channels that pass are not touched) or overlaps none of q, k and v.  q, k, v and q_out share a
  * dtype (GDN_F32, GDN_BF16 or GDN_F16); strides in elements, multiples of 16 bytes.  Nodes that
  * do not exist give q_out = 0, and their positions are not looked at.  A position outside
  * [0, n_positions), or a pair's axis outside [0, n_axes), leaves the node's pairs on that axis

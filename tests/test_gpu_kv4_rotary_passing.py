@@ -90,3 +90,17 @@ def test_a_finite_key_beside_an_infinity_stays(gpu_lib):
     gpu_lib.gdn_kv4_read(s.g_pages, s.g_table, s.g_len, ko, vo, **kw)
     # (elsewhere 1 is stored as 6 * 11/64: 1/6 lies between 10/64 and 11/64, next to the latter)
     assert ko[0, 0, 0, 3] == 2688 and (ko[0, 0, 0, 16:] == 6 * 11 / 64).all()
+
+
+@pytest.mark.parametrize("B, N", [(1, 3), (3, 1), (1, 1)])
+def test_in_place_with_another_stride_of_an_axis_of_one(gpu_lib, B, N):
+    rng, t = np.random.default_rng(B + 4 * N), torch()
+    s = Setup(rng, [40, 21, 33][:B], 2, 64, 32)
+    kw = s.gpu()
+    q, k, v = (x.contiguous() for x in block(rng, B, N, 4, 2, 64, "bf16"))
+    pos, cs = rng.integers(0, 30, (1, B, N)), angles(rng, 30, 16)
+    want = t.from_numpy(forms.turned(as_float(q), pos, cs, None, False)).to(q.dtype)
+    strides = (8 if B == 1 else q.stride(0), 16 if N == 1 else q.stride(1), 64, 1)
+    gpu_lib.gdn_kv4_append_rotary(q, k, v, i32(pos), cuda(cs), s.g_pages, s.g_table, s.g_len,
+                                  q.as_strided(q.shape, strides), **kw)
+    assert int(s.status.item()) == 0 and t.equal(q.cpu(), want)
