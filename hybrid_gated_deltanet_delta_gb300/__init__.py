@@ -685,8 +685,8 @@ def gdn_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_o
     positions int32 [axes,B,N]; cos_sin float32 [n_positions,2,pairs], the cosines and sines of
     every position; axis an optional uint8 [pairs], the axis that each pair goes by (None: all by
     axis 0); adjacent=False pairs channels i and pairs + i, True 2i and 2i + 1; channels from
-    2*pairs on pass.  float32, bfloat16 or float16, any batch and node strides; the others as for
-    gdn_kv4_append (see include/gdn.h)."""
+    2*pairs on pass.  float32, bfloat16 or float16, any batch and node strides (rows of q_out must
+    not overlap); the others as for gdn_kv4_append (see include/gdn.h)."""
     bind_kv4_append_rotary(q, k, v, positions, cos_sin, pages, table, kv_len, q_out, **kw)()
 
 

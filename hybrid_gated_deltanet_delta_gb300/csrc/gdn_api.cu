@@ -4,6 +4,8 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <utility>
+
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 
@@ -194,6 +196,18 @@ int kv4_checks(const gdn_kv4_cache* c, int32_t N) {
       !ok_ptr4(c->v_scale) || !ok_ptr4(c->status))
     return GDN_ERR_MISALIGNED;
   return GDN_OK;
+}
+
+// Whether rows of `extent` elements at b*stride_b + n*stride_n (b < B, n < N) lie apart: of the
+// axes longer than one, the one of smaller steps has steps of a row at least, and the other's
+// pass all of it.
+bool rows_apart(int32_t B, int64_t stride_b, int32_t N, int64_t stride_n, int64_t extent) {
+  const auto size = [](int64_t x) { return x < 0 ? 0 - (uint64_t)x : (uint64_t)x; };
+  uint64_t step = size(stride_n), wide = size(stride_b);
+  int64_t steps = N, others = B;
+  if (steps == 1 || (others > 1 && wide < step)) std::swap(step, wide), std::swap(steps, others);
+  return steps == 1 || (step >= (uint64_t)extent &&
+                        (others == 1 || (wide - extent) / (steps - 1) >= step));
 }
 
 // Query rows of a batch, that the join of shared and own parts counts in 31 bits (a block of it
@@ -453,6 +467,8 @@ int gdn_kv4_append_rotary(const gdn_kv4_cache* c, const gdn_rotary* r, const voi
   for (int64_t stride : {q_stride_b, q_stride_n, out_stride_b, out_stride_n, k_stride_b, k_stride_n,
                          v_stride_b, v_stride_n})
     if (stride % unit != 0) return GDN_ERR_MISALIGNED;
+  if (!rows_apart(c->B, out_stride_b, N, out_stride_n, (int64_t)Hq * c->D))
+    return GDN_ERR_INVALID_ARG;
   return gdn::launch_kv4_append_rotary(*c, *r, q, q_stride_b, q_stride_n, Hq, q_out, out_stride_b,
                                        out_stride_n, k, v, dtype, k_stride_b, k_stride_n,
                                        v_stride_b, v_stride_n, N,

@@ -486,13 +486,15 @@ int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t
  * fixed to the operation.
  *
  * q_out [B][N][Hq][D] is either q itself (with q's strides on axes longer than one: the queries
- * are turned in place, and channels that pass are not touched) or overlaps none of q, k and v.  q, k, v and q_out share a
- * dtype (GDN_F32, GDN_BF16 or GDN_F16); strides in elements, multiples of 16 bytes.  Nodes that
- * do not exist give q_out = 0, and their positions are not looked at.  A position outside
- * [0, n_positions), or a pair's axis outside [0, n_axes), leaves the node's pairs on that axis
- * as they are (an infinity's or a NaN's partner and the sign of a zero too), and
- * GDN_ERR_POSITION_RANGE is reported.  A NaN or infinity in a key is treated as
- * gdn_kv4_append treats what the rotation makes of it.  Hq is a multiple of Hkv, at most 65535.
+ * are turned in place, and channels that pass are not touched) or overlaps none of q, k and v;
+ * its rows of Hq*D lie apart (the smaller of its strides is at least Hq*D, and the other passes
+ * all of those rows), else GDN_ERR_INVALID_ARG.  q, k, v and q_out share a dtype (GDN_F32,
+ * GDN_BF16 or GDN_F16); strides in elements, multiples of 16 bytes.  Nodes that do not exist give
+ * q_out = 0, and their positions are not looked at.  A position outside [0, n_positions), or a
+ * pair's axis outside [0, n_axes), leaves the node's pairs on that axis as they are (an infinity's
+ * or a NaN's partner and the sign of a zero too), and GDN_ERR_POSITION_RANGE is reported.  A NaN
+ * or infinity in a key is treated as gdn_kv4_append treats what the rotation makes of it.  Hq is a
+ * multiple of Hkv, at most 65535.
  */
 typedef struct gdn_rotary {
   const float* cos_sin;

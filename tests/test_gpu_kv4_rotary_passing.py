@@ -104,3 +104,17 @@ def test_in_place_with_another_stride_of_an_axis_of_one(gpu_lib, B, N):
     gpu_lib.gdn_kv4_append_rotary(q, k, v, i32(pos), cuda(cs), s.g_pages, s.g_table, s.g_len,
                                   q.as_strided(q.shape, strides), **kw)
     assert int(s.status.item()) == 0 and t.equal(q.cpu(), want)
+
+
+def test_nodes_outermost(gpu_lib):
+    """q_out with the sequences of a node beside each other, rows one after another."""
+    rng, t = np.random.default_rng(10), torch()
+    s = Setup(rng, [40, 21, 33], 2, 64, 32)
+    kw = s.gpu()
+    q, k, v = block(rng, 3, 5, 4, 2, 64, "f16")
+    pos, cs = rng.integers(0, 30, (1, 3, 5)), angles(rng, 30, 32)
+    want = t.from_numpy(forms.turned(as_float(q), pos, cs, None, True)).to(q.dtype)
+    out = t.empty(5, 3, 4, 64, dtype=q.dtype, device="cuda").transpose(0, 1)
+    gpu_lib.gdn_kv4_append_rotary(q, k, v, i32(pos), cuda(cs), s.g_pages, s.g_table, s.g_len, out,
+                                  adjacent=True, **kw)
+    assert int(s.status.item()) == 0 and t.equal(out.cpu(), want)

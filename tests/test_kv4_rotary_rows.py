@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import hybrid_gated_deltanet_delta_gb300 as gdn
-from test_kv4_forms_host import _tensors
+from test_kv4_forms_host import _rotary, _tensors, append_rotary
+from test_kv4_host import _cache, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("B, N, strides", [(1, 3, (64, 256, 64, 1)), (2, 1, (256, 8, 64, 1)),
@@ -26,3 +27,19 @@ def test_binding_refuses_other_strides_in_place(monkeypatch):
     a["q_out"] = a["q"].as_strided(a["q"].shape, (256, 512, 64, 1))
     with pytest.raises(ValueError, match="strides"):
         gdn.gdn_kv4_append_rotary(**a)
+
+
+@pytest.mark.parametrize("B, N, sb, sn", [
+    (2, 4, 24576, 0), (2, 4, 0, 6144),        # one row for all nodes, for all sequences
+    (2, 4, 24576, 6136), (2, 4, 6136, 24576),  # rows that end in the next
+    (2, 4, 18432, 6144),                      # a sequence's last node in the next one's first
+    (4, 2, 6144, 18432), (3, 3, 6144, 6144), (2, 4, -6144, 6144),
+    (1, 4, 0, 0), (4, 1, 8, 1 << 40),
+])
+@pytest.mark.parametrize("out", [0x100, 0x200000])   # in place, apart
+def test_rows_of_q_out_that_overlap_are_refused(lib, B, N, sb, sn, out):  # noqa: F811
+    """24 heads of 256: rows of 6,144 elements.  (Two blocks would write, or in place turn, the
+    same queries.)"""
+    c, r = _cache(B=B), _rotary()
+    assert append_rotary(lib, c, r, q=0x100, qsb=sb, qsn=sn, out=out, osb=sb, osn=sn,
+                         N=N) == gdn.GDN_ERR_INVALID_ARG
