@@ -51,7 +51,7 @@
 //
 // What bounds it.  With few rows the bytes: a tile of 36.8 KB (D = 256) takes 0.93 us a
 // block, 39.6 GB/s an SM of 43.8 measured for a copy; 131072 tokens of 4 heads take
-// 38.7 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
+// 37.9 us, 23 us of them the floor, about 5 us before the first tile and 5 us for the last
 // item's output and the join.  With 96 rows the softmax warps: 1.6 us a tile, of which 0.5
 // us is the exponentials' issue at 80 registers, the tensor pipe 0.8 us; a 2048-token piece
 // of a prompt at 8192 tokens takes 350 us, 1,030 TFLOP/s of 1,937 measured.
@@ -122,6 +122,15 @@ struct AttnCfg {
   // few they do less (131072 tokens: unrolled 37.3 us, rolled 38.4), but where items are short
   // (a window of 1,024 over 48 sequences: unrolled 41.7 us, rolled 41.1)
   static constexpr int UNROLL = NT < 64 && M_ == kFull ? 8 : 1;
+  // rows that a softmax warp has on their way in one step of its loop: with few rows all (131072
+  // tokens 38.4 us against 38.8, 200,000 50.9 against 51.1), with many, or where items are short,
+  // the loop's instructions count more than its steps
+  static constexpr int COPIES = NT < 64 && M_ == kFull ? ROWS : 1;
+  // whether heads' scales are staged in shared memory, or read where they are used.  Staged they
+  // save a wait an item (16 sequences of 20,000 tokens, D = 128: 64.9 us against 65.5), but one of
+  // 131072 tokens of D = 256, with hardly more than an item a block, takes 38.4 us against 37.9,
+  // and 16 of 20,000 50.1 against 48.8.
+  static constexpr bool STAGED = M_ != kFull || D < 256 || NT >= 64;
   static constexpr int cS = KW * KU, cO = cS + 2 * NT, cV = cO + MB * NT;
   static_assert(cV + VU * VW * 16 * MB <= 512, "TMEM");
   // shared memory
@@ -788,7 +797,7 @@ static __device__ __noinline__ void attn_rows_copy(const AttnArgs& a, int b, int
                        (int64_t)(h * a.G + row - node * a.G) * D;
   const uint16_t* src = static_cast<const uint16_t*>(a.q) + ch;
   q += (ch >> 6) * (NT * 128) + (ch & 7) * 2;
-#pragma unroll 1  // (run once an item: its instructions count more than its steps)
+#pragma unroll (AttnCfg<D, NT, M>::COPIES)
   for (int i = 0; i < ROWS; ++i) {
     const int r = r0 + i;
     uint8_t* at = q + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4);
@@ -1033,8 +1042,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
   __syncthreads();
   pdl_enter();
   // by the last warp: the first ones wait for lengths (48 sequences through a window 37.1 us with
-  // the first warp, here 36.9; a token at 131,072 39.0 and 38.65)
-  if (threadIdx.x >= C::THREADS - 2 * kHeads) {
+  // the first warp, here 36.9)
+  if (C::STAGED && threadIdx.x >= C::THREADS - 2 * kHeads) {
     const int i = threadIdx.x - (C::THREADS - 2 * kHeads), h = i & (kHeads - 1);
     const float* scales = i < kHeads ? a.c.k_scale : a.c.v_scale;
     sh.scale[i / kHeads][h] = scales != nullptr && h < a.c.Hkv ? scales[h] : 1.f;
@@ -1056,7 +1065,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
   tc::fence_before_sync();
   const bool again = __syncthreads_or(changed) || (M != kShared && !kept);
   auto head_scale = [&](int kind, const float* scales, int h) {
-    return h < kHeads ? sh.scale[kind][h] : scales != nullptr ? scales[h] : 1.f;
+    return C::STAGED && h < kHeads ? sh.scale[kind][h] : scales != nullptr ? scales[h] : 1.f;
   };
   tc::fence_after_sync();
   // all 512 columns are this block's, so its tensor memory begins at address 0, and
@@ -1216,10 +1225,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
       if (no > 0 || again) attn_wait(&sh.seg_full[no & (kSegs - 1)], (no / kSegs) & 1, dead);
       return sh.seg[no & (kSegs - 1)].t1 > 0 && !__any_sync(0xffffffffu, *dead);
     };
+    float k_scale = 1.f;  // of the rows fetched last, where scales are not staged
     auto fetch_rows = [&](const Seg& n) {
+      if (!C::STAGED) k_scale = head_scale(0, a.c.k_scale, n.h);
       attn_rows_copy<D, NT, M>(args, n.b, n.h, n.row0, n.rows, n.group, smem + C::oQ,
                                warp - C::wS);
     };
+    if (!C::STAGED && kept && !again) k_scale = head_scale(0, a.c.k_scale, sh.seg[0].h);
     bool more = find_seg(0);
     if (again || M == kShared) {
       cp_async_wait_all();  // of the early copy, to the same place
@@ -1232,7 +1244,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT, M>::THREADS, 1) attn_kernel(con
       const float c_all =
           attn_rows<D, NT, M>(args, sh, e.b, e.len, e.row0, e.rows, e.group, smem + C::oQ,
                               warp - C::wS,
-                              a.scale * (head_scale(0, a.c.k_scale, e.h) * kLog2e));
+                              a.scale * ((C::STAGED ? head_scale(0, a.c.k_scale, e.h) : k_scale) *
+                                         kLog2e));
       tc::named_barrier(4, 128 * C::NS);
       if (threadIdx.x == 32 * C::wS) mbar_arrive(&sh.q_full);
       if (gt < C::NH) sh.neg_m[c0 + gt] = -kNone;
