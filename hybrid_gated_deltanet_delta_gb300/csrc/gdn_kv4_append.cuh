@@ -67,19 +67,8 @@ __device__ __forceinline__ uint2 pair_bytes(uint32_t a, uint32_t b) {
 struct Place {
   uint8_t* rec;  // NULL: the page is not there
   int base, t0;  // positions of node 0 and of the record's first token
-  int lo, hi;    // the record's tokens that are the block's; none where it touches fewer records
+  int lo, hi;    // the record's tokens that are the block's
 };
-
-__device__ __forceinline__ Place find_place(const gdn_kv4_cache& c, int N, int b, int h, int part) {
-  Place p = {};
-  const int len = seq_len(c, b, part == 0 && h == 0 && threadIdx.x == 0);
-  p.base = len - N;
-  p.t0 = ((p.base > 0 ? p.base : 0) / kRec + part) * kRec;
-  if (p.t0 >= len) return p;
-  p.lo = p.base > p.t0 ? p.base - p.t0 : 0, p.hi = len - p.t0 < kRec ? len - p.t0 : kRec;
-  p.rec = record(c, b, h, p.t0);
-  return p;
-}
 
 // Quantises channels 16*g .. of a pair of tokens; `load(slot, x)` brings in one token's.  K goes
 // to the record, V's codes to `code`.
@@ -116,39 +105,6 @@ __device__ __forceinline__ void quantise_pair(const Place& p, bool is_v, float i
     const uint2 first = pair_bytes(q[0].w[0], q[1].w[0]), second = pair_bytes(q[0].w[1], q[1].w[1]);
     *reinterpret_cast<uint4*>(&code[pair][g * 16]) =
         make_uint4(first.x, first.y, second.x, second.y);
-  }
-}
-
-// What a channel's 16 bytes of V codes hold, where the block covers only part of them.
-template <int D>
-__device__ __forceinline__ uint4 old_v(const Place& p, int ch) {
-  return p.lo != 0 || p.hi != kRec ? *reinterpret_cast<const uint4*>(p.rec + off_v(D) + ch * 16)
-                                   : make_uint4(0, 0, 0, 0);
-}
-
-// V's codes to the record, after a barrier; `old(ch)`: what is there.
-template <int D, typename Old>
-__device__ __forceinline__ void store_v(const Place& p, const uint8_t (*code)[D], Old old_of) {
-  // nibbles of the block in each word of 8 tokens
-  uint32_t mine[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int from = min(max(p.lo - 8 * w, 0), 8), to = min(max(p.hi - 8 * w, 0), 8);
-    mine[w] = (uint32_t)(((1ull << (4 * to)) - 1) & ~((1ull << (4 * from)) - 1));
-  }
-  for (int ch = threadIdx.x; ch < D; ch += kThreads) {
-    uint4* at = reinterpret_cast<uint4*>(p.rec + off_v(D) + ch * 16);
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = (code[4 * k][ch] | (uint32_t)code[4 * k + 1][ch] << 8 |
-              (uint32_t)code[4 * k + 2][ch] << 16 | (uint32_t)code[4 * k + 3][ch] << 24) & mine[k];
-    if (p.lo != 0 || p.hi != kRec) {
-      const uint4 old = old_of(ch);
-      w[0] |= old.x & ~mine[0], w[1] |= old.y & ~mine[1];
-      w[2] |= old.z & ~mine[2], w[3] |= old.w & ~mine[3];
-    }
-    *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

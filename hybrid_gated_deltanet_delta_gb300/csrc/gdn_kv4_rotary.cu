@@ -30,6 +30,18 @@ using namespace kv4;
 
 constexpr int kTurnTokens = kRec;  // tokens whose angles fit in shared memory
 
+// The `part`-th record that the block of N tokens of sequence b touches, of head h.
+__device__ __forceinline__ Place find_place(const gdn_kv4_cache& c, int N, int b, int h, int part) {
+  Place p = {};
+  const int len = seq_len(c, b, part == 0 && h == 0 && threadIdx.x == 0);
+  p.base = len - N;
+  p.t0 = ((p.base > 0 ? p.base : 0) / kRec + part) * kRec;
+  if (p.t0 >= len) return p;
+  p.lo = p.base > p.t0 ? p.base - p.t0 : 0, p.hi = len - p.t0 < kRec ? len - p.t0 : kRec;
+  p.rec = record(c, b, h, p.t0);
+  return p;
+}
+
 // Position of a node on an axis, -1 where the table or the axes have none.
 __device__ __forceinline__ int position(const gdn_rotary& r, int b, int node, int axis) {
   if (axis >= r.n_axes) return -1;
@@ -283,6 +295,39 @@ __device__ __forceinline__ void turn_queries(const gdn_kv4_cache& c, const gdn_r
   }
 }
 
+// What a channel's 16 bytes of V codes hold, where the block covers only part of them.
+template <int D>
+__device__ __forceinline__ uint4 old_v(const Place& p, int ch) {
+  return p.lo != 0 || p.hi != kRec ? *reinterpret_cast<const uint4*>(p.rec + off_v(D) + ch * 16)
+                                   : make_uint4(0, 0, 0, 0);
+}
+
+// V's codes to the record, after a barrier; `old`: what is there, of the thread's channel.
+template <int D>
+__device__ __forceinline__ void store_v(const Place& p, const uint8_t (*code)[D], uint4 old) {
+  static_assert(D <= kThreads, "a channel of V a thread");
+  // nibbles of the block in each word of 8 tokens
+  uint32_t mine[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int from = min(max(p.lo - 8 * w, 0), 8), to = min(max(p.hi - 8 * w, 0), 8);
+    mine[w] = (uint32_t)(((1ull << (4 * to)) - 1) & ~((1ull << (4 * from)) - 1));
+  }
+  for (int ch = threadIdx.x; ch < D; ch += kThreads) {
+    uint4* at = reinterpret_cast<uint4*>(p.rec + off_v(D) + ch * 16);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = (code[4 * k][ch] | (uint32_t)code[4 * k + 1][ch] << 8 |
+              (uint32_t)code[4 * k + 2][ch] << 16 | (uint32_t)code[4 * k + 3][ch] << 24) & mine[k];
+    if (p.lo != 0 || p.hi != kRec) {
+      w[0] |= old.x & ~mine[0], w[1] |= old.y & ~mine[1];
+      w[2] |= old.z & ~mine[2], w[3] |= old.w & ~mine[3];
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // BLOCKS an SM: registers against blocks in flight.  With 3 one token takes 6.2 us and 128 of
 // eight sequences 8.5 (with reading back), a prompt of 8,192 68.3; with 4 6.5, 9.0 and 66.0.
 template <int DT, int D, int BLOCKS>
@@ -341,7 +386,6 @@ append_rotary_kernel(const __grid_constant__ gdn_kv4_cache c, const __grid_const
     if (threadIdx.x == 0) report(c.status, GDN_ERR_PAGE_RANGE);
     return;
   }
-  static_assert(D <= kThreads, "a channel of V a thread");
   const uint4 old = threadIdx.x < D ? old_v<D>(at, threadIdx.x) : make_uint4(0, 0, 0, 0);
   const float inv_k = c.k_scale != nullptr ? 1.0f / c.k_scale[h] : 1.0f;
   const float inv_v = c.v_scale != nullptr ? 1.0f / c.v_scale[h] : 1.0f;
@@ -372,7 +416,7 @@ append_rotary_kernel(const __grid_constant__ gdn_kv4_cache c, const __grid_const
                      });
   }
   __syncthreads();
-  store_v<D>(at, code, [&](int) { return old; });
+  store_v<D>(at, code, old);
   if (bad) report(c.status, GDN_ERR_NONFINITE);
 }
 
