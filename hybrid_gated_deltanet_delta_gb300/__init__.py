@@ -763,10 +763,10 @@ def bind_kv4_attention_window(q, pages, table, kv_len, o, workspace, *, scale, w
     lead, trail, keep = _kv4_attention(q, pages, table, kv_len, o, workspace, scale, parent, lse,
                                        k_scale, v_scale, status)
     _on_device(*keep[1:])
-    most = 2 ** 31 - 1  # longer than any sequence
+    # ctypes keeps the low 32 bits: longer than any sequence, and below what is refused
+    sinks, window = (max(-1, min(x, 2 ** 31 - 1)) for x in (sinks, window))
     return BoundCall(load().gdn_kv4_attention_window, "gdn_kv4_attention_window",
-                     (*lead, min(sinks, most), min(window, most), _ptr(parent), *trail,
-                      _stream(stream)), keep)
+                     (*lead, sinks, window, _ptr(parent), *trail, _stream(stream)), keep)
 
 
 def gdn_kv4_attention_window(q, pages, table, kv_len, o, workspace, **kw):
