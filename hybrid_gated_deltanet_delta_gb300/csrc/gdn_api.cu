@@ -452,6 +452,7 @@ int gdn_kv4_append_rotary(const gdn_kv4_cache* c, const gdn_rotary* r, const voi
   if (r->pairs < 1 || r->n_positions < 1 || r->n_axes < 1) return GDN_ERR_INVALID_ARG;
   if (r->adjacent != 0 && r->adjacent != 1) return GDN_ERR_INVALID_ARG;
   if (r->pairs % 8 != 0 || r->pairs > c->D / 2 || Hq > 65535) return GDN_ERR_UNSUPPORTED;
+  if (c->Hkv > 65535 - gdn::kRotaryQueryRows) return GDN_ERR_UNSUPPORTED;
   if (c->B == 0) return GDN_OK;
   if (q == nullptr || q_out == nullptr || k == nullptr || v == nullptr || r->cos_sin == nullptr ||
       r->positions == nullptr)

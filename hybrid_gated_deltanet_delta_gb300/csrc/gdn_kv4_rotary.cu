@@ -454,7 +454,6 @@ int launch_kv4_append_rotary(const gdn_kv4_cache& c, const gdn_rotary& r, const 
   if (tokens > kTurnTokens) tokens = kTurnTokens;
   while (tokens > 1 && (int64_t)c.B * ((N + tokens - 1) / tokens) < 2 * sms) tokens /= 2;
   const int64_t blocks = (N + tokens - 1) / tokens, rows = c.Hkv + (blocks + records - 1) / records;
-  if (rows > 65535) return GDN_ERR_UNSUPPORTED;
   const dim3 grid(records, (unsigned)rows, c.B);
   const Queries qs = {q, q_out, qsb, qsn, osb, osn, Hq, tokens};
   // blocks of one wave have an SM to three of them at most

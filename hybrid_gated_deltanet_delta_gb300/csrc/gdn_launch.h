@@ -62,6 +62,9 @@ size_t kv4_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 int launch_kv4_attention(const gdn_kv4_cache& c, const void* q, int dtype, int64_t qsb,
                          int64_t qsn, int N, int Hq, float scale, const int32_t* parent, void* o,
                          float* lse, void* workspace, cudaStream_t s);
+// Rows of its grid beside the kv heads: N blocks of queries at most, in rows as long as the
+// records that N tokens touch.
+constexpr int kRotaryQueryRows = 32;
 int launch_kv4_append_rotary(const gdn_kv4_cache& c, const gdn_rotary& r, const void* q, int64_t qsb,
                              int64_t qsn, int Hq, void* q_out, int64_t osb, int64_t osn,
                              const void* k, const void* v, int dtype, int64_t ksb, int64_t ksn,

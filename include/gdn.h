@@ -494,7 +494,7 @@ int gdn_kv4_append(const gdn_kv4_cache* c, const void* k, const void* v, int32_t
  * pair's axis outside [0, n_axes), leaves the node's pairs on that axis as they are (an infinity's
  * or a NaN's partner and the sign of a zero too), and GDN_ERR_POSITION_RANGE is reported.  A NaN
  * or infinity in a key is treated as gdn_kv4_append treats what the rotation makes of it.  Hq is a
- * multiple of Hkv, at most 65535.
+ * multiple of Hkv, at most 65535, and Hkv at most 65503.
  */
 typedef struct gdn_rotary {
   const float* cos_sin;

@@ -43,3 +43,18 @@ def test_rows_of_q_out_that_overlap_are_refused(lib, B, N, sb, sn, out):  # noqa
     c, r = _cache(B=B), _rotary()
     assert append_rotary(lib, c, r, q=0x100, qsb=sb, qsn=sn, out=out, osb=sb, osn=sn,
                          N=N) == gdn.GDN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("Hkv, want", [(65504, gdn.GDN_ERR_UNSUPPORTED), (65536, gdn.GDN_ERR_UNSUPPORTED)])
+def test_kv_heads_beside_the_blocks_of_queries(lib, Hkv, want):  # noqa: F811
+    """Both stand on one axis of the grid, which has 65,535 places: refused before anything else is
+    looked at (the missing queries are a later refusal)."""
+    c = _cache(D=64, Hkv=Hkv, page_stride=Hkv * 2 * 36 * 64)
+    assert append_rotary(lib, c, _rotary(), q=0, Hq=Hkv, N=1) == want
+
+
+def test_most_kv_heads(lib):  # noqa: F811
+    c = _cache(D=64, Hkv=65503, page_stride=65503 * 2 * 36 * 64)
+    assert append_rotary(lib, c, _rotary(), q=0, Hq=65503, N=1) == gdn.GDN_ERR_INVALID_ARG
+    # rows of blocks of queries beside them: (blocks of one token) / (records that N tokens touch)
+    assert max(-(-N // ((N + 30) // 32 + 1)) for N in range(1, 1 << 16)) <= 32
