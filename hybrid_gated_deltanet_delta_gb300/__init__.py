@@ -797,7 +797,9 @@ def gdn_kv4_attention_shared(q, pages, table, kv_len, group, o, workspace, **kw)
     the part that the sequences of a group have in common is read once for all of them.
 
     group int32 [n_groups + 1]: group g is sequences group[g] .. group[g+1] - 1 of the batch; how
-    much they share follows from the table.  workspace a uint8 tensor of
+    much they share follows from the table.  Whether sharing can pay is decided by the table's
+    width: of a wide one, table[:, :k] with the columns that the lengths need is faster where they
+    are short.  workspace a uint8 tensor of
     gdn_kv4_attention_shared_workspace_bytes(...) bytes; the others as for gdn_kv4_attention."""
     bind_kv4_attention_shared(q, pages, table, kv_len, group, o, workspace, **kw)()
 

@@ -143,14 +143,18 @@ bool rows_worth_sharing(int N, int G) {
 // And whether it does by the most that there can be to read: plan, longer prologue and join
 // cost some 12 us, and the more rows a sequence has the less there is to win.  Measured (shared /
 // each sequence for itself, us; W: tiles of 128, and six more an item, of all items at the
-// table's width):
-//   rows of a kv head      W too small                       W large enough
-//    4, D 128    2,176: 26 / 20   4,352: 31 / 31     5,248: 27 / 35   17,536: 34 / 92
-//    6, D 256    2,176: 31 / 27   2,624: 29 / 32     5,248: 34 / 48   35,072: 77 / 223
-//   24, D 256    2,624: 38 / 36   4,352: 49 / 53    10,496: 70 / 102  35,072: 135 / 275
-//   32, D 128    5,248: 49 / 44  10,496: 72 / 74    20,992: 112 / 134 70,144: 278 / 419
-//   48, D 256    5,248: 63 / 61   8,768: 78 / 89    17,536: 129 / 164 35,072: 230 / 309
-//   66, D 256    5,248: 74 / 75   8,768: 98 / 111   17,536: 165 / 199 35,072: 326 / 379
+// table's width; shared from the bound on; rows of a kv head):
+//   rows, D  bound   below it                        above it
+//    4, 128  4,594   2,176: 26 / 20, 4,352: 31 / 31  5,248: 27 / 35, 17,536: 34 / 92
+//    6, 256  2,469   2,176: 31 / 27                  2,624: 29 / 32, 5,248: 34 / 48
+//   24, 256  4,016   2,624: 38 / 36                  4,352: 49 / 53, 10,496: 70 / 102
+//   32, 128  9,407   5,248: 49 / 44                  10,496: 72 / 74, 20,992: 112 / 134
+//   48, 256  6,079   5,248: 63 / 61                  8,768: 78 / 89, 17,536: 129 / 164
+//   66, 256  7,625   5,248: 74 / 75                  8,768: 98 / 111, 17,536: 165 / 199
+// The lengths are the device's, so short sequences in a wide table are shared as well: four of
+// 700 tokens (6 rows, D 256) take 13.0 us in a table of 16,384 tokens, each for itself, and 17.6
+// in one of 32,768 or a million, shared.  (A caller who knows a bound of the lengths gives it as
+// max_pages.)
 bool worth_sharing(const gdn_kv4_cache& c, int rows, int row_tiles, int n_groups) {
   const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + 127) / 128 + 6;
   const int64_t most = (int64_t)c.B * c.Hkv * row_tiles * tiles;

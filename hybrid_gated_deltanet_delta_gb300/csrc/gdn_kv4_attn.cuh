@@ -120,7 +120,7 @@ struct AttnCfg {
   // of the K and V warps' units: with many rows all roles' loops together strain the
   // instruction cache (a 2048-token piece of a prompt: unrolled 377 us, rolled 365), with
   // few they do less (131072 tokens: unrolled 37.3 us, rolled 38.4), but where items are short
-  // (a window of 1,024 over 48 sequences: unrolled 41.7 us, rolled 41.1)
+  // (a window of 1,024 over 48 sequences: unrolled 38.9 us, rolled 36.7)
   static constexpr int UNROLL = NT < 64 && M_ == kFull ? 8 : 1;
   // rows that a softmax warp has on their way in one step of its loop: with few rows all (131072
   // tokens 38.4 us against 38.8, 200,000 50.9 against 51.1), with many, or where items are short,
@@ -186,6 +186,9 @@ constexpr int kLead = 6;
 // goes with an item kSharedLead and kSharedMore for each of them.  Measured (32 branches of
 // 32,768 tokens / 8 x 8 draft chains / 2 x 8 draft trees, us): a lead of 16 82.5 / 114.8 / 170,
 // 30 + 6 a group 69.6 / 97.8 / 108.1, 40 + 6 67.1 / 94.3 / 109.3, 50 + 10 70.0 / 94.6 / 111.
+// On the present kernels, with 56 branches of 4,096 tokens last: 24 + 6 61.9 / 96.1 / 108.9 /
+// 41.6, 30 + 6 60.8 / 89.7 / 104.0 / 42.6, 40 + 2 60.8 / 92.3 / 105.7 / 44.5, 40 + 6 60.5 / 88.9 /
+// 104.5 / 43.9, 40 + 12 62.0 / 86.4 / 105.5 / 45.9, 50 + 6 62.0 / 89.0 / 104.7 / 46.2.
 constexpr int kSharedLead = 40, kSharedMore = 6, kMostWeight = 10;
 template <int NT>
 __device__ __forceinline__ int row_groups(int rows) {
@@ -1836,7 +1839,9 @@ int attn_launch_nt(const AttnArgs& a, int parts, cudaStream_t s) {
   const dim3 grid(parts, (a.rows_per_tile + NP - 1) / NP);
   // Few parts an item: two in flight, and more threads.  A 2048-token piece of a prompt through
   // a window of 1,024 (512 items) takes 106.4 us with two and 110.3 with eight, a tree of 22
-  // nodes at 32,768 tokens (8 items of 19 parts) 43.6 and 41.8.
+  // nodes at 32,768 tokens (8 items of 19 parts) 43.6 and 41.8; chains of 16 at about 14,000 tokens
+  // (96 rows, D = 256) 32.4 and 28.1 with 4 items, 36.7 and 36.4 with 12, 40.2 and 40.6 with 16,
+  // 45.3 and 46.4 with 20 (the bound is 19), 60.6 and 61.7 with 32.
   if ((int64_t)a.c.B * a.c.Hkv * a.row_tiles * 8 >= parts)
     return launch_pdl(join_kernel<D, false, 2>, grid, block, 0, s, a, NT);
   return launch_pdl(join_kernel<D, false, 8>, grid, block, 0, s, a, NT);

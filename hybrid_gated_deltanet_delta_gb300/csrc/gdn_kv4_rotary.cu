@@ -11,13 +11,14 @@
 // sines, which all heads use, are gathered in shared memory.
 //
 // Bound by the bytes where tokens are many: 8,192 tokens of 24 and 4 heads of 256 channels, 32
-// pairs, bf16, move 243 MB (36 us at the rate of a copy) in 50 us: the queries alone take 36 us,
-// keys and values alone 19.  Measured on the way there (with 15 us of reading back): angles
+// pairs, bf16, move 243 MB (36 us at the rate of a copy) in 49.5 us: the queries alone take 36 us,
+// keys and values alone 19.  In place (95 MB, 14 us) 29.7; f32 (481 MB, 71 us) 86.6, in place (179
+// MB, 26 us) 38.1.  Measured on the way there (with 15 us of reading back): angles
 // staged for keys too, each item with two divisions 91 us; the queries' loads before the angles
 // 77; items of a thread in one place of every row, channels that pass moved without conversion,
 // keys turned before they are quantised 70; 2,048 items a block instead of 1,024 64 (512: 94 in
 // the version before, 4,096: 68).  A few tokens are bound by the latency of the length, the
-// page, axis, position and angle, one after another: one token 3.1 us.
+// page, axis, position and angle, one after another: one token 3.8 us.
 #include "gdn_common.cuh"
 #include "gdn_kv4.cuh"
 #include "gdn_kv4_append.cuh"

@@ -194,7 +194,10 @@ plan_kernel(gdn_kv4_cache c, int N, const int32_t* __restrict__ parent,
 // ones, in block order, and then the shared ones.  Bound by latency: the numbers of the plan and of
 // the row, then the parts; 6 us after the pass for 8,192 rows of 128 channels.  With eight parts
 // in flight 9.5 us, with two 6; one row a block up to 8 rows an SM (32 branches: 62.0 us in all,
-// up to 2 rows 66.6; 8 x 8 chains, always one row a block, 115.7 against 92.8).
+// up to 2 rows 66.6; 8 x 8 chains, always one row a block, 115.7 against 92.8; branches of 4,096
+// tokens, 24/4 heads of 256, one row a block / several: 16 of them 27.6 / 32.2, 32 33.3 / 35.3, 44
+// 38.4 / 39.2, 56 (past the bound of 1,216 rows) 44.1 / 44.1, 64 46.9 / 46.3, 96 59.0 / 56.6; 32/8 of
+// 128: 38 42.4 / 43.0, 44 44.7 / 44.4).
 constexpr int kJoinThreads = 256;
 
 template <int D, bool ONE_ROW>
@@ -308,8 +311,16 @@ int join_d(const AttnArgs& a, int NT, int blocks, cudaStream_t s) {
 int launch_kv4_shared_plan(const gdn_kv4_cache& c, int N, const int32_t* parent,
                            const int32_t* group, int n_groups, const SharedPlan& plan,
                            cudaStream_t s) {
-  // several blocks where the usual group has many sequences: 32 of 520 pages take 8 us less in
-  // eight, eight of 133 2 us more
+  // Several blocks where the usual group has many sequences.  One block / eight, us of the whole
+  // call, pages of 64 tokens (24/4 heads of 256):
+  //   members    32 pages      128 pages     512 pages     2,048 pages
+  //     8       21.8 / 22.1   25.9 / 26.7   37.1 / 36.7    73.0 / 65.6
+  //     9       22.0 / 22.5   26.1 / 27.1   39.8 / 36.8    84.3 / 66.3
+  //    16       25.7 / 26.0   31.8 / 32.2   47.0 / 43.9    98.6 / 80.9
+  //    24       30.0 / 28.8   38.4 / 36.1   63.2 / 55.5
+  //    48       41.3 / 38.4   53.3 / 48.0   92.8 / 76.6
+  // (the host does not know the lengths: a bound of 8 members loses up to 1 us with few pages and
+  // wins up to 18 with many).
   const int blocks = c.B > 8 * (int64_t)n_groups ? kPlanBlocks : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_groups * blocks);

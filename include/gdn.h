@@ -591,7 +591,8 @@ int gdn_kv4_attention_window(const gdn_kv4_cache* c, const void* q, int32_t dtyp
  * sizes (the rows of a sequence fill the tensor cores' tiles by themselves, the table's width
  * leaves little to read, there are as many groups as sequences, or the work counted in tenths of
  * tiles would not fit 31 bits) every sequence is read for itself, and the offsets are not looked
- * at.
+ * at.  The sizes are what the host is given: where the lengths are short for the table's width
+ * (max_pages * page_tokens), gdn_kv4_attention, or a max_pages that the lengths need, is faster.
  *
  * The result is gdn_kv4_attention's up to the order of the sums, which depends on the lengths,
  * the table, the groups and the device alone.  The workspace

@@ -190,3 +190,21 @@ def test_more_sequences_than_a_block_keeps(gpu_lib, group_of, alone):
     s.lens[3], s.lens[group_of - 1] = -1, 50
     status, prefix = s.check(gpu_lib)
     assert status == gpu_lib.GDN_ERR_ROW_RANGE and prefix == [1] + [0] * alone
+
+
+def test_the_columns_that_the_lengths_need(gpu_lib):
+    """A wide table's first columns, rows as far apart as before: short sequences are then read
+    each for itself, with the full attention's bits."""
+    t = torch()
+    rng = np.random.default_rng(5)
+    s = Batch(rng, [(4, 10)], [700, 650, 641, 690], 64)
+    q = t.randn((4, 1, 6, 64), generator=t.Generator("cuda").manual_seed(1), device="cuda").half()
+    ws = t.empty(gpu_lib.gdn_kv4_attention_shared_workspace_bytes(4, 1, 6, 1, 64, 1),
+                 dtype=t.uint8, device="cuda")
+    pages, table, lens, status = cuda(s.pages), i32(s.table), i32(s.lens), status_word()
+    o, want = t.empty_like(q), t.empty_like(q)
+    assert table[:, :11].stride(0) == table.shape[1] > 11
+    kw = dict(scale=0.125, status=status)
+    gpu_lib.gdn_kv4_attention_shared(q, pages, table[:, :11], lens, i32([0, 4]), o, ws, **kw)
+    gpu_lib.gdn_kv4_attention(q, pages, table, lens, want, ws, **kw)
+    assert int(status.item()) == 0 and t.equal(o, want)
